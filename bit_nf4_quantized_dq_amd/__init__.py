@@ -1,7 +1,8 @@
 """MI355X (gfx950) NF4 + double-quantized frozen linear with a 16-bit LoRA side path.
 
-The compute runs in the HIP library ``libqlora_nf4.so`` (C ABI in ``include/qlora.h``);
-this package only marshals arguments.  ``lib`` raises if the library is missing -- there is
+The compute runs in the HIP library ``libqlora_nf4.so`` (C ABI in ``include/qlora.h``
+and, for the operators of a training step beside the linears, ``include/qlora_train.h``); this
+package only marshals arguments.  ``lib`` raises if the library is missing -- there is
 no CPU fallback.
 """
 
@@ -38,4 +39,17 @@ from ._binding import (  # noqa: F401
     OP_QUANTIZE,
     OP_FWD,
     OP_BWD,
+)
+from ._training import (  # noqa: F401
+    GradList,
+    adamw_step_clipped,
+    grad_clip,
+    grad_norm,
+    logps_workspace_size,
+    norm_residual_bwd,
+    norm_residual_fwd,
+    norm_residual_workspace_size,
+    preference_loss,
+    preference_workspace_size,
+    token_logps,
 )

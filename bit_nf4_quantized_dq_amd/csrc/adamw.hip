@@ -13,8 +13,13 @@
 // The kernel is a pure stream: 14 bytes read and 14 written per parameter (28 B), so it is
 // bound by HBM.  Each lane takes 4 consecutive parameters (16-byte state loads, 8-byte
 // gradient loads and parameter stores); a tail of n % 4 parameters runs element by element.
-#include "qlora_device.h"
-#include "qlora_host.h"
+//
+// With clipping (kClip) each gradient is multiplied by min(1, max_norm / (norm + 1e-6)) as it
+// is read, in FP32 and without a rounding to BF16: the clipped gradients are never written, so
+// the step still moves 28 B per parameter.  A norm that is not finite leaves every state as it
+// is.
+#include "qlora_train_host.h"
+#include "train_device.h"
 
 namespace qlora {
 namespace {
@@ -29,9 +34,21 @@ __device__ __forceinline__ void adamw1(float& th, float& m, float& v, float g, c
   th = __fsub_rn(th, __fdiv_rn(__fmul_rn(a.step_size, m), den));
 }
 
+template <bool kClip>
+__device__ __forceinline__ float clipped(float g, float c) {
+  return kClip ? __fmul_rn(g, c) : g;
+}
+
+template <bool kClip>
 __global__ __launch_bounds__(kThreads) void k_adamw(float* __restrict__ master, float* __restrict__ mom1,
                                                     float* __restrict__ mom2, const uint16_t* __restrict__ grad,
-                                                    uint16_t* __restrict__ param, int64_t n, AdamWScalars a) {
+                                                    uint16_t* __restrict__ param, int64_t n, AdamWScalars a,
+                                                    const float* __restrict__ norm, float max_norm) {
+  float c = 1.f;
+  if (kClip) {
+    if (!(fabsf(*norm) < INFINITY)) return;
+    c = clip_coefficient(*norm, max_norm);
+  }
   const int64_t n4 = n >> 2;
   const int64_t stride = (int64_t)gridDim.x * kThreads;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n4; i += stride) {
@@ -39,10 +56,10 @@ __global__ __launch_bounds__(kThreads) void k_adamw(float* __restrict__ master, 
     float4 m = reinterpret_cast<const float4*>(mom1)[i];
     float4 v = reinterpret_cast<const float4*>(mom2)[i];
     const uint2 gb = reinterpret_cast<const uint2*>(grad)[i];
-    adamw1(th.x, m.x, v.x, bf16lo_to_f32(gb.x), a);
-    adamw1(th.y, m.y, v.y, bf16hi_to_f32(gb.x), a);
-    adamw1(th.z, m.z, v.z, bf16lo_to_f32(gb.y), a);
-    adamw1(th.w, m.w, v.w, bf16hi_to_f32(gb.y), a);
+    adamw1(th.x, m.x, v.x, clipped<kClip>(bf16lo_to_f32(gb.x), c), a);
+    adamw1(th.y, m.y, v.y, clipped<kClip>(bf16hi_to_f32(gb.x), c), a);
+    adamw1(th.z, m.z, v.z, clipped<kClip>(bf16lo_to_f32(gb.y), c), a);
+    adamw1(th.w, m.w, v.w, clipped<kClip>(bf16hi_to_f32(gb.y), c), a);
     reinterpret_cast<float4*>(master)[i] = th;
     reinterpret_cast<float4*>(mom1)[i] = m;
     reinterpret_cast<float4*>(mom2)[i] = v;
@@ -52,7 +69,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(float* __restrict__ master, 
   if (blockIdx.x == 0 && threadIdx.x < (n & 3)) {
     const int64_t j = 4 * n4 + threadIdx.x;
     float th = master[j], m = mom1[j], v = mom2[j];
-    adamw1(th, m, v, __uint_as_float((uint32_t)grad[j] << 16), a);
+    adamw1(th, m, v, clipped<kClip>(__uint_as_float((uint32_t)grad[j] << 16), c), a);
     master[j] = th;
     mom1[j] = m;
     mom2[j] = v;
@@ -60,15 +77,26 @@ __global__ __launch_bounds__(kThreads) void k_adamw(float* __restrict__ master, 
   }
 }
 
+unsigned grid_for(int64_t n) {
+  const int64_t want = ((n >> 2) + kThreads - 1) / kThreads;
+  return (unsigned)(want < 1 ? 1 : (want > 65536 ? 65536 : want));
+}
+
 }  // namespace
 
 hipError_t launch_adamw(float* master, float* m, float* v, const uint16_t* grad, uint16_t* param, int64_t n,
                         const AdamWScalars& a, hipStream_t s) {
-  const int64_t n4 = n >> 2;
-  const int64_t want = (n4 + kThreads - 1) / kThreads;
-  const unsigned grid = (unsigned)(want < 1 ? 1 : (want > 65536 ? 65536 : want));
   LaunchTimer t(10, s);
-  hipExtLaunchKernelGGL(k_adamw, dim3(grid), dim3(kThreads), 0, s, t.start, t.stop, 0, master, m, v, grad, param, n, a);
+  hipExtLaunchKernelGGL(k_adamw<false>, dim3(grid_for(n)), dim3(kThreads), 0, s, t.start, t.stop, 0, master, m, v, grad,
+                        param, n, a, (const float*)nullptr, 0.f);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw_clipped(float* master, float* m, float* v, const uint16_t* grad, uint16_t* param, int64_t n,
+                                const AdamWScalars& a, const float* norm, float max_norm, hipStream_t s) {
+  LaunchTimer t(10, s);
+  hipExtLaunchKernelGGL(k_adamw<true>, dim3(grid_for(n)), dim3(kThreads), 0, s, t.start, t.stop, 0, master, m, v, grad,
+                        param, n, a, norm, max_norm);
   return hipGetLastError();
 }
 

@@ -1,0 +1,147 @@
+// Global norm of a list of gradient tensors, and clipping:
+//   norm = sqrt(sum over all tensors of sum g^2),   c = min(1, max_norm / (norm + 1e-6)),
+//   out = c g.
+// The list is a table in device memory with one entry per 16384 elements of a tensor, so one
+// launch covers any number of tensors and no workgroup searches for its own.
+#include "qlora_train_host.h"
+#include "train_device.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVecs = (int)(kGradChunk / (8 * kThreads));  // vectors of eight per thread of a full chunk
+
+__global__ __launch_bounds__(kThreads) void k_grad_table(GradTensors batch, GradChunk* __restrict__ table) {
+  const GradTensor t = batch.t[blockIdx.x];
+  const int64_t chunks = (t.n + kGradChunk - 1) / kGradChunk;
+  for (int64_t c = threadIdx.x; c < chunks; c += kThreads) {
+    const int64_t at = c * kGradChunk, left = t.n - at;
+    GradChunk e;
+    e.in = static_cast<const char*>(t.in) + at * (t.in_f32 ? 4 : 2);
+    e.out = static_cast<char*>(t.out) + at * (t.out_f32 ? 4 : 2);
+    e.n = (int32_t)(left < kGradChunk ? left : kGradChunk);
+    e.in_f32 = (int16_t)t.in_f32;
+    e.out_f32 = (int16_t)t.out_f32;
+    table[t.first + c] = e;
+  }
+}
+
+template <class E>
+__device__ __forceinline__ double chunk_sum(const E* __restrict__ p, int32_t n, double sum) {
+  if (n == kGradChunk) {
+    Raw8<E> r[kVecs];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) load8(r[v], p + 8 * (v * kThreads + (int)threadIdx.x), 8);
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double g = (double)r[v].get(i);
+        sum = fma(g, g, sum);
+      }
+  } else {
+    for (int e = 8 * (int)threadIdx.x; e < n; e += 8 * kThreads) {
+      Raw8<E> r;
+      load8(r, p + e, n - e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double g = (double)r.get(i);
+        sum = fma(g, g, sum);
+      }
+    }
+  }
+  return sum;
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_norm(const GradChunk* __restrict__ table, int64_t chunks,
+                                                        float* norm, double* part, unsigned int* counter) {
+  __shared__ double lds[2][kThreads / 64];
+  __shared__ bool s_last;
+  double sum = 0.0;
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const GradChunk e = table[c];
+    sum = e.in_f32 ? chunk_sum(static_cast<const float*>(e.in), e.n, sum)
+                   : chunk_sum(static_cast<const uint16_t*>(e.in), e.n, sum);
+  }
+  sum = block_sum_f64<kThreads>(sum, lds[0]);
+  if (threadIdx.x == 0) {
+    __hip_atomic_store(part + blockIdx.x, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const unsigned int old = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = old + 1u == gridDim.x;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  // the last workgroup adds the partials in the workgroups' order
+  sum = 0.0;
+  for (unsigned int i = threadIdx.x; i < gridDim.x; i += kThreads)
+    sum += __hip_atomic_load(part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  sum = block_sum_f64<kThreads>(sum, lds[1]);
+  if (threadIdx.x == 0) {
+    *norm = (float)sqrt(sum);
+    __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+
+template <class A, class B>
+__device__ __forceinline__ void chunk_scale(const A* p, B* q, int32_t n, float c) {
+  if (n == kGradChunk) {
+    Raw8<A> r[kVecs];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) load8(r[v], p + 8 * (v * kThreads + (int)threadIdx.x), 8);
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = r[v].get(i) * c;
+      store8(q + 8 * (v * kThreads + (int)threadIdx.x), f, 8);
+    }
+  } else {
+    for (int e = 8 * (int)threadIdx.x; e < n; e += 8 * kThreads) {
+      Raw8<A> r;
+      load8(r, p + e, n - e);
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = r.get(i) * c;
+      store8(q + e, f, n - e);
+    }
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_clip(const GradChunk* __restrict__ table, const float* norm,
+                                                        float max_norm) {
+  const float c = clip_coefficient(*norm, max_norm);
+  const GradChunk e = table[blockIdx.x];
+  if (e.in == e.out && e.in_f32 == e.out_f32 && c == 1.f) return;
+  if (e.in_f32) {
+    if (e.out_f32) chunk_scale(static_cast<const float*>(e.in), static_cast<float*>(e.out), e.n, c);
+    else chunk_scale(static_cast<const float*>(e.in), static_cast<uint16_t*>(e.out), e.n, c);
+  } else {
+    if (e.out_f32) chunk_scale(static_cast<const uint16_t*>(e.in), static_cast<float*>(e.out), e.n, c);
+    else chunk_scale(static_cast<const uint16_t*>(e.in), static_cast<uint16_t*>(e.out), e.n, c);
+  }
+}
+
+}  // namespace
+
+int64_t grad_norm_parts(int64_t chunks) { return chunks < 1 ? 1 : (chunks < 1024 ? chunks : 1024); }
+
+hipError_t launch_grad_table(const GradTensors& batch, int count, GradChunk* table, hipStream_t st) {
+  hipLaunchKernelGGL(k_grad_table, dim3((unsigned)count), dim3(kThreads), 0, st, batch, table);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_norm(const GradChunk* table, int64_t chunks, float* norm, double* part, unsigned int* counter,
+                            hipStream_t st) {
+  hipLaunchKernelGGL(k_grad_norm, dim3((unsigned)grad_norm_parts(chunks)), dim3(kThreads), 0, st, table, chunks, norm,
+                     part, counter);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const GradChunk* table, int64_t chunks, const float* norm, float max_norm,
+                            hipStream_t st) {
+  hipLaunchKernelGGL(k_grad_clip, dim3((unsigned)chunks), dim3(kThreads), 0, st, table, norm, max_norm);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

@@ -83,6 +83,10 @@ struct AdamWScalars {
   float inv_bc2_sqrt;  // 1 / sqrt(1 - beta2^t)
   float eps;
 };
+// The step's argument checks and its scalars (api.cpp); for n == 0 only the checks.
+int adamw_prepare(const float* master, const float* m, const float* v, const uint16_t* grad, const uint16_t* param,
+                  int64_t n, int64_t step, float lr, float beta1, float beta2, float eps, float weight_decay,
+                  AdamWScalars* a);
 hipError_t launch_adamw(float* master, float* m, float* v, const uint16_t* grad, uint16_t* param, int64_t n,
                         const AdamWScalars& a, hipStream_t s);
 

@@ -1,0 +1,147 @@
+// Device helpers of the training-step operators (norms, losses, gradients): eight consecutive
+// elements of a row as FP32, at any element alignment, and sums over a workgroup in a fixed
+// order.
+#pragma once
+
+#include "qlora_device.h"
+
+namespace qlora {
+
+// A row of odd width starts at any multiple of its element size.  gfx950 loads and stores
+// 16 bytes from any address, so the types below only lower the alignment that the compiler
+// may assume; the instructions are the same ones.
+typedef uint32_t u32x4_e2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_e4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// ---- eight BF16 (uint16_t bit patterns) or eight FP32 elements, as loaded
+template <class E>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  uint32_t w[4];
+  __device__ __forceinline__ float get(int i) const {
+    return (i & 1) ? bf16hi_to_f32(w[i >> 1]) : bf16lo_to_f32(w[i >> 1]);
+  }
+};
+template <>
+struct Raw8<float> {
+  float f[8];
+  __device__ __forceinline__ float get(int i) const { return f[i]; }
+};
+
+// Elements [0, n) of p, n in 0..8, zeros beyond them.
+__device__ __forceinline__ void load8(Raw8<uint16_t>& r, const uint16_t* __restrict__ p, int n) {
+  if (n >= 8) {
+    const u32x4_e2 v = *reinterpret_cast<const u32x4_e2*>(p);
+    r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = 2 * i < n ? p[2 * i] : 0u, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0u;
+      r.w[i] = lo | (hi << 16);
+    }
+  }
+}
+__device__ __forceinline__ void load8(Raw8<float>& r, const float* __restrict__ p, int n) {
+  if (n >= 8) {
+    const f32x4_e4 a = *reinterpret_cast<const f32x4_e4*>(p), b = *reinterpret_cast<const f32x4_e4*>(p + 4);
+    r.f[0] = a.x, r.f[1] = a.y, r.f[2] = a.z, r.f[3] = a.w;
+    r.f[4] = b.x, r.f[5] = b.y, r.f[6] = b.z, r.f[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.f[i] = i < n ? p[i] : 0.f;
+  }
+}
+// The first n (0..8) of f, rounded to the element type (nearest, ties to even).
+__device__ __forceinline__ void store8(uint16_t* __restrict__ p, const float f[8], int n) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  if (n >= 8) {
+    *reinterpret_cast<u32x4_e2*>(p) = u32x4_e2{w[0], w[1], w[2], w[3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (uint16_t)((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xFFFFu));
+  }
+}
+__device__ __forceinline__ void store8(float* __restrict__ p, const float f[8], int n) {
+  if (n >= 8) {
+    *reinterpret_cast<f32x4_e4*>(p) = f32x4_e4{f[0], f[1], f[2], f[3]};
+    *reinterpret_cast<f32x4_e4*>(p + 4) = f32x4_e4{f[4], f[5], f[6], f[7]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = f[i];
+  }
+}
+
+// Eight ones, for a weight that is not given.
+__device__ __forceinline__ void ones8(Raw8<uint16_t>& r) { r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0x3F803F80u; }
+
+// Hides from the compiler that r keeps its value, so that nothing derived from it is held in
+// registers across the point.
+__device__ __forceinline__ void opaque(Raw8<uint16_t>& r) {
+  asm volatile("" : "+v"(r.w[0]), "+v"(r.w[1]), "+v"(r.w[2]), "+v"(r.w[3]));
+}
+__device__ __forceinline__ void opaque(Raw8<float>&) {}
+
+__device__ __forceinline__ float to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ float to_f32(float f) { return f; }
+__device__ __forceinline__ uint16_t bf16_of(float f) { return (uint16_t)(pack_bf16x2(f, 0.f) & 0xFFFFu); }
+
+// Clipping coefficient of a global gradient norm; a norm that is NaN gives NaN.
+__device__ __forceinline__ float clip_coefficient(float norm, float max_norm) {
+  const float c = max_norm / (norm + 1e-6f);
+  return c >= 1.f ? 1.f : c;
+}
+
+// Sum over W lanes (a power of two up to 16) of each aligned group of W, the same in them all.
+template <int W>
+__device__ __forceinline__ float group_sum(float v) {
+  if constexpr (W >= 2) v += dpp_partner<0xB1>(v);    // quad_perm [1, 0, 3, 2]
+  if constexpr (W >= 4) v += dpp_partner<0x4E>(v);    // quad_perm [2, 3, 0, 1]
+  if constexpr (W >= 8) v += dpp_partner<0x141>(v);   // row_half_mirror
+  if constexpr (W >= 16) v += dpp_partner<0x140>(v);  // row_mirror
+  return v;
+}
+
+// ---- sums of N values over the T threads of a workgroup, the same in every thread: each
+// wavefront, then the wavefronts' sums as a group of lanes.  `lds` holds N * T / 64 floats; a
+// caller that sums again without a barrier of its own in between gives the next call another
+// array.
+template <int T, int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float* lds) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (T > 64) {
+    constexpr int W = T / 64;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) lds[i * W + wave] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = group_sum<W>(lds[i * W + (threadIdx.x & (W - 1))]);
+  }
+}
+
+// The same for one FP64 value; `lds` holds T / 64 doubles, and the caller separates two calls
+// on one array by a barrier.
+template <int T>
+__device__ __forceinline__ double block_sum_f64(double v, double* lds) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+  if constexpr (T > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) lds[wave] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int w = 0; w < T / 64; ++w) v += lds[w];
+  }
+  return v;
+}
+
+}  // namespace qlora
