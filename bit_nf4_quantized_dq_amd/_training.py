@@ -9,7 +9,7 @@ import functools
 
 import torch
 
-from ._binding import _check, _check_ws, _ptr, _stream, _validate, _WS, load_library
+from ._binding import _check, _check_ws, _ptr, _validate, _WS, load_library
 
 TYPES = {torch.bfloat16: 0, torch.float32: 1}
 NORM_MAX_WIDTH = 8192
@@ -55,12 +55,35 @@ def _lib() -> ctypes.CDLL:
     return _typed
 
 
+# The small calls here take a few microseconds on the device, about as long as their checks, so
+# the marshalling below avoids what costs one on the host: the stream's handle is asked for
+# directly (0.1 us; through a Stream object 2 us), and what is right passes a short check.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream(t: torch.Tensor) -> int:
+    return _raw_stream(t.get_device())
+
+
 def _tensors(specs, device) -> None:
-    """_validate, with a quick pass first: these calls take microseconds on the device."""
-    for t, dtype, _, shape in specs:
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-                and t.device == device and t.is_cuda):
-            _validate(specs, device)
+    """_validate, with a quick pass first."""
+    if device is not None and device.type == "cuda":
+        for t, dtype, _, shape in specs:
+            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+                    and t.is_contiguous()):
+                break
+        else:
+            return
+    _validate(specs, device)
+
+
+def _workspace(ws, nbytes: int, t: torch.Tensor, stream: int) -> torch.Tensor:
+    """The caller's workspace, checked, or the binding's own for this device and stream."""
+    if ws is not None:
+        _check_ws(ws, t.device)
+        return ws
+    buf = _WS._bufs.get((t.get_device(), stream, "train"))
+    return buf if buf is not None and buf.numel() >= nbytes else _WS.get(nbytes, t.device, "train")
 
 
 def _type(t: torch.Tensor, name: str) -> int:
@@ -172,12 +195,12 @@ def norm_residual_bwd(x_out: torch.Tensor | None, y: torch.Tensor | None, dh: to
     dw_pre = torch.empty_like(w_pre) if w_pre is not None and need_weights else None
     dgate = torch.empty_like(gate) if gate is not None and need_gate else None
     rows = int(gate_rows) if gate is not None else 0
-    ws = ws if ws is not None else _WS.get(norm_residual_workspace_size(M, d, rows), dev, "train")
-    _check_ws(ws, dev)
+    st = _stream(stream)
+    ws = _workspace(ws, norm_residual_workspace_size(M, d, rows), stream, st)
     _check(_lib().qlora_norm_residual_bwd(_ptr(x_out), _ptr(y), _ptr(dh), _ptr(dx_out), M, d, kind, int(post_norm),
                                           _ptr(w_post), _ptr(gate), rows, _ptr(w_pre), res_scale, eps, dx.data_ptr(),
                                           _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), ws.data_ptr(),
-                                          ws.numel(), _stream(stream)), "norm_residual_bwd")
+                                          ws.numel(), st), "norm_residual_bwd")
     return dx, dy, dw_post, dgate, dw_pre
 
 
@@ -196,10 +219,10 @@ def token_logps(logits: torch.Tensor, labels: torch.Tensor, logps: torch.Tensor 
     rows = labels.numel()
     if logps is None:
         logps = torch.empty(lead, dtype=torch.float32, device=dev)
-    ws = ws if ws is not None else _WS.get(logps_workspace_size(rows, V), dev, "train")
-    _check_ws(ws, dev)
+    st = _stream(logits)
+    ws = _workspace(ws, logps_workspace_size(rows, V), logits, st)
     _check(_lib().qlora_token_logps(logits.data_ptr(), labels.data_ptr(), rows, V, kind, logps.data_ptr(),
-                                    ws.data_ptr(), ws.numel(), _stream(logits)), "token_logps")
+                                    ws.data_ptr(), ws.numel(), st), "token_logps")
     return logps
 
 
@@ -229,12 +252,12 @@ def preference_loss(logits: torch.Tensor, labels: torch.Tensor, ref_logps: torch
     loss, log_ratios, logps = out[:1], out[1:1 + n], out[1 + n:].view(n, S)
     if need_grad and dlogits is None:
         dlogits = torch.empty_like(logits)
-    ws = ws if ws is not None else _WS.get(preference_workspace_size(n // 2, S, V), dev, "train")
-    _check_ws(ws, dev)
+    st = _stream(logits)
+    ws = _workspace(ws, preference_workspace_size(n // 2, S, V), logits, st)
     at = out.data_ptr()
     _check(_lib().qlora_preference_loss(logits.data_ptr(), labels.data_ptr(), _ptr(ref_logps), n // 2, S, V, kind,
                                         beta, label_smoothing, grad_scale, at, at + 4, at + 4 * (1 + n), _ptr(dlogits),
-                                        ws.data_ptr(), ws.numel(), _stream(logits)), "preference_loss")
+                                        ws.data_ptr(), ws.numel(), st), "preference_loss")
     return loss, log_ratios, logps, dlogits
 
 
@@ -293,10 +316,9 @@ def _grad_call(fn, grads, norm, ws, *args):
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     else:
         _tensors([(norm, torch.float32, "norm", (1,))], dev)
-    ws = ws if ws is not None else _WS.get(grads._ws_bytes, dev, "train")
-    _check_ws(ws, dev)
-    _check(getattr(_lib(), fn)(grads._ref, *args, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(norm)),
-           fn[len("qlora_"):])
+    st = _stream(norm)
+    ws = _workspace(ws, grads._ws_bytes, norm, st)
+    _check(getattr(_lib(), fn)(grads._ref, *args, norm.data_ptr(), ws.data_ptr(), ws.numel(), st), fn[len("qlora_"):])
     return norm
 
 

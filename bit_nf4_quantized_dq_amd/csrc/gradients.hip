@@ -32,7 +32,7 @@ __device__ __forceinline__ double chunk_sum(const E* __restrict__ p, int32_t n, 
   if (n == kGradChunk) {
     Raw8<E> r[kVecs];
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) load8(r[v], p + 8 * (v * kThreads + (int)threadIdx.x), 8);
+    for (int v = 0; v < kVecs; ++v) load_all8(r[v], p + 8 * (v * kThreads + (int)threadIdx.x));
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
 #pragma unroll
@@ -43,7 +43,7 @@ __device__ __forceinline__ double chunk_sum(const E* __restrict__ p, int32_t n, 
   } else {
     for (int e = 8 * (int)threadIdx.x; e < n; e += 8 * kThreads) {
       Raw8<E> r;
-      load8(r, p + e, n - e);
+      load8(r, p + e, n - e, n >= 8);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const double g = (double)r.get(i);
@@ -66,8 +66,12 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(const GradChunk* __restr
   }
   sum = block_sum_f64<kThreads>(sum, lds[0]);
   if (threadIdx.x == 0) {
-    __hip_atomic_store(part + blockIdx.x, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const unsigned int old = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    // The partials travel by system-scope (cache-bypassing) stores and loads, and a store has
+    // completed before its workgroup is counted: a release fence here writes back and drops
+    // an L2 for each of the 1024 workgroups (67 us for the 84 MB of 41.9M BF16 gradients).
+    __hip_atomic_store(part + blockIdx.x, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+    __builtin_amdgcn_s_waitcnt(0);
+    const unsigned int old = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     s_last = old + 1u == gridDim.x;
   }
   __syncthreads();
@@ -75,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(const GradChunk* __restr
   // the last workgroup adds the partials in the workgroups' order
   sum = 0.0;
   for (unsigned int i = threadIdx.x; i < gridDim.x; i += kThreads)
-    sum += __hip_atomic_load(part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    sum += __hip_atomic_load(part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
   sum = block_sum_f64<kThreads>(sum, lds[1]);
   if (threadIdx.x == 0) {
     *norm = (float)sqrt(sum);
@@ -88,7 +92,7 @@ __device__ __forceinline__ void chunk_scale(const A* p, B* q, int32_t n, float c
   if (n == kGradChunk) {
     Raw8<A> r[kVecs];
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) load8(r[v], p + 8 * (v * kThreads + (int)threadIdx.x), 8);
+    for (int v = 0; v < kVecs; ++v) load_all8(r[v], p + 8 * (v * kThreads + (int)threadIdx.x));
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       float f[8];
@@ -99,7 +103,7 @@ __device__ __forceinline__ void chunk_scale(const A* p, B* q, int32_t n, float c
   } else {
     for (int e = 8 * (int)threadIdx.x; e < n; e += 8 * kThreads) {
       Raw8<A> r;
-      load8(r, p + e, n - e);
+      load8(r, p + e, n - e, n >= 8);
       float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = r.get(i) * c;

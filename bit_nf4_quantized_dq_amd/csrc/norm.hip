@@ -27,84 +27,67 @@ struct FwdArgs {
   int post;
 };
 
-// One workgroup of T threads per row; thread t holds the vectors of eight elements t, t + T,
-// ... (V of them) in registers, so every operand is read once.
-template <class S, int T, int V>
+// One workgroup of T threads per row, eight columns to a thread: every operand is read once and
+// kept in registers.
+template <class S, int T, bool SHORT>
 __global__ __launch_bounds__(T) void k_norm_fwd(FwdArgs<S> a) {
   __shared__ float lds[2][T / 64];
-  const int64_t row = blockIdx.x;
-  const int64_t d = a.d, at = row * d;
-  Raw8<S> x[V];
-  Raw8<uint16_t> y[V];
-  int n[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int64_t e = 8 * ((int64_t)v * T + threadIdx.x);
-    n[v] = (int)(d - e < 0 ? 0 : (d - e > 8 ? 8 : d - e));
-    load8(x[v], a.x + at + e, n[v]);
-    if (a.y) load8(y[v], a.y + at + e, n[v]);
+  const int64_t row = blockIdx.x, d = a.d;
+  const Columns<SHORT> col((int)d, 8 * threadIdx.x);
+  Raw8<S> x;
+  Raw8<uint16_t> y, w;
+  col.load(x, a.x + row * d);
+  col.drop(x);
+  if (a.y) {
+    col.load(y, a.y + row * d);
+    col.drop(y);
   }
   float r_y = 1.f;
   if (a.post) {
     float s[1] = {0.f};
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] = fmaf(y[v].get(i), y[v].get(i), s[0]);
+    for (int i = 0; i < 8; ++i) s[0] = fmaf(y.get(i), y.get(i), s[0]);
     block_sum<T>(s, lds[0]);
     r_y = 1.f / sqrtf(s[0] * a.inv_d + a.eps);
   }
-  float xo[V][8], s[1] = {0.f};
-  const int64_t gate_at = a.gate ? row / a.gate_rows * d : 0;
+  float xo[8], s[1] = {0.f};
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int64_t e = 8 * ((int64_t)v * T + threadIdx.x);
+  for (int i = 0; i < 8; ++i) xo[i] = a.scale * x.get(i);
+  if (a.y) {
+    float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) xo[v][i] = a.scale * x[v].get(i);
-    if (a.y) {
-      float q[8];
+    for (int i = 0; i < 8; ++i) q[i] = y.get(i) * r_y;
+    if (a.w_post) {
+      col.load(w, a.w_post);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = y[v].get(i) * r_y;
-      if (a.w_post) {
-        Raw8<uint16_t> w;
-        load8(w, a.w_post + e, n[v]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] *= w.get(i);
-      }
-      if (a.gate) {
-        Raw8<uint16_t> g;
-        load8(g, a.gate + gate_at + e, n[v]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] *= g.get(i);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) xo[v][i] += q[i];
+      for (int i = 0; i < 8; ++i) q[i] *= w.get(i);
     }
+    if (a.gate) {
+      col.load(w, a.gate + row / a.gate_rows * d);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[0] = fmaf(xo[v][i], xo[v][i], s[0]);
-    if (a.x_out) store8(a.x_out + at + e, xo[v], n[v]);
+      for (int i = 0; i < 8; ++i) q[i] *= w.get(i);
+    }
+    // (a column that is not the lane's own gives 0 times a weight: an infinite one would reach
+    // the sum)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= 8 - col.n || SHORT) xo[i] += q[i];
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[0] = fmaf(xo[i], xo[i], s[0]);
+  if (a.x_out) col.store(a.x_out + row * d, xo);
   if (!a.h) return;
   block_sum<T>(s, lds[1]);
   const float r_x = 1.f / sqrtf(s[0] * a.inv_d + a.eps);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int64_t e = 8 * ((int64_t)v * T + threadIdx.x);
+  for (int i = 0; i < 8; ++i) xo[i] *= r_x;
+  if (a.w_pre) {
+    col.load(w, a.w_pre);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) xo[v][i] *= r_x;
-    if (a.w_pre) {
-      Raw8<uint16_t> w;
-      load8(w, a.w_pre + e, n[v]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) xo[v][i] *= w.get(i);
-    }
-    store8(a.h + at + e, xo[v], n[v]);
+    for (int i = 0; i < 8; ++i) xo[i] *= w.get(i);
   }
+  col.store(a.h + row * d, xo);
 }
-
-// How the gate's gradient leaves the backward: each row its own (one gate row per row), one
-// FP32 partial per segment, or whole gate rows inside a segment.
-enum GateMode : int { kGateNone = 0, kGateRow = 1, kGatePart = 2, kGateWhole = 3 };
 
 template <class S>
 struct BwdArgs {
@@ -114,70 +97,89 @@ struct BwdArgs {
   const uint16_t *w_post, *gate, *w_pre;
   S* dx;
   uint16_t* dy;
-  uint16_t* dgate;
+  uint16_t* dgate;                 // for gate rows whole in a segment, else null
   float *p_pre, *p_post, *p_gate;  // [segment][d] FP32 partials, null where not wanted
   int64_t M, d, gate_rows;
   NormSegments seg;
   float scale, eps, inv_d;
-  int post, gate_mode;
+  int post;
 };
 
-// What one row gives the eight columns of a vector.  An operand that is not given is zeros, a
-// weight or gate that is not given is ones, so the arithmetic has no cases.
-template <class S>
+// What one row gives a lane's columns.  An operand that is not given is zeros, a weight or gate
+// that is not given is ones, so the arithmetic has no cases.
+template <class S, bool SHORT>
 struct RowVec {
   Raw8<S> x, dxo;
-  Raw8<uint16_t> y, dh, g;
-  // at, gate_at: the starts of the rows (the same in every lane); e, n: the lane's vector
-  __device__ __forceinline__ void load(const BwdArgs<S>& a, int64_t at, int64_t gate_at, uint32_t e, int n) {
-    load8(x, (a.x + at) + e, a.dh ? n : 0);
-    load8(dxo, (a.dx_out + at) + e, a.dx_out ? n : 0);
-    load8(y, (a.y + at) + e, a.y ? n : 0);
-    load8(dh, (a.dh + at) + e, a.dh ? n : 0);
-    if (a.gate) load8(g, (a.gate + gate_at) + e, n);
-    else ones8(g);
+  Raw8<uint16_t> y, dh;
+  __device__ __forceinline__ void load(const BwdArgs<S>& a, const Columns<SHORT>& col, int64_t at) {
+    if (a.dh) {
+      col.load(x, a.x + at);
+      col.load(dh, a.dh + at);
+    } else {
+      zero8(x), zero8(dh);
+    }
+    if (a.dx_out) col.load(dxo, a.dx_out + at);
+    else zero8(dxo);
+    if (a.y) col.load(y, a.y + at);
+    else zero8(y);
   }
-  __device__ __forceinline__ void pack() { opaque(x), opaque(dxo), opaque(y), opaque(dh), opaque(g); }
+  __device__ __forceinline__ void pack() { opaque(x), opaque(dxo), opaque(y), opaque(dh); }
 };
 
 // One workgroup per segment of consecutive rows.  Its threads own columns, so the column sums
 // (weights, gate) stay in registers over the segment; the sums over a row are one exchange:
 // with q = g w_post y,  sum(b y) = sum(dx' q) + r_x sum(a q) - k sum(x' q),  k = r_x^3 mean(a x').
-template <class S, int T>
-__global__ __launch_bounds__(T) void k_norm_bwd(BwdArgs<S> a) {
+template <class S, int T, bool SHORT>
+__global__ __launch_bounds__(T, SHORT ? 1 : 4) void k_norm_bwd(BwdArgs<S> a) {
   __shared__ float lds[2][6 * (T / 64)];
   const int64_t d = a.d, seg = blockIdx.x;
   // segments inside a gate row's rows (per_group of them), or of whole gate rows
-  int64_t r0 = seg * a.seg.rows, end = a.M;
+  int64_t r0 = seg * a.seg.rows, end = a.M, group;
   if (a.seg.per_group) {
-    const int64_t group = seg / a.seg.per_group;
+    group = seg / a.seg.per_group;
     r0 = group * a.gate_rows + (seg - group * a.seg.per_group) * a.seg.rows;
     end = (group + 1) * a.gate_rows < a.M ? (group + 1) * a.gate_rows : a.M;
+  } else {
+    group = r0 / a.gate_rows;
   }
   const int64_t r1 = r0 + a.seg.rows < end ? r0 + a.seg.rows : end;
-  const uint32_t e = 8 * threadIdx.x;
-  const int left = (int)d - (int)e, n = left < 0 ? 0 : (left > 8 ? 8 : left);
-  Raw8<uint16_t> w_pre, w_post;
-  if (a.w_pre) load8(w_pre, a.w_pre + e, n);
+  int64_t group_end = (group + 1) * a.gate_rows < a.M ? (group + 1) * a.gate_rows : a.M;
+  const Columns<SHORT> col((int)d, 8 * threadIdx.x);
+  Raw8<uint16_t> w_pre, w_post, g;
+  if (a.w_pre) col.load(w_pre, a.w_pre);
   else ones8(w_pre);
-  if (a.w_post) load8(w_post, a.w_post + e, n);
+  if (a.w_post) col.load(w_post, a.w_post);
   else ones8(w_post);
-  float s_pre[8], s_post[8], s_gate[8];
+  const auto load_gate = [&] {
+    if (a.gate) col.load(g, a.gate + group * d);
+    else ones8(g);
+  };
+  // s_tu: sum of t u over the rows of one gate row; times the gate it goes into dw_post, times
+  // w_post it is the gate's gradient
+  float s_pre[8], s_post[8], s_tu[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s_pre[i] = s_post[i] = s_gate[i] = 0.f;
+  for (int i = 0; i < 8; ++i) s_pre[i] = s_post[i] = s_tu[i] = 0.f;
   const bool post = a.post != 0;
+  const uint32_t post_bits = post ? 0xFFFFFFFFu : 0u;
+  // sixteen wavefronts to a compute unit have 128 registers each: with an FP32 stream the next
+  // row does not fit
+  constexpr bool kAhead = sizeof(S) == 2 && !SHORT;
+  RowVec<S, SHORT> r, next;
+  if (r0 < r1) r.load(a, col, r0 * d), load_gate();
+  else if (a.p_gate) col.store(a.p_gate + seg * d, s_tu);
   for (int64_t row = r0; row < r1; ++row) {
-    const int64_t at = row * d, group = a.gate ? row / a.gate_rows : 0;
-    RowVec<S> r;
-    r.load(a, at, group * d, e, n);
+    const int64_t at = row * d;
+    // the next row's loads run under this row's exchange
+    if (kAhead && row + 1 < r1) next.load(a, col, at + d);
     // what is held across the exchange stays packed (unpacked once for both uses it would take
     // 56 registers more)
-    opaque(w_pre), opaque(w_post);
+    opaque(w_pre), opaque(w_post), opaque(g), r.pack();
+    col.drop(r.x), col.drop(r.y);
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float xi = r.x.get(i), yi = r.y.get(i), ai = r.dh.get(i) * w_pre.get(i);
-      const float q = yi * w_post.get(i) * r.g.get(i);
+      const float q = yi * w_post.get(i) * g.get(i);
       s[0] = fmaf(xi, xi, s[0]);
       s[1] = fmaf(ai, xi, s[1]);
       s[2] = fmaf(yi, yi, s[2]);
@@ -186,40 +188,49 @@ __global__ __launch_bounds__(T) void k_norm_bwd(BwdArgs<S> a) {
       s[5] = fmaf(xi, q, s[5]);
     }
     block_sum<T>(s, lds[(row - r0) & 1]);
-    opaque(w_pre), opaque(w_post), r.pack();
+    opaque(w_pre), opaque(w_post), opaque(g), r.pack();
     const float r_x = a.dh ? 1.f / sqrtf(s[0] * a.inv_d + a.eps) : 0.f;
     const float k = a.dh ? r_x * r_x * r_x * (s[1] * a.inv_d) : 0.f;
     const float r_y = post ? 1.f / sqrtf(s[2] * a.inv_d + a.eps) : 1.f;
     const float c = post ? r_y * r_y * r_y * ((s[3] + r_x * s[4] - k * s[5]) * a.inv_d) : 0.f;
-    float dx[8], dy[8], dg[8];
+    float t[8], o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float xi = r.x.get(i), yi = r.y.get(i), dhi = r.dh.get(i), wi = w_post.get(i);
-      const float t = r.dxo.get(i) + (r_x * (dhi * w_pre.get(i)) - xi * k);
-      const float u = yi * r_y, tg = t * r.g.get(i);
+      const float xi = r.x.get(i), dhi = r.dh.get(i);
+      t[i] = r.dxo.get(i) + (r_x * (dhi * w_pre.get(i)) - xi * k);
       s_pre[i] = fmaf(dhi, xi * r_x, s_pre[i]);
-      s_post[i] = fmaf(tg, u, s_post[i]);
-      dg[i] = t * (u * wi);
-      dx[i] = a.scale * t;
-      dy[i] = post ? r_y * (tg * wi) - yi * c : tg;
+      o[i] = a.scale * t[i];
     }
-    if (a.dx) store8((a.dx + at) + e, dx, n);
-    if (a.dy) store8((a.dy + at) + e, dy, n);
-    if (a.gate_mode == kGateRow) {
-      store8((a.dgate + at) + e, dg, n);
-    } else {
+    if (a.dx) col.store(a.dx + at, o);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s_gate[i] += dg[i];
-      if (a.gate_mode == kGateWhole && ((row + 1) % a.gate_rows == 0 || row + 1 == a.M)) {
-        store8((a.dgate + group * d) + e, s_gate, n);
+    for (int i = 0; i < 8; ++i) {
+      const float yi = r.y.get(i);
+      s_tu[i] = fmaf(t[i], yi * r_y, s_tu[i]);
+      o[i] = r_y * (t[i] * g.get(i) * w_post.get(i)) - __uint_as_float(__float_as_uint(yi) & post_bits) * c;
+    }
+    if (a.dy) col.store(a.dy + at, o);
+    if (row + 1 == group_end || row + 1 == r1) {
+      float dg[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s_gate[i] = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        s_post[i] = fmaf(s_tu[i], g.get(i), s_post[i]);
+        dg[i] = s_tu[i] * w_post.get(i);
+        s_tu[i] = 0.f;
+      }
+      if (a.dgate) col.store(a.dgate + group * d, dg);
+      if (a.p_gate) col.store(a.p_gate + seg * d, dg);
+      if (row + 1 < r1) {
+        ++group;
+        group_end = group_end + a.gate_rows < a.M ? group_end + a.gate_rows : a.M;
+        load_gate();
       }
     }
+    if (kAhead) r = next;
+    else if (row + 1 < r1) r.load(a, col, at + d);
   }
-  if (a.p_pre) store8((a.p_pre + seg * d) + e, s_pre, n);
-  if (a.p_post) store8((a.p_post + seg * d) + e, s_post, n);
-  if (a.p_gate) store8((a.p_gate + seg * d) + e, s_gate, n);
+  if (a.p_pre) col.store(a.p_pre + seg * d, s_pre);
+  if (a.p_post) col.store(a.p_post + seg * d, s_post);
 }
 
 // Column sums of the segments' partials, in the segments' order within each of the 16 slices
@@ -258,25 +269,26 @@ __global__ __launch_bounds__(kColThreads) void k_norm_cols(const float* __restri
   }
 }
 
-template <class S, int T, int V>
+template <class S, int T, bool SHORT = false>
 hipError_t fwd_as(const NormFwd& p, hipStream_t st) {
   FwdArgs<S> a{static_cast<const S*>(p.x), p.y, p.w_post, p.gate, p.w_pre, static_cast<S*>(p.x_out), p.h, p.d,
                p.gate_rows, p.scale, p.eps, (float)(1.0 / (double)p.d), p.post};
-  hipLaunchKernelGGL((k_norm_fwd<S, T, V>), dim3((unsigned)p.M), dim3(T), 0, st, a);
+  hipLaunchKernelGGL((k_norm_fwd<S, T, SHORT>), dim3((unsigned)p.M), dim3(T), 0, st, a);
   return hipGetLastError();
 }
 
 template <class S>
 hipError_t fwd(const NormFwd& p, hipStream_t st) {
   const int64_t n8 = (p.d + 7) / 8;
-  if (n8 <= 64) return fwd_as<S, 64, 1>(p, st);
-  if (n8 <= 128) return fwd_as<S, 128, 1>(p, st);
-  if (n8 <= 256) return fwd_as<S, 256, 1>(p, st);
-  if (n8 <= 512) return fwd_as<S, 512, 1>(p, st);
-  return fwd_as<S, 1024, 1>(p, st);
+  if (p.d < 8) return fwd_as<S, 64, true>(p, st);
+  if (n8 <= 64) return fwd_as<S, 64>(p, st);
+  if (n8 <= 128) return fwd_as<S, 128>(p, st);
+  if (n8 <= 256) return fwd_as<S, 256>(p, st);
+  if (n8 <= 512) return fwd_as<S, 512>(p, st);
+  return fwd_as<S, 1024>(p, st);
 }
 
-template <class S, int T>
+template <class S, int T, bool SHORT = false>
 hipError_t bwd_as(const NormBwd& p, hipStream_t st) {
   const NormSegments seg = norm_segments(p.M, p.d, p.gate ? p.gate_rows : 0);
   const int64_t per = seg.count * p.d;
@@ -284,14 +296,14 @@ hipError_t bwd_as(const NormBwd& p, hipStream_t st) {
   BwdArgs<S> a{};
   a.x = static_cast<const S*>(p.x), a.y = p.y, a.dh = p.dh, a.dx_out = static_cast<const S*>(p.dx_out);
   a.w_post = p.w_post, a.gate = p.gate, a.w_pre = p.w_pre;
-  a.dx = static_cast<S*>(p.dx), a.dy = p.dy, a.dgate = p.dgate;
-  a.M = p.M, a.d = p.d, a.gate_rows = p.gate ? p.gate_rows : 1, a.seg = seg;
+  a.dx = static_cast<S*>(p.dx), a.dy = p.dy;
+  a.M = p.M, a.d = p.d, a.gate_rows = p.gate ? p.gate_rows : p.M, a.seg = seg;
   a.scale = p.scale, a.eps = p.eps, a.inv_d = (float)(1.0 / (double)p.d), a.post = p.post;
-  a.gate_mode = !p.dgate ? kGateNone : (p.gate_rows == 1 ? kGateRow : (seg.per_group ? kGatePart : kGateWhole));
+  if (!seg.per_group) a.dgate = p.dgate;
   if (p.dw_pre) a.p_pre = part, part += per;
   if (p.dw_post) a.p_post = part, part += per;
-  if (a.gate_mode == kGatePart) a.p_gate = part;
-  hipLaunchKernelGGL((k_norm_bwd<S, T>), dim3((unsigned)seg.count), dim3(T), 0, st, a);
+  if (p.dgate && seg.per_group) a.p_gate = part;
+  hipLaunchKernelGGL((k_norm_bwd<S, T, SHORT>), dim3((unsigned)seg.count), dim3(T), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t groups = a.p_gate ? (p.M + p.gate_rows - 1) / p.gate_rows : 0;
@@ -306,6 +318,7 @@ hipError_t bwd_as(const NormBwd& p, hipStream_t st) {
 template <class S>
 hipError_t bwd(const NormBwd& p, hipStream_t st) {
   const int64_t n8 = (p.d + 7) / 8;
+  if (p.d < 8) return bwd_as<S, 64, true>(p, st);
   if (n8 <= 64) return bwd_as<S, 64>(p, st);
   if (n8 <= 128) return bwd_as<S, 128>(p, st);
   if (n8 <= 256) return bwd_as<S, 256>(p, st);

@@ -25,25 +25,27 @@ __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2) {
   m = t;
 }
 
-// Rows of a launch: `half` rows of chosen answers from row `first`, then as many of rejected
-// ones from row first + offset (or, with offset 0, simply the rows from `first`).
-struct Rows {
-  int64_t first, half, offset;
-  __device__ __forceinline__ int64_t at(int64_t i) const { return first + (i < half ? i : i - half + offset); }
-};
+// What one pass over a row gives, rounded to FP32 only at the end: the label's log-probability
+// from the exact difference to the maximum and an FP64 logarithm.
+__device__ __forceinline__ double label_logp(float xl, float m, float s) {
+  return (double)xl - (double)m - log((double)s);
+}
 
-// One workgroup per row and part: one pass with the running maximum and sum of each thread.
+// One workgroup per row and part: one pass with the running maximum and sum of each thread.  A
+// whole row (parts == 1) is finished here, a split one by its readers.
 template <class E>
 __global__ __launch_bounds__(kRowThreads) void k_row_stats(const E* __restrict__ logits,
-                                                           const int64_t* __restrict__ labels, Rows rows, int64_t V,
-                                                           int64_t parts, int64_t len, MaxSum* part, MaxSum* row_stat,
-                                                           float* label_logit, float* logps) {
+                                                           const int64_t* __restrict__ labels,
+                                                           const float* __restrict__ ref, int64_t V, int64_t parts,
+                                                           int64_t len, RowStats ws, float* __restrict__ logps) {
   __shared__ float lm[kRowThreads / 64], ls[kRowThreads / 64];
-  const int64_t i = blockIdx.x / parts, p = blockIdx.x - i * parts;
-  const int64_t row = rows.at(i);
+  const int64_t row = blockIdx.x / parts, p = blockIdx.x - row * parts;
   const int64_t label = labels[row];
   if (label < 0 || label >= V) {
-    if (parts == 1 && threadIdx.x == 0) logps[row] = 0.f;
+    if (parts == 1 && threadIdx.x == 0) {
+      logps[row] = 0.f;
+      if (ws.ratio) ws.ratio[row] = 0.0;
+    }
     return;
   }
   const E* x = logits + row * V;
@@ -51,34 +53,33 @@ __global__ __launch_bounds__(kRowThreads) void k_row_stats(const E* __restrict__
   float xl = 0.f;
   if (threadIdx.x == 0) xl = to_f32(x[label]);
   float m = -INFINITY, s = 0.f;
-  constexpr int64_t kStep = 8 * kRowThreads;
-  for (int64_t v = v0 + 8 * threadIdx.x; v < v1; v += kUnroll * kStep) {
+  const auto take = [&](const Raw8<E>& r, int n) {
+    float f[8], t = m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j < n ? r.get(j) : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t = fmaxf(t, f[j]);
+    const float base = t == -INFINITY ? 0.f : t;
+    s *= exp2_hw((m - base) * kLog2e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += exp2_hw((f[j] - base) * kLog2e);
+    m = t;
+  };
+  const int64_t full = (v1 - v0) >> 3;
+  const E* xp = x + v0;
+  for (int64_t i = threadIdx.x; i < full; i += kUnroll * kRowThreads) {
     Raw8<E> r[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t left = v1 - (v + u * kStep);
-      if (left >= 8) load8(r[u], x + v + u * kStep, 8);
-    }
+    for (int u = 0; u < kUnroll; ++u)
+      if (i + u * kRowThreads < full) load_all8(r[u], xp + 8 * (i + u * kRowThreads));
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t left = v1 - (v + u * kStep);
-      if (left <= 0) break;
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = r[u].get(j);
-      if (left < 8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = j < left ? to_f32(x[v + u * kStep + j]) : -INFINITY;
-      }
-      float t = m;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t = fmaxf(t, f[j]);
-      const float ref = t == -INFINITY ? 0.f : t;
-      s *= exp2_hw((m - ref) * kLog2e);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += exp2_hw((f[j] - ref) * kLog2e);
-      m = t;
-    }
+    for (int u = 0; u < kUnroll; ++u)
+      if (i + u * kRowThreads < full) take(r[u], 8);
+  }
+  if (const int tail = (int)((v1 - v0) & 7); tail && threadIdx.x == 0) {
+    Raw8<E> r;
+    load8(r, xp + 8 * full, tail, V >= 8);
+    take(r, tail);
   }
 #pragma unroll
   for (int k = 32; k >= 1; k >>= 1) merge(m, s, __shfl_xor(m, k, 64), __shfl_xor(s, k, 64));
@@ -87,158 +88,200 @@ __global__ __launch_bounds__(kRowThreads) void k_row_stats(const E* __restrict__
   if (threadIdx.x == 0) {
     m = lm[0], s = ls[0];
     for (int w = 1; w < kRowThreads / 64; ++w) merge(m, s, lm[w], ls[w]);
+    ws.part[row * parts + p] = MaxSum{m, s};
     if (parts == 1) {
-      logps[row] = (xl - m) - logf(s);
-      row_stat[row] = MaxSum{m, 1.f / s};
-    } else {
-      part[row * parts + p] = MaxSum{m, s};
-      if (p == 0) label_logit[row] = xl;
+      const double lp = label_logp(xl, m, s);
+      logps[row] = (float)lp;
+      if (ws.ratio) ws.ratio[row] = lp - (ref ? (double)ref[row] : 0.0);
+    } else if (p == 0) {
+      ws.label_logit[row] = xl;
     }
   }
 }
 
 // The parts of one row, joined in their order.
-__device__ __forceinline__ float join_row(const MaxSum* part, int64_t parts, float xl, MaxSum* stat) {
-  float m = part[0].m, s = part[0].s;
-  for (int64_t p = 1; p < parts; ++p) merge(m, s, part[p].m, part[p].s);
-  *stat = MaxSum{m, 1.f / s};
-  return (xl - m) - logf(s);
+__device__ __forceinline__ MaxSum join_row(const MaxSum* part, int64_t parts) {
+  MaxSum r = part[0];
+  for (int64_t p = 1; p < parts; ++p) merge(r.m, r.s, part[p].m, part[p].s);
+  return r;
 }
 
-__global__ __launch_bounds__(kRowThreads) void k_row_join(const MaxSum* __restrict__ part, int64_t parts,
-                                                          const float* __restrict__ label_logit,
-                                                          const int64_t* __restrict__ labels, int64_t V, int64_t rows,
-                                                          MaxSum* row_stat, float* logps) {
+__global__ __launch_bounds__(kRowThreads) void k_row_join(const int64_t* __restrict__ labels, int64_t V, int64_t rows,
+                                                          int64_t parts, RowStats ws, float* __restrict__ logps) {
   const int64_t row = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
   if (row >= rows) return;
-  const bool counted = labels[row] >= 0 && labels[row] < V;
-  logps[row] = counted ? join_row(part + row * parts, parts, label_logit[row], row_stat + row) : 0.f;
+  float lp = 0.f;
+  if (labels[row] >= 0 && labels[row] < V) {
+    const MaxSum r = join_row(ws.part + row * parts, parts);
+    lp = (float)label_logp(ws.label_logit[row], r.m, r.s);
+  }
+  logps[row] = lp;
 }
 
-// One workgroup per pair: joins split rows, sums the log ratios in FP64 and forms the pair's
-// loss and the coefficient of its gradient.
-constexpr int kPairThreads = 1024;
 struct PairArgs {
   const int64_t* labels;
   const float* ref;
-  int64_t pairs, S, V, parts, first;
+  int64_t pairs, S, V, parts;
   float beta, smoothing, grad_scale;
   RowStats ws;
-  float *logps, *log_ratios;
+  float *logps, *log_ratios, *loss;
 };
-__global__ __launch_bounds__(kPairThreads) void k_pairs(PairArgs a) {
-  __shared__ double lds[2][kPairThreads / 64];
-  const int64_t pair = a.first + blockIdx.x;
-  double sum[2] = {0.0, 0.0};
+struct PairLds {
+  double sum[2][kRowThreads / 64];
+  double mean[kRowThreads / 64];
+  bool last;
+};
+
+// The pair's log ratios, summed in FP64 in one order by whichever workgroup asks: for whole rows
+// two short sums of what the first pass left, for split rows after joining their parts.
+__device__ __forceinline__ void pair_sums(const PairArgs& a, int64_t pair, bool write, PairLds& lds, double out[2]) {
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
     const int64_t r0 = (pair + side * a.pairs) * a.S;
-    for (int64_t t = threadIdx.x; t < a.S; t += kPairThreads) {
-      const int64_t row = r0 + t, label = a.labels[row];
-      if (label < 0 || label >= a.V) {
-        if (a.parts > 1) a.logps[row] = 0.f;
-        continue;
-      }
-      float lp;
-      if (a.parts > 1) {
-        lp = join_row(a.ws.part + row * a.parts, a.parts, a.ws.label_logit[row], a.ws.row + row);
-        a.logps[row] = lp;
-      } else {
-        lp = a.logps[row];
-      }
-      sum[side] += (double)lp - (a.ref ? (double)a.ref[row] : 0.0);
-    }
-    sum[side] = block_sum_f64<kPairThreads>(sum[side], lds[side]);
-  }
-  if (threadIdx.x == 0) {
-    a.log_ratios[pair] = (float)sum[0];
-    a.log_ratios[pair + a.pairs] = (float)sum[1];
-    const double z = (double)a.beta * (sum[0] - sum[1]), e = a.smoothing;
-    const double tail = log1p(exp(-fabs(z)));
-    // a product with a smoothing of exactly 0 or 1 leaves out an infinite softplus
-    const double win = tail + fmax(-z, 0.0), lose = tail + fmax(z, 0.0);
-    a.ws.pair_loss[pair] = (e == 1.0 ? 0.0 : (1.0 - e) * (z != z ? z : win)) + (e == 0.0 ? 0.0 : e * (z != z ? z : lose));
-    const double sig = z >= 0.0 ? 1.0 / (1.0 + exp(-z)) : exp(z) / (1.0 + exp(z));
-    const double c = (double)a.grad_scale * ((double)a.beta / (double)a.pairs) * (z != z ? z : sig + e - 1.0);
-    a.ws.coef[pair] = (float)c;
-    a.ws.coef[pair + a.pairs] = (float)-c;
-  }
-}
-
-__device__ __forceinline__ void mean_loss(const double* pair_loss, int64_t pairs, float* loss, double* lds) {
-  double s = 0.0;
-  for (int64_t i = threadIdx.x; i < pairs; i += kRowThreads) s += pair_loss[i];
-  s = block_sum_f64<kRowThreads>(s, lds);
-  if (threadIdx.x == 0) *loss = (float)(s / (double)pairs);
-}
-__global__ __launch_bounds__(kRowThreads) void k_loss(const double* pair_loss, int64_t pairs, float* loss) {
-  __shared__ double lds[kRowThreads / 64];
-  mean_loss(pair_loss, pairs, loss, lds);
-}
-
-// The gradient: one workgroup per row and part, each element read and written once.
-template <class E>
-__global__ __launch_bounds__(kRowThreads) void k_pref_grad(const E* logits, E* dlogits,
-                                                           const int64_t* __restrict__ labels, Rows rows, int64_t S,
-                                                           int64_t V, int64_t parts, int64_t len,
-                                                           const MaxSum* __restrict__ row_stat,
-                                                           const float* __restrict__ coef,
-                                                           const double* __restrict__ pair_loss, int64_t pairs,
-                                                           float* loss) {
-  __shared__ double lds[kRowThreads / 64];
-  if (loss && blockIdx.x == 0) mean_loss(pair_loss, pairs, loss, lds);
-  const int64_t i = blockIdx.x / parts, p = blockIdx.x - i * parts;
-  const int64_t row = rows.at(i);
-  const int64_t label = labels[row];
-  const bool counted = label >= 0 && label < V;
-  const float c = counted ? coef[row / S] : 0.f;
-  const MaxSum stat = counted ? row_stat[row] : MaxSum{0.f, 0.f};
-  const float scale = -c * stat.s;
-  const int64_t v0 = p * len, v1 = v0 + len < V ? v0 + len : V;
-  const E* x = logits + row * V;
-  E* out = dlogits + row * V;
-  constexpr int64_t kStep = 8 * kRowThreads;
-  for (int64_t v = v0 + 8 * threadIdx.x; v < v1; v += kUnroll * kStep) {
-    Raw8<E> r[kUnroll];
-    if (counted) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int64_t left = v1 - (v + u * kStep);
-        if (left > 0) load8(r[u], x + v + u * kStep, left < 8 ? (int)left : 8);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t at = v + u * kStep, left = v1 - at;
-      if (left <= 0) break;
-      float f[8];
-      if (counted) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = scale * exp2_hw((r[u].get(j) - stat.m) * kLog2e);
-        if (label >= at && label < at + 8) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (at + j == label) f[j] += c;
+    double sum = 0.0;
+    if (a.parts == 1) {
+#pragma unroll 4
+      for (int64_t t = threadIdx.x; t < a.S; t += kRowThreads) sum += a.ws.ratio[r0 + t];
+    } else {
+      for (int64_t t = threadIdx.x; t < a.S; t += kRowThreads) {
+        const int64_t row = r0 + t, label = a.labels[row];
+        double lp = 0.0;
+        if (label >= 0 && label < a.V) {
+          const MaxSum r = join_row(a.ws.part + row * a.parts, a.parts);
+          lp = label_logp(a.ws.label_logit[row], r.m, r.s);
+          sum += lp - (a.ref ? (double)a.ref[row] : 0.0);
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = 0.f;
+        if (write) a.logps[row] = (float)lp;
       }
-      store8(out + at, f, left < 8 ? (int)left : 8);
     }
+    out[side] = block_sum_f64<kRowThreads>(sum, lds.sum[side]);
   }
+}
+
+// d loss / d (chosen log ratio) of a pair, times grad_scale.
+__device__ __forceinline__ float pair_slope(const PairArgs& a, const double d[2]) {
+  const double z = (double)a.beta * (d[0] - d[1]);
+  const double t = exp(-fabs(z)), sig = (z >= 0.0 ? 1.0 : t) / (1.0 + t);
+  return (float)((double)a.grad_scale * ((double)a.beta / (double)a.pairs) * (sig + (double)a.smoothing - 1.0));
+}
+
+// One workgroup of each pair writes its log ratios and its loss; the last of them to arrive adds
+// the losses in the pairs' order.  The losses travel by system-scope (cache-bypassing) stores
+// and loads, and a store has completed before its workgroup is counted.
+__device__ void finish_pair(const PairArgs& a, int64_t pair, const double d[2], PairLds& lds) {
+  if (threadIdx.x == 0) {
+    a.log_ratios[pair] = (float)d[0];
+    a.log_ratios[pair + a.pairs] = (float)d[1];
+    const double z = (double)a.beta * (d[0] - d[1]), e = a.smoothing;
+    const double tail = log1p(exp(-fabs(z)));
+    double loss = z;  // NaN stays NaN
+    if (z == z) {
+      // a factor of exactly 0 leaves an infinite term out
+      loss = (e == 1.0 ? 0.0 : (1.0 - e) * (tail + fmax(-z, 0.0))) + (e == 0.0 ? 0.0 : e * (tail + fmax(z, 0.0)));
+    }
+    __hip_atomic_store(a.ws.pair_loss + pair, loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+    __builtin_amdgcn_s_waitcnt(0);
+    const unsigned int old =
+        __hip_atomic_fetch_add(a.ws.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    lds.last = old + 1u == (unsigned int)a.pairs;
+    if (lds.last) __hip_atomic_store(a.ws.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!lds.last) return;
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < a.pairs; i += kRowThreads)
+    s += __hip_atomic_load(a.ws.pair_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+  s = block_sum_f64<kRowThreads>(s, lds.mean);
+  if (threadIdx.x == 0) *a.loss = (float)(s / (double)a.pairs);
+}
+
+// The loss alone: one workgroup per pair.
+__global__ __launch_bounds__(kRowThreads) void k_pref_loss(PairArgs a) {
+  __shared__ PairLds lds;
+  double d[2];
+  pair_sums(a, blockIdx.x, true, lds, d);
+  finish_pair(a, blockIdx.x, d, lds);
+}
+
+// The gradient: one workgroup per row and part, each element read and written once.  Each takes
+// its pair's slope from the pair's sums itself, so nothing runs between the two passes.  Rows
+// go from the last to the first: the end of what the first pass read is still in the cache.
+template <class E>
+__global__ __launch_bounds__(kRowThreads) void k_pref_grad(const E* logits, E* dlogits, PairArgs a, int64_t len) {
+  __shared__ PairLds lds;
+  const int64_t block = (int64_t)gridDim.x - 1 - blockIdx.x;
+  const int64_t row = block / a.parts, p = block - row * a.parts;
+  const int64_t seq = row / a.S, pair = seq < a.pairs ? seq : seq - a.pairs;
+  const int64_t label = a.labels[row], V = a.V;
+  const bool counted = label >= 0 && label < V;
+  const bool lead = p == 0 && seq < a.pairs && row == seq * a.S;  // this pair's workgroup
+  double d[2];
+  if (counted || lead) pair_sums(a, pair, lead, lds, d);
+  if (lead) finish_pair(a, pair, d, lds);
+  float c = 0.f, scale = 0.f, m = 0.f;
+  if (counted) {
+    c = pair_slope(a, d);
+    if (seq >= a.pairs) c = -c;
+    const MaxSum r = join_row(a.ws.part + row * a.parts, a.parts);
+    m = r.m;
+    scale = -c / r.s;
+  }
+  const int64_t v0 = p * len, v1 = v0 + len < V ? v0 + len : V;
+  const E* x = logits + row * V + v0;
+  E* out = dlogits + row * V + v0;
+  const auto give = [&](const Raw8<E>& r, int64_t at, int n) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = scale * exp2_hw((r.get(j) - m) * kLog2e);
+    const int64_t j0 = label - v0 - at;
+    if (j0 >= 0 && j0 < 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j == j0) f[j] += c;
+    }
+    store8(out + at, f, n);
+  };
+  const int64_t full = (v1 - v0) >> 3;
+  const int tail = (int)((v1 - v0) & 7);
+  if (!counted) {
+    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int64_t i = threadIdx.x; i < full; i += kRowThreads) store8(out + 8 * i, zero, 8);
+    if (tail && threadIdx.x == 0) store8(out + 8 * full, zero, tail);
+    return;
+  }
+  for (int64_t i = threadIdx.x; i < full; i += kUnroll * kRowThreads) {
+    Raw8<E> r[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (i + u * kRowThreads < full) load_all8(r[u], x + 8 * (i + u * kRowThreads));
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (i + u * kRowThreads < full) give(r[u], 8 * (i + u * kRowThreads), 8);
+  }
+  if (tail && threadIdx.x == 0) {
+    // in place, a neighbour may have replaced the elements before the tail: they are dropped
+    Raw8<E> r;
+    load8(r, x + 8 * full, tail, V >= 8);
+    give(r, 8 * full, tail);
+  }
+}
+
+template <class E>
+hipError_t stats(const E* logits, const int64_t* labels, const float* ref, int64_t rows, int64_t V, const RowSplit& sp,
+                 float* logps, const RowStats& ws, hipStream_t st) {
+  hipLaunchKernelGGL((k_row_stats<E>), dim3((unsigned)(rows * sp.parts)), dim3(kRowThreads), 0, st, logits, labels, ref,
+                     V, sp.parts, sp.len, ws, logps);
+  return hipGetLastError();
 }
 
 template <class E>
 hipError_t logps_as(const E* logits, const int64_t* labels, int64_t rows, int64_t V, float* logps, const RowStats& ws,
                     hipStream_t st) {
   const RowSplit sp = row_split(rows, V);
-  hipLaunchKernelGGL((k_row_stats<E>), dim3((unsigned)(rows * sp.parts)), dim3(kRowThreads), 0, st, logits, labels,
-                     (Rows{0, rows, 0}), V, sp.parts, sp.len, ws.part, ws.row, ws.label_logit, logps);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = stats(logits, labels, nullptr, rows, V, sp, logps, ws, st);
   if (e != hipSuccess || sp.parts == 1) return e;
   hipLaunchKernelGGL(k_row_join, dim3((unsigned)((rows + kRowThreads - 1) / kRowThreads)), dim3(kRowThreads), 0, st,
-                     ws.part, sp.parts, ws.label_logit, labels, V, rows, ws.row, logps);
+                     labels, V, rows, sp.parts, ws, logps);
   return hipGetLastError();
 }
 
@@ -247,22 +290,16 @@ hipError_t preference_as(const Preference& p, const RowStats& ws, hipStream_t st
   const int64_t rows = 2 * p.pairs * p.S;
   const RowSplit sp = row_split(rows, p.V);
   const E* logits = static_cast<const E*>(p.logits);
-  const Rows all{0, p.pairs * p.S, p.pairs * p.S};
-  hipLaunchKernelGGL((k_row_stats<E>), dim3((unsigned)(rows * sp.parts)), dim3(kRowThreads), 0, st, logits, p.labels,
-                     all, p.V, sp.parts, sp.len, ws.part, ws.row, ws.label_logit, p.logps);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = stats(logits, p.labels, p.ref_logps, rows, p.V, sp, p.logps, ws, st);
   if (e != hipSuccess) return e;
-  const PairArgs pa{p.labels, p.ref_logps, p.pairs, p.S, p.V, sp.parts, 0, p.beta, p.smoothing, p.grad_scale, ws,
-                    p.logps, p.log_ratios};
-  hipLaunchKernelGGL(k_pairs, dim3((unsigned)p.pairs), dim3(kPairThreads), 0, st, pa);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (!p.dlogits) {
-    hipLaunchKernelGGL(k_loss, dim3(1), dim3(kRowThreads), 0, st, ws.pair_loss, p.pairs, p.loss);
-    return hipGetLastError();
+  const PairArgs a{p.labels,    p.ref_logps,  p.pairs, p.S,     p.V,          sp.parts, p.beta,
+                   p.smoothing, p.grad_scale, ws,      p.logps, p.log_ratios, p.loss};
+  if (p.dlogits) {
+    hipLaunchKernelGGL((k_pref_grad<E>), dim3((unsigned)(rows * sp.parts)), dim3(kRowThreads), 0, st, logits,
+                       static_cast<E*>(p.dlogits), a, sp.len);
+  } else {
+    hipLaunchKernelGGL(k_pref_loss, dim3((unsigned)p.pairs), dim3(kRowThreads), 0, st, a);
   }
-  hipLaunchKernelGGL((k_pref_grad<E>), dim3((unsigned)(rows * sp.parts)), dim3(kRowThreads), 0, st, logits,
-                     static_cast<E*>(p.dlogits), p.labels, all, p.S, p.V, sp.parts, sp.len, ws.row, ws.coef,
-                     ws.pair_loss, p.pairs, p.loss);
   return hipGetLastError();
 }
 

@@ -52,15 +52,15 @@ struct RowSplit {
   int64_t parts, len;  // vocabulary parts of a row and their length
 };
 RowSplit row_split(int64_t rows, int64_t V);
-struct MaxSum {  // a maximum, and a sum of exponentials beside it (or its reciprocal)
+struct MaxSum {  // a maximum, and the sum of the exponentials of the differences to it
   float m, s;
 };
 struct RowStats {       // carved from the workspace
-  MaxSum* part;         // [rows][parts]: maximum and sum of exponentials of one part
-  MaxSum* row;           // [rows]: maximum and reciprocal sum
-  float* label_logit;   // [rows]
+  MaxSum* part;         // [rows][parts]
+  float* label_logit;   // [rows], for split rows
+  double* ratio;        // [rows] log ratios of whole rows (null without a loss)
   double* pair_loss;    // [pairs]
-  float* coef;          // [2 pairs]: d loss / d logp of a sequence's tokens
+  unsigned int* counter;
 };
 struct Preference {
   const void* logits;

@@ -56,20 +56,19 @@ int check_logits(const void* logits, const int64_t* labels, int64_t rows, int64_
 // The statistics of `rows` rows, and for the loss what belongs to `pairs` pairs.
 size_t carve_stats(void* ws, int64_t rows, int64_t V, int64_t pairs, RowStats* out) {
   const RowSplit sp = row_split(rows, V);
-  char* base = static_cast<char*>(ws);
   size_t off = kHead;
+  const auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return static_cast<char*>(ws) + at;
+  };
   RowStats s{};
-  s.row = reinterpret_cast<MaxSum*>(base + off);
-  off = align_up(off + sizeof(MaxSum) * (size_t)rows, 256);
-  s.pair_loss = reinterpret_cast<double*>(base + off);
-  off = align_up(off + sizeof(double) * (size_t)pairs, 256);
-  s.coef = reinterpret_cast<float*>(base + off);
-  off = align_up(off + sizeof(float) * 2 * (size_t)pairs, 256);
-  if (sp.parts > 1) {
-    s.part = reinterpret_cast<MaxSum*>(base + off);
-    off = align_up(off + sizeof(MaxSum) * (size_t)(rows * sp.parts), 256);
-    s.label_logit = reinterpret_cast<float*>(base + off);
-    off = align_up(off + sizeof(float) * (size_t)rows, 256);
+  s.counter = static_cast<unsigned int*>(ws);
+  s.part = reinterpret_cast<MaxSum*>(take(sizeof(MaxSum) * (size_t)(rows * sp.parts)));
+  if (sp.parts > 1) s.label_logit = reinterpret_cast<float*>(take(sizeof(float) * (size_t)rows));
+  if (pairs) {
+    if (sp.parts == 1) s.ratio = reinterpret_cast<double*>(take(sizeof(double) * (size_t)rows));
+    s.pair_loss = reinterpret_cast<double*>(take(sizeof(double) * (size_t)pairs));
   }
   if (out) *out = s;
   return off;

@@ -29,27 +29,60 @@ struct Raw8<float> {
   __device__ __forceinline__ float get(int i) const { return f[i]; }
 };
 
-// Elements [0, n) of p, n in 0..8, zeros beyond them.
-__device__ __forceinline__ void load8(Raw8<uint16_t>& r, const uint16_t* __restrict__ p, int n) {
-  if (n >= 8) {
-    const u32x4_e2 v = *reinterpret_cast<const u32x4_e2*>(p);
-    r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
-  } else {
+// The full vector at p.
+__device__ __forceinline__ void load_all8(Raw8<uint16_t>& r, const uint16_t* __restrict__ p) {
+  const u32x4_e2 v = *reinterpret_cast<const u32x4_e2*>(p);
+  r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+}
+__device__ __forceinline__ void load_all8(Raw8<float>& r, const float* __restrict__ p) {
+  const f32x4_e4 a = *reinterpret_cast<const f32x4_e4*>(p), b = *reinterpret_cast<const f32x4_e4*>(p + 4);
+  r.f[0] = a.x, r.f[1] = a.y, r.f[2] = a.z, r.f[3] = a.w;
+  r.f[4] = b.x, r.f[5] = b.y, r.f[6] = b.z, r.f[7] = b.w;
+}
+__device__ __forceinline__ void zero8(Raw8<uint16_t>& r) { r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0u; }
+__device__ __forceinline__ void zero8(Raw8<float>& r) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = 2 * i < n ? p[2 * i] : 0u, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0u;
-      r.w[i] = lo | (hi << 16);
-    }
+  for (int i = 0; i < 8; ++i) r.f[i] = 0.f;
+}
+// Drops the first s (1..7) elements and appends zeros.
+__device__ __forceinline__ void shift8(Raw8<uint16_t>& r, int s) {
+  if (s & 4) r.w[0] = r.w[2], r.w[1] = r.w[3], r.w[2] = r.w[3] = 0u;
+  if (s & 2) r.w[0] = r.w[1], r.w[1] = r.w[2], r.w[2] = r.w[3], r.w[3] = 0u;
+  if (s & 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = (r.w[i] >> 16) | (i < 3 ? r.w[i + 1] << 16 : 0u);
   }
 }
-__device__ __forceinline__ void load8(Raw8<float>& r, const float* __restrict__ p, int n) {
-  if (n >= 8) {
-    const f32x4_e4 a = *reinterpret_cast<const f32x4_e4*>(p), b = *reinterpret_cast<const f32x4_e4*>(p + 4);
-    r.f[0] = a.x, r.f[1] = a.y, r.f[2] = a.z, r.f[3] = a.w;
-    r.f[4] = b.x, r.f[5] = b.y, r.f[6] = b.z, r.f[7] = b.w;
-  } else {
+__device__ __forceinline__ void shift8(Raw8<float>& r, int s) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.f[i] = i < n ? p[i] : 0.f;
+  for (int k = 4; k >= 1; k >>= 1)
+    if (s & k) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.f[i] = i + k < 8 ? r.f[i + k] : 0.f;
+    }
+}
+__device__ __forceinline__ void set8(Raw8<uint16_t>& r, int i, uint16_t v) { r.w[i >> 1] |= (uint32_t)v << (16 * (i & 1)); }
+__device__ __forceinline__ void set8(Raw8<float>& r, int i, float v) { r.f[i] = v; }
+
+// Elements [0, n) of p, n in 0..8, zeros beyond them.  `wide`: the eight elements that end at
+// p + n belong to the same row; a short vector is then one load of those and a shift (a load
+// under a condition for each element would be waited for before the next one).
+template <class E>
+__device__ __forceinline__ void load8(Raw8<E>& r, const E* __restrict__ p, int n, bool wide) {
+  if (n >= 8) {
+    load_all8(r, p);
+  } else {
+    zero8(r);
+    if (n > 0) {
+      if (wide) {
+        load_all8(r, p + (n - 8));
+        shift8(r, 8 - n);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+          if (i < n) set8(r, i, p[i]);
+      }
+    }
   }
 }
 // The first n (0..8) of f, rounded to the element type (nearest, ties to even).
@@ -75,6 +108,63 @@ __device__ __forceinline__ void store8(float* __restrict__ p, const float f[8], 
       if (i < n) p[i] = f[i];
   }
 }
+
+// ---- a lane's eight columns of a row of d: [8 lane, 8 lane + 8), and where the row ends inside
+// them the row's last eight, of which the first 8 - n belong to the lane before (SHORT: d < 8,
+// element by element).  Every load is then a whole vector without a branch; what is not the
+// lane's own is dropped from sums and not stored.
+template <bool SHORT>
+struct Columns {
+  uint32_t at;  // first column of the vector
+  int n;        // the lane's own columns: the last n of the eight (SHORT: the first n)
+  __device__ __forceinline__ Columns(int d, uint32_t e) {
+    const int left = d - (int)e;
+    n = left < 0 ? 0 : (left > 8 ? 8 : left);
+    at = SHORT || n == 8 ? e : (uint32_t)(d - 8);
+  }
+  // The vector's place in a row; asked for anew at each use, so that no address of a later use
+  // is held in registers.
+  __device__ __forceinline__ uint32_t place() const {
+    uint32_t o = at;
+    asm volatile("" : "+v"(o));
+    return o;
+  }
+  template <class E>
+  __device__ __forceinline__ void load(Raw8<E>& r, const E* __restrict__ row) const {
+    if (SHORT) load8(r, row + at, n, false);
+    else load_all8(r, row + place());
+  }
+  // Zeros where the element is not the lane's own.
+  __device__ __forceinline__ void drop(Raw8<uint16_t>& r) const {
+    if (!SHORT && n < 8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (2 * i < 8 - n) r.w[i] &= 0xFFFF0000u;
+        if (2 * i + 1 < 8 - n) r.w[i] &= 0x0000FFFFu;
+      }
+    }
+  }
+  __device__ __forceinline__ void drop(Raw8<float>& r) const {
+    if (!SHORT && n < 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < 8 - n) r.f[i] = 0.f;
+    }
+  }
+  template <class E>
+  __device__ __forceinline__ void store(E* __restrict__ row, const float f[8]) const {
+    E* p = row + place();
+    if (SHORT || n == 8) {
+      store8(p, f, n);
+    } else if (n > 0) {
+#pragma unroll
+      for (int i = 1; i < 8; ++i)
+        if (i >= 8 - n) put(p + i, f[i]);
+    }
+  }
+  static __device__ __forceinline__ void put(float* p, float f) { *p = f; }
+  static __device__ __forceinline__ void put(uint16_t* p, float f) { *p = (uint16_t)(pack_bf16x2(f, 0.f) & 0xFFFFu); }
+};
 
 // Eight ones, for a weight that is not given.
 __device__ __forceinline__ void ones8(Raw8<uint16_t>& r) { r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0x3F803F80u; }
