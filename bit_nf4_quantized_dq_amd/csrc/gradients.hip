@@ -98,7 +98,7 @@ __device__ __forceinline__ void chunk_scale(const A* p, B* q, int32_t n, float c
       float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = r[v].get(i) * c;
-      store8(q + 8 * (v * kThreads + (int)threadIdx.x), f, 8);
+      stream8(q + 8 * (v * kThreads + (int)threadIdx.x), f);
     }
   } else {
     for (int e = 8 * (int)threadIdx.x; e < n; e += 8 * kThreads) {

@@ -16,81 +16,91 @@
 namespace qlora {
 namespace {
 
+// The gate of a row: none or one gate row for a run of rows (loaded where a run begins), or loaded
+// with each row.
+enum GateKind { kGateRuns, kGateRows };
+// Which outputs: any of them, or both large ones (stored without a branch); the latter also with
+// operands larger than the cache, which are read past it.
+enum Outputs { kAny, kBoth, kBothStream };
+
 template <class S>
 struct FwdArgs {
   const S* x;
-  const uint16_t *y, *w_post, *gate, *w_pre;
+  const uint16_t *y, *w_post, *gate, *w_pre;  // y is never null here: see y_bits
   S* x_out;
   uint16_t* h;
-  int64_t d, gate_rows;
+  int64_t M, d, gate_rows;
+  uint32_t y_bits;                // zeros where the block adds nothing
   float scale, eps, inv_d;
   int post;
 };
 
-// One workgroup of T threads per row, eight columns to a thread: every operand is read once and
-// kept in registers.
-template <class S, int T, bool SHORT>
+// One workgroup of T threads for every gridDim.x-th row, one row at a time and eight columns to
+// a thread: every operand is read once and kept in registers, the weights for all rows, and
+// the next row is loaded while this one's two sums cross the workgroup.  (Rows that are worked
+// on at the same time lie together in memory.)
+template <class S, int T, bool SHORT, GateKind KIND, Outputs OUT>
 __global__ __launch_bounds__(T) void k_norm_fwd(FwdArgs<S> a) {
-  __shared__ float lds[2][T / 64];
-  const int64_t row = blockIdx.x, d = a.d;
+  constexpr bool STREAM = OUT == kBothStream;
+  __shared__ float lds[2][2][T / 64];
+  const int64_t d = a.d;
+  const uint32_t rows = (uint32_t)a.M, run = (uint32_t)a.gate_rows;  // below 2^24
   const Columns<SHORT> col((int)d, 8 * threadIdx.x);
-  Raw8<S> x;
-  Raw8<uint16_t> y, w;
-  col.load(x, a.x + row * d);
-  col.drop(x);
-  if (a.y) {
-    col.load(y, a.y + row * d);
-    col.drop(y);
-  }
-  float r_y = 1.f;
-  if (a.post) {
+  Raw8<S> x, x_next;
+  Raw8<uint16_t> y, y_next, g, g_next, w_post, w_pre;
+  load_in<STREAM>(col, x, a.x + blockIdx.x * d);
+  load_in<STREAM>(col, y, a.y + blockIdx.x * d);
+  if (a.gate) col.load(g, a.gate + (KIND == kGateRows ? blockIdx.x / run * d : 0));
+  else ones8(g);
+  if (a.w_post) col.load(w_post, a.w_post);
+  else ones8(w_post);
+  if (a.w_pre) col.load(w_pre, a.w_pre);
+  else ones8(w_pre);
+  // all of it waited for here: a load that may still be under way where the loop is entered
+  // would make each row wait for the stores of the row before
+  opaque(w_post), opaque(w_pre), opaque(g), opaque(x), opaque(y);
+  bool odd = false;
+  for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, odd = !odd) {
+    // past the last row: once more the last one, so that the loop's loads need no condition
+    const uint32_t ahead = row + gridDim.x < rows ? row + gridDim.x : row;
+    load_in<STREAM>(col, x_next, a.x + ahead * d);
+    load_in<STREAM>(col, y_next, a.y + ahead * d);
+    if constexpr (KIND == kGateRows) col.load(g_next, a.gate + ahead / run * d);
+    and8(y, a.y_bits);
+    float r_y = 1.f;
+    if (a.post) {
+      const Raw8<uint16_t> own = col.own(y);
+      float s[1] = {0.f};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] = fmaf(own.get(i), own.get(i), s[0]);
+      block_sum<T>(s, lds[odd][0]);
+      r_y = 1.f / sqrtf(s[0] * a.inv_d + a.eps);
+    }
+    Raw8<float> xo;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) xo.f[i] = a.scale * x.get(i) + y.get(i) * r_y * w_post.get(i) * g.get(i);
+    const Raw8<float> own = col.own(xo);
     float s[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[0] = fmaf(y.get(i), y.get(i), s[0]);
-    block_sum<T>(s, lds[0]);
-    r_y = 1.f / sqrtf(s[0] * a.inv_d + a.eps);
-  }
-  float xo[8], s[1] = {0.f};
+    for (int i = 0; i < 8; ++i) s[0] = fmaf(own.f[i], own.f[i], s[0]);
+    // (also where h is not wanted: the exchange lies between the loads of a row and the stores
+    // that may replace it)
+    block_sum<T>(s, lds[odd][1]);
+    if (OUT != kAny || a.x_out) col.store(a.x_out + row * d, xo.f);
+    if (OUT != kAny || a.h) {
+      const float r_x = 1.f / sqrtf(s[0] * a.inv_d + a.eps);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) xo[i] = a.scale * x.get(i);
-  if (a.y) {
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = y.get(i) * r_y;
-    if (a.w_post) {
-      col.load(w, a.w_post);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] *= w.get(i);
+      for (int i = 0; i < 8; ++i) xo.f[i] *= r_x * w_pre.get(i);
+      col.store(a.h + row * d, xo.f);
     }
-    if (a.gate) {
-      col.load(w, a.gate + row / a.gate_rows * d);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] *= w.get(i);
-    }
-    // (a column that is not the lane's own gives 0 times a weight: an infinite one would reach
-    // the sum)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i >= 8 - col.n || SHORT) xo[i] += q[i];
+    x = x_next, y = y_next;
+    if constexpr (KIND == kGateRows) g = g_next;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s[0] = fmaf(xo[i], xo[i], s[0]);
-  if (a.x_out) col.store(a.x_out + row * d, xo);
-  if (!a.h) return;
-  block_sum<T>(s, lds[1]);
-  const float r_x = 1.f / sqrtf(s[0] * a.inv_d + a.eps);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) xo[i] *= r_x;
-  if (a.w_pre) {
-    col.load(w, a.w_pre);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) xo[i] *= w.get(i);
-  }
-  col.store(a.h + row * d, xo);
 }
 
 template <class S>
 struct BwdArgs {
+  // an operand that is not given points at another of the call (read, and made zeros by its bits)
   const S* x;  // x', as the forward stored it
   const uint16_t *y, *dh;
   const S* dx_out;
@@ -101,85 +111,93 @@ struct BwdArgs {
   float *p_pre, *p_post, *p_gate;  // [segment][d] FP32 partials, null where not wanted
   int64_t M, d, gate_rows;
   NormSegments seg;
+  uint32_t y_bits, h_bits, o_bits;  // y; x and dh; dx_out
   float scale, eps, inv_d;
   int post;
 };
 
-// What one row gives a lane's columns.  An operand that is not given is zeros, a weight or gate
-// that is not given is ones, so the arithmetic has no cases.
-template <class S, bool SHORT>
+// What one row gives a lane's columns.
+template <class S, bool SHORT, GateKind KIND, bool STREAM>
 struct RowVec {
   Raw8<S> x, dxo;
-  Raw8<uint16_t> y, dh;
+  Raw8<uint16_t> y, dh, g;
   __device__ __forceinline__ void load(const BwdArgs<S>& a, const Columns<SHORT>& col, int64_t at) {
-    if (a.dh) {
-      col.load(x, a.x + at);
-      col.load(dh, a.dh + at);
-    } else {
-      zero8(x), zero8(dh);
-    }
-    if (a.dx_out) col.load(dxo, a.dx_out + at);
-    else zero8(dxo);
-    if (a.y) col.load(y, a.y + at);
-    else zero8(y);
+    load_in<STREAM>(col, x, a.x + at);
+    load_in<STREAM>(col, dh, a.dh + at);
+    load_in<STREAM>(col, dxo, a.dx_out + at);
+    load_in<STREAM>(col, y, a.y + at);
+    if constexpr (KIND == kGateRows) col.load(g, a.gate + at);
   }
-  __device__ __forceinline__ void pack() { opaque(x), opaque(dxo), opaque(y), opaque(dh); }
+  __device__ __forceinline__ void pack() { opaque(x), opaque(dxo), opaque(y), opaque(dh), opaque(g); }
 };
 
 // One workgroup per segment of consecutive rows.  Its threads own columns, so the column sums
 // (weights, gate) stay in registers over the segment; the sums over a row are one exchange:
 // with q = g w_post y,  sum(b y) = sum(dx' q) + r_x sum(a q) - k sum(x' q),  k = r_x^3 mean(a x').
-template <class S, int T, bool SHORT>
+// An operand that is not given is zeros, a weight or gate that is not given is ones, so the
+// arithmetic has no cases.
+template <class S, int T, bool SHORT, GateKind KIND, Outputs OUT>
 __global__ __launch_bounds__(T, SHORT ? 1 : 4) void k_norm_bwd(BwdArgs<S> a) {
   __shared__ float lds[2][6 * (T / 64)];
   const int64_t d = a.d, seg = blockIdx.x;
-  // segments inside a gate row's rows (per_group of them), or of whole gate rows
-  int64_t r0 = seg * a.seg.rows, end = a.M, group;
+  // a segment of whole gate rows, or one of per_group segments that share a gate row's rows
+  int64_t r0 = seg * a.seg.rows, r1 = r0 + a.seg.rows < a.M ? r0 + a.seg.rows : a.M, group;
+  int64_t step = 1;
   if (a.seg.per_group) {
+    // (rows that are worked on at the same time lie together in memory)
     group = seg / a.seg.per_group;
-    r0 = group * a.gate_rows + (seg - group * a.seg.per_group) * a.seg.rows;
-    end = (group + 1) * a.gate_rows < a.M ? (group + 1) * a.gate_rows : a.M;
+    step = a.seg.per_group;
+    r0 = group * a.gate_rows + (seg - group * step);
+    r1 = (group + 1) * a.gate_rows < a.M ? (group + 1) * a.gate_rows : a.M;
   } else {
     group = r0 / a.gate_rows;
   }
-  const int64_t r1 = r0 + a.seg.rows < end ? r0 + a.seg.rows : end;
-  int64_t group_end = (group + 1) * a.gate_rows < a.M ? (group + 1) * a.gate_rows : a.M;
+  int64_t group_end = (group + 1) * a.gate_rows;
   const Columns<SHORT> col((int)d, 8 * threadIdx.x);
-  Raw8<uint16_t> w_pre, w_post, g;
-  if (a.w_pre) col.load(w_pre, a.w_pre);
-  else ones8(w_pre);
-  if (a.w_post) col.load(w_post, a.w_post);
-  else ones8(w_post);
-  const auto load_gate = [&] {
-    if (a.gate) col.load(g, a.gate + group * d);
-    else ones8(g);
-  };
   // s_tu: sum of t u over the rows of one gate row; times the gate it goes into dw_post, times
   // w_post it is the gate's gradient
   float s_pre[8], s_post[8], s_tu[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) s_pre[i] = s_post[i] = s_tu[i] = 0.f;
+  if (r0 >= r1) {  // a segment past the rows of a short last gate row
+    if (a.p_pre) col.store(a.p_pre + seg * d, s_pre);
+    if (a.p_post) col.store(a.p_post + seg * d, s_post);
+    if (a.p_gate) col.store(a.p_gate + seg * d, s_tu);
+    return;
+  }
+  RowVec<S, SHORT, KIND, OUT == kBothStream> r, next;
+  r.load(a, col, r0 * d);
+  Raw8<uint16_t> w_pre, w_post;
+  if (a.w_pre) col.load(w_pre, a.w_pre);
+  else ones8(w_pre);
+  if (a.w_post) col.load(w_post, a.w_post);
+  else ones8(w_post);
+  if constexpr (KIND == kGateRuns) {
+    if (a.gate) col.load(r.g, a.gate + group * d);
+    else ones8(r.g);
+  }
+  // all of it waited for here: a load that may still be under way where the loop is entered
+  // would make each row wait for the stores of the row before
+  opaque(w_pre), opaque(w_post), r.pack();
   const bool post = a.post != 0;
   const uint32_t post_bits = post ? 0xFFFFFFFFu : 0u;
-  // sixteen wavefronts to a compute unit have 128 registers each: with an FP32 stream the next
-  // row does not fit
-  constexpr bool kAhead = sizeof(S) == 2 && !SHORT;
-  RowVec<S, SHORT> r, next;
-  if (r0 < r1) r.load(a, col, r0 * d), load_gate();
-  else if (a.p_gate) col.store(a.p_gate + seg * d, s_tu);
-  for (int64_t row = r0; row < r1; ++row) {
+  const bool all = (a.y_bits & a.h_bits & a.o_bits) != 0u;
+  bool odd = false;
+  for (int64_t row = r0; row < r1; row += step, odd = !odd) {
     const int64_t at = row * d;
-    // the next row's loads run under this row's exchange
-    if (kAhead && row + 1 < r1) next.load(a, col, at + d);
+    // the next row's loads run under this row's exchange (past the last row: that one again)
+    next.load(a, col, (row + step < r1 ? row + step : row) * d);
     // what is held across the exchange stays packed (unpacked once for both uses it would take
     // 56 registers more)
-    opaque(w_pre), opaque(w_post), opaque(g), r.pack();
-    col.drop(r.x), col.drop(r.y);
+    opaque(w_pre), opaque(w_post), r.pack();
+    if (!all) and8(r.x, a.h_bits), and8(r.dh, a.h_bits), and8(r.dxo, a.o_bits), and8(r.y, a.y_bits);
+    const Raw8<S> x_own = col.own(r.x);
+    const Raw8<uint16_t> y_own = col.own(r.y);
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float xi = r.x.get(i), yi = r.y.get(i), ai = r.dh.get(i) * w_pre.get(i);
-      const float q = yi * w_post.get(i) * g.get(i);
+      const float xi = x_own.get(i), yi = y_own.get(i), ai = r.dh.get(i) * w_pre.get(i);
+      const float q = yi * w_post.get(i) * r.g.get(i);
       s[0] = fmaf(xi, xi, s[0]);
       s[1] = fmaf(ai, xi, s[1]);
       s[2] = fmaf(yi, yi, s[2]);
@@ -187,10 +205,10 @@ __global__ __launch_bounds__(T, SHORT ? 1 : 4) void k_norm_bwd(BwdArgs<S> a) {
       s[4] = fmaf(ai, q, s[4]);
       s[5] = fmaf(xi, q, s[5]);
     }
-    block_sum<T>(s, lds[(row - r0) & 1]);
-    opaque(w_pre), opaque(w_post), opaque(g), r.pack();
-    const float r_x = a.dh ? 1.f / sqrtf(s[0] * a.inv_d + a.eps) : 0.f;
-    const float k = a.dh ? r_x * r_x * r_x * (s[1] * a.inv_d) : 0.f;
+    block_sum<T>(s, lds[odd]);
+    opaque(w_pre), opaque(w_post), r.pack();
+    const float r_x = a.h_bits ? 1.f / sqrtf(s[0] * a.inv_d + a.eps) : 0.f;
+    const float k = a.h_bits ? r_x * r_x * r_x * (s[1] * a.inv_d) : 0.f;
     const float r_y = post ? 1.f / sqrtf(s[2] * a.inv_d + a.eps) : 1.f;
     const float c = post ? r_y * r_y * r_y * ((s[3] + r_x * s[4] - k * s[5]) * a.inv_d) : 0.f;
     float t[8], o[8];
@@ -201,16 +219,19 @@ __global__ __launch_bounds__(T, SHORT ? 1 : 4) void k_norm_bwd(BwdArgs<S> a) {
       s_pre[i] = fmaf(dhi, xi * r_x, s_pre[i]);
       o[i] = a.scale * t[i];
     }
-    if (a.dx) col.store(a.dx + at, o);
+    if (OUT != kAny || a.dx) col.store(a.dx + at, o);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float yi = r.y.get(i);
       s_tu[i] = fmaf(t[i], yi * r_y, s_tu[i]);
-      o[i] = r_y * (t[i] * g.get(i) * w_post.get(i)) - __uint_as_float(__float_as_uint(yi) & post_bits) * c;
+      o[i] = r_y * (t[i] * r.g.get(i) * w_post.get(i)) - __uint_as_float(__float_as_uint(yi) & post_bits) * c;
     }
-    if (a.dy) col.store(a.dy + at, o);
-    if (row + 1 == group_end || row + 1 == r1) {
+    if (OUT != kAny || a.dy) col.store(a.dy + at, o);
+    const Raw8<uint16_t> g = r.g;
+    r = next;
+    if constexpr (KIND == kGateRuns) r.g = g;
+    if (KIND == kGateRows || row + 1 == group_end || row + step >= r1) {
       float dg[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -220,14 +241,14 @@ __global__ __launch_bounds__(T, SHORT ? 1 : 4) void k_norm_bwd(BwdArgs<S> a) {
       }
       if (a.dgate) col.store(a.dgate + group * d, dg);
       if (a.p_gate) col.store(a.p_gate + seg * d, dg);
-      if (row + 1 < r1) {
-        ++group;
-        group_end = group_end + a.gate_rows < a.M ? group_end + a.gate_rows : a.M;
-        load_gate();
+      if (row + step < r1) {
+        ++group, group_end += a.gate_rows;
+        if constexpr (KIND == kGateRuns) {
+          col.load(r.g, a.gate + group * d);
+          opaque(r.g);  // waited for here, not in every row
+        }
       }
     }
-    if (kAhead) r = next;
-    else if (row + 1 < r1) r.load(a, col, at + d);
   }
   if (a.p_pre) col.store(a.p_pre + seg * d, s_pre);
   if (a.p_post) col.store(a.p_post + seg * d, s_post);
@@ -269,23 +290,56 @@ __global__ __launch_bounds__(kColThreads) void k_norm_cols(const float* __restri
   }
 }
 
+// Whether a call's operands, of so many bytes an element, are more than the cache keeps.
+bool stream(int64_t M, int64_t d, int64_t bytes) { return M * d * bytes > (int64_t)128 << 20; }
+
 template <class S, int T, bool SHORT = false>
 hipError_t fwd_as(const NormFwd& p, hipStream_t st) {
-  FwdArgs<S> a{static_cast<const S*>(p.x), p.y, p.w_post, p.gate, p.w_pre, static_cast<S*>(p.x_out), p.h, p.d,
-               p.gate_rows, p.scale, p.eps, (float)(1.0 / (double)p.d), p.post};
-  hipLaunchKernelGGL((k_norm_fwd<S, T, SHORT>), dim3((unsigned)p.M), dim3(T), 0, st, a);
+  // all 2048 threads of each of the 256 compute units at once
+  const unsigned grid = (unsigned)(p.M < 256 * 2048 / T ? p.M : 256 * 2048 / T);
+  const FwdArgs<S> a{static_cast<const S*>(p.x),
+                     p.y ? p.y : static_cast<const uint16_t*>(p.x),
+                     p.w_post,
+                     p.gate,
+                     p.w_pre,
+                     static_cast<S*>(p.x_out),
+                     p.h,
+                     p.M,
+                     p.d,
+                     p.gate && p.gate_rows < p.M ? p.gate_rows : p.M,
+                     p.y ? 0xFFFFFFFFu : 0u,
+                     p.scale,
+                     p.eps,
+                     (float)(1.0 / (double)p.d),
+                     p.post};
+  const Outputs out = !a.x_out || !a.h ? kAny : (stream(p.M, p.d, 2 * sizeof(S) + 4) ? kBothStream : kBoth);
+  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(T), 0, st, a); };
+  if (a.gate && a.gate_rows < a.M) {
+    if (out == kAny) launch(k_norm_fwd<S, T, SHORT, kGateRows, kAny>);
+    else if (out == kBoth) launch(k_norm_fwd<S, T, SHORT, kGateRows, kBoth>);
+    else launch(k_norm_fwd<S, T, SHORT, kGateRows, kBothStream>);
+  } else {
+    if (out == kAny) launch(k_norm_fwd<S, T, SHORT, kGateRuns, kAny>);
+    else if (out == kBoth) launch(k_norm_fwd<S, T, SHORT, kGateRuns, kBoth>);
+    else launch(k_norm_fwd<S, T, SHORT, kGateRuns, kBothStream>);
+  }
   return hipGetLastError();
 }
 
-template <class S>
-hipError_t fwd(const NormFwd& p, hipStream_t st) {
-  const int64_t n8 = (p.d + 7) / 8;
-  if (p.d < 8) return fwd_as<S, 64, true>(p, st);
-  if (n8 <= 64) return fwd_as<S, 64>(p, st);
-  if (n8 <= 128) return fwd_as<S, 128>(p, st);
-  if (n8 <= 256) return fwd_as<S, 256>(p, st);
-  if (n8 <= 512) return fwd_as<S, 512>(p, st);
-  return fwd_as<S, 1024>(p, st);
+template <class S, int T, bool SHORT>
+hipError_t bwd_rows(const BwdArgs<S>& a, GateKind kind, hipStream_t st) {
+  const Outputs out = !a.dx || !a.dy ? kAny : (stream(a.M, a.d, 3 * sizeof(S) + 6) ? kBothStream : kBoth);
+  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)a.seg.count), dim3(T), 0, st, a); };
+  if (kind == kGateRows) {
+    if (out == kAny) launch(k_norm_bwd<S, T, SHORT, kGateRows, kAny>);
+    else if (out == kBoth) launch(k_norm_bwd<S, T, SHORT, kGateRows, kBoth>);
+    else launch(k_norm_bwd<S, T, SHORT, kGateRows, kBothStream>);
+  } else {
+    if (out == kAny) launch(k_norm_bwd<S, T, SHORT, kGateRuns, kAny>);
+    else if (out == kBoth) launch(k_norm_bwd<S, T, SHORT, kGateRuns, kBoth>);
+    else launch(k_norm_bwd<S, T, SHORT, kGateRuns, kBothStream>);
+  }
+  return hipGetLastError();
 }
 
 template <class S, int T, bool SHORT = false>
@@ -293,18 +347,22 @@ hipError_t bwd_as(const NormBwd& p, hipStream_t st) {
   const NormSegments seg = norm_segments(p.M, p.d, p.gate ? p.gate_rows : 0);
   const int64_t per = seg.count * p.d;
   float* part = p.part;
+  const S *x = static_cast<const S*>(p.x), *o = static_cast<const S*>(p.dx_out);
+  // any tensor of the call with as many elements of the type or wider
+  const S* any = x && p.dh ? x : o;
+  const uint16_t* any16 = p.dh ? p.dh : reinterpret_cast<const uint16_t*>(any);
   BwdArgs<S> a{};
-  a.x = static_cast<const S*>(p.x), a.y = p.y, a.dh = p.dh, a.dx_out = static_cast<const S*>(p.dx_out);
+  a.x = p.dh ? x : any, a.dh = p.dh ? p.dh : any16, a.dx_out = o ? o : any, a.y = p.y ? p.y : any16;
+  a.h_bits = p.dh ? ~0u : 0u, a.o_bits = o ? ~0u : 0u, a.y_bits = p.y ? ~0u : 0u;
   a.w_post = p.w_post, a.gate = p.gate, a.w_pre = p.w_pre;
   a.dx = static_cast<S*>(p.dx), a.dy = p.dy;
+  if (!seg.per_group) a.dgate = p.dgate;
   a.M = p.M, a.d = p.d, a.gate_rows = p.gate ? p.gate_rows : p.M, a.seg = seg;
   a.scale = p.scale, a.eps = p.eps, a.inv_d = (float)(1.0 / (double)p.d), a.post = p.post;
-  if (!seg.per_group) a.dgate = p.dgate;
   if (p.dw_pre) a.p_pre = part, part += per;
   if (p.dw_post) a.p_post = part, part += per;
   if (p.dgate && seg.per_group) a.p_gate = part;
-  hipLaunchKernelGGL((k_norm_bwd<S, T, SHORT>), dim3((unsigned)seg.count), dim3(T), 0, st, a);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = bwd_rows<S, T, SHORT>(a, p.gate && p.gate_rows == 1 ? kGateRows : kGateRuns, st);
   if (e != hipSuccess) return e;
   const int64_t groups = a.p_gate ? (p.M + p.gate_rows - 1) / p.gate_rows : 0;
   const int64_t job0 = a.p_pre ? 0 : (a.p_post ? 1 : 2), jobs = (groups ? 2 + groups : (a.p_post ? 2 : 1)) - job0;
@@ -315,14 +373,23 @@ hipError_t bwd_as(const NormBwd& p, hipStream_t st) {
   return hipGetLastError();
 }
 
+// The threads of a row: one for each eight columns.
+template <class S>
+hipError_t fwd(const NormFwd& p, hipStream_t st) {
+  if (p.d < 8) return fwd_as<S, 64, true>(p, st);
+  if (p.d <= 512) return fwd_as<S, 64>(p, st);
+  if (p.d <= 1024) return fwd_as<S, 128>(p, st);
+  if (p.d <= 2048) return fwd_as<S, 256>(p, st);
+  if (p.d <= 4096) return fwd_as<S, 512>(p, st);
+  return fwd_as<S, 1024>(p, st);
+}
 template <class S>
 hipError_t bwd(const NormBwd& p, hipStream_t st) {
-  const int64_t n8 = (p.d + 7) / 8;
   if (p.d < 8) return bwd_as<S, 64, true>(p, st);
-  if (n8 <= 64) return bwd_as<S, 64>(p, st);
-  if (n8 <= 128) return bwd_as<S, 128>(p, st);
-  if (n8 <= 256) return bwd_as<S, 256>(p, st);
-  if (n8 <= 512) return bwd_as<S, 512>(p, st);
+  if (p.d <= 512) return bwd_as<S, 64>(p, st);
+  if (p.d <= 1024) return bwd_as<S, 128>(p, st);
+  if (p.d <= 2048) return bwd_as<S, 256>(p, st);
+  if (p.d <= 4096) return bwd_as<S, 512>(p, st);
   return bwd_as<S, 1024>(p, st);
 }
 

@@ -239,13 +239,14 @@ __global__ __launch_bounds__(kRowThreads) void k_pref_grad(const E* logits, E* d
       for (int j = 0; j < 8; ++j)
         if (j == j0) f[j] += c;
     }
-    store8(out + at, f, n);
+    if (n == 8) stream8(out + at, f);
+    else store8(out + at, f, n);
   };
   const int64_t full = (v1 - v0) >> 3;
   const int tail = (int)((v1 - v0) & 7);
   if (!counted) {
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int64_t i = threadIdx.x; i < full; i += kRowThreads) store8(out + 8 * i, zero, 8);
+    for (int64_t i = threadIdx.x; i < full; i += kRowThreads) stream8(out + 8 * i, zero);
     if (tail && threadIdx.x == 0) store8(out + 8 * full, zero, tail);
     return;
   }

@@ -38,8 +38,9 @@ struct NormBwd {
   int f32, post;
 };
 // The backward's rows in `count` segments of at most `rows` rows, one workgroup each.  A gate
-// row's rows are either split into per_group segments (per_group > 0) or lie whole in one
-// segment (per_group == 0: rows is a multiple of gate_rows; always so without a gate).
+// row's rows (without a gate all rows) are either split into per_group segments, each taking
+// every per_group-th row (per_group > 0), or lie whole in one segment of consecutive rows
+// (per_group == 0: rows is a multiple of gate_rows).
 struct NormSegments {
   int64_t rows, count, per_group;
 };

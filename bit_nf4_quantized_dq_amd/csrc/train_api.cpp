@@ -103,7 +103,7 @@ NormSegments norm_segments(int64_t M, int64_t d, int64_t gate_rows) {
   const int64_t threads = std::max<int64_t>(64, std::min<int64_t>(1024, (d + 7) / 8));
   int64_t rows = std::max<int64_t>(4, (M * threads + 256 * 1024 - 1) / (256 * 1024));
   NormSegments s{};
-  gate_rows = std::min(gate_rows, M);
+  gate_rows = gate_rows ? std::min(gate_rows, M) : M;
   if (gate_rows <= rows) {
     if (gate_rows > 1) rows = rows / gate_rows * gate_rows;
     s.rows = rows;

@@ -39,6 +39,17 @@ __device__ __forceinline__ void load_all8(Raw8<float>& r, const float* __restric
   r.f[0] = a.x, r.f[1] = a.y, r.f[2] = a.z, r.f[3] = a.w;
   r.f[4] = b.x, r.f[5] = b.y, r.f[6] = b.z, r.f[7] = b.w;
 }
+// The same for an operand that is not read again soon.
+__device__ __forceinline__ void stream_all8(Raw8<uint16_t>& r, const uint16_t* __restrict__ p) {
+  const u32x4_e2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_e2*>(p));
+  r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+}
+__device__ __forceinline__ void stream_all8(Raw8<float>& r, const float* __restrict__ p) {
+  const f32x4_e4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4_e4*>(p));
+  const f32x4_e4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4_e4*>(p + 4));
+  r.f[0] = a.x, r.f[1] = a.y, r.f[2] = a.z, r.f[3] = a.w;
+  r.f[4] = b.x, r.f[5] = b.y, r.f[6] = b.z, r.f[7] = b.w;
+}
 __device__ __forceinline__ void zero8(Raw8<uint16_t>& r) { r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0u; }
 __device__ __forceinline__ void zero8(Raw8<float>& r) {
 #pragma unroll
@@ -109,10 +120,24 @@ __device__ __forceinline__ void store8(float* __restrict__ p, const float f[8], 
   }
 }
 
-// ---- a lane's eight columns of a row of d: [8 lane, 8 lane + 8), and where the row ends inside
-// them the row's last eight, of which the first 8 - n belong to the lane before (SHORT: d < 8,
-// element by element).  Every load is then a whole vector without a branch; what is not the
-// lane's own is dropped from sums and not stored.
+// store8 for results that are not read again soon.
+__device__ __forceinline__ void stream8(uint16_t* __restrict__ p, const float f[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  __builtin_nontemporal_store(u32x4_e2{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4_e2*>(p));
+}
+__device__ __forceinline__ void stream8(float* __restrict__ p, const float f[8]) {
+  __builtin_nontemporal_store(f32x4_e4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f32x4_e4*>(p));
+  __builtin_nontemporal_store(f32x4_e4{f[4], f[5], f[6], f[7]}, reinterpret_cast<f32x4_e4*>(p + 4));
+}
+
+// ---- a lane's eight columns of a row of d >= 8: [8 lane, 8 lane + 8), and from the row's end on
+// the row's last eight columns.  Every load and store is then a whole vector of the row without
+// a branch, which lets the compiler count what is in flight (behind a branch it waits for all
+// of it).  Columns that several lanes hold count once in sums (own()); each of the lanes stores
+// them, with the same bits.
+// SHORT: d < 8, in the first lane, element by element.
 template <bool SHORT>
 struct Columns {
   uint32_t at;  // first column of the vector
@@ -131,11 +156,15 @@ struct Columns {
   }
   template <class E>
   __device__ __forceinline__ void load(Raw8<E>& r, const E* __restrict__ row) const {
-    if (SHORT) load8(r, row + at, n, false);
+    if constexpr (SHORT) load8(r, row + at, n, false);
     else load_all8(r, row + place());
   }
-  // Zeros where the element is not the lane's own.
-  __device__ __forceinline__ void drop(Raw8<uint16_t>& r) const {
+  template <class E>
+  __device__ __forceinline__ void store(E* __restrict__ row, const float f[8]) const {
+    store8(row + place(), f, SHORT ? n : 8);
+  }
+  // Zeros where the column is another lane's.
+  __device__ __forceinline__ Raw8<uint16_t> own(Raw8<uint16_t> r) const {
     if (!SHORT && n < 8) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -143,28 +172,33 @@ struct Columns {
         if (2 * i + 1 < 8 - n) r.w[i] &= 0x0000FFFFu;
       }
     }
+    return r;
   }
-  __device__ __forceinline__ void drop(Raw8<float>& r) const {
+  __device__ __forceinline__ Raw8<float> own(Raw8<float> r) const {
     if (!SHORT && n < 8) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < 8 - n) r.f[i] = 0.f;
     }
+    return r;
   }
-  template <class E>
-  __device__ __forceinline__ void store(E* __restrict__ row, const float f[8]) const {
-    E* p = row + place();
-    if (SHORT || n == 8) {
-      store8(p, f, n);
-    } else if (n > 0) {
-#pragma unroll
-      for (int i = 1; i < 8; ++i)
-        if (i >= 8 - n) put(p + i, f[i]);
-    }
-  }
-  static __device__ __forceinline__ void put(float* p, float f) { *p = f; }
-  static __device__ __forceinline__ void put(uint16_t* p, float f) { *p = (uint16_t)(pack_bf16x2(f, 0.f) & 0xFFFFu); }
 };
+
+// The columns of an operand that (STREAM) is not read again soon.
+template <bool STREAM, bool SHORT, class E>
+__device__ __forceinline__ void load_in(const Columns<SHORT>& col, Raw8<E>& r, const E* __restrict__ row) {
+  if constexpr (SHORT || !STREAM) col.load(r, row);
+  else stream_all8(r, row + col.place());
+}
+
+__device__ __forceinline__ void and8(Raw8<uint16_t>& r, uint32_t bits) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.w[i] &= bits;
+}
+__device__ __forceinline__ void and8(Raw8<float>& r, uint32_t bits) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.f[i] = __uint_as_float(__float_as_uint(r.f[i]) & bits);
+}
 
 // Eight ones, for a weight that is not given.
 __device__ __forceinline__ void ones8(Raw8<uint16_t>& r) { r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0x3F803F80u; }
@@ -174,7 +208,10 @@ __device__ __forceinline__ void ones8(Raw8<uint16_t>& r) { r.w[0] = r.w[1] = r.w
 __device__ __forceinline__ void opaque(Raw8<uint16_t>& r) {
   asm volatile("" : "+v"(r.w[0]), "+v"(r.w[1]), "+v"(r.w[2]), "+v"(r.w[3]));
 }
-__device__ __forceinline__ void opaque(Raw8<float>&) {}
+__device__ __forceinline__ void opaque(Raw8<float>& r) {
+  asm volatile("" : "+v"(r.f[0]), "+v"(r.f[1]), "+v"(r.f[2]), "+v"(r.f[3]), "+v"(r.f[4]), "+v"(r.f[5]), "+v"(r.f[6]),
+               "+v"(r.f[7]));
+}
 
 __device__ __forceinline__ float to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ float to_f32(float f) { return f; }
