@@ -34,6 +34,22 @@ __device__ __forceinline__ void adamw1(float& th, float& m, float& v, float g, c
   th = __fsub_rn(th, __fdiv_rn(__fmul_rn(a.step_size, m), den));
 }
 
+// Four values of a state.  kPast: read and written past the cache, which then still holds the
+// gradients that the norm has just read.
+template <bool kPast>
+__device__ __forceinline__ float4 state_load(const float* p, int64_t i) {
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  if (!kPast) return reinterpret_cast<const float4*>(p)[i];
+  const f4 v = __builtin_nontemporal_load(reinterpret_cast<const f4*>(p) + i);
+  return make_float4(v.x, v.y, v.z, v.w);
+}
+template <bool kPast>
+__device__ __forceinline__ void state_store(float* p, int64_t i, const float4& v) {
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  if (kPast) __builtin_nontemporal_store(f4{v.x, v.y, v.z, v.w}, reinterpret_cast<f4*>(p) + i);
+  else reinterpret_cast<float4*>(p)[i] = v;
+}
+
 template <bool kClip>
 __device__ __forceinline__ float clipped(float g, float c) {
   return kClip ? __fmul_rn(g, c) : g;
@@ -52,17 +68,17 @@ __global__ __launch_bounds__(kThreads) void k_adamw(float* __restrict__ master, 
   const int64_t n4 = n >> 2;
   const int64_t stride = (int64_t)gridDim.x * kThreads;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n4; i += stride) {
-    float4 th = reinterpret_cast<const float4*>(master)[i];
-    float4 m = reinterpret_cast<const float4*>(mom1)[i];
-    float4 v = reinterpret_cast<const float4*>(mom2)[i];
+    float4 th = state_load<kClip>(master, i);
+    float4 m = state_load<kClip>(mom1, i);
+    float4 v = state_load<kClip>(mom2, i);
     const uint2 gb = reinterpret_cast<const uint2*>(grad)[i];
     adamw1(th.x, m.x, v.x, clipped<kClip>(bf16lo_to_f32(gb.x), c), a);
     adamw1(th.y, m.y, v.y, clipped<kClip>(bf16hi_to_f32(gb.x), c), a);
     adamw1(th.z, m.z, v.z, clipped<kClip>(bf16lo_to_f32(gb.y), c), a);
     adamw1(th.w, m.w, v.w, clipped<kClip>(bf16hi_to_f32(gb.y), c), a);
-    reinterpret_cast<float4*>(master)[i] = th;
-    reinterpret_cast<float4*>(mom1)[i] = m;
-    reinterpret_cast<float4*>(mom2)[i] = v;
+    state_store<kClip>(master, i, th);
+    state_store<kClip>(mom1, i, m);
+    state_store<kClip>(mom2, i, v);
     if (param) reinterpret_cast<uint2*>(param)[i] = make_uint2(pack_bf16x2(th.x, th.y), pack_bf16x2(th.z, th.w));
   }
   // tail: the last n % 4 parameters, one per lane of the first workgroup

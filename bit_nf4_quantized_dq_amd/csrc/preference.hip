@@ -5,6 +5,8 @@
 //   loss = mean_p ((1 - e) softplus(-z_p) + e softplus(z_p))
 //   dloss/dx_t[v] = c_i ([v = label_t] - exp(x_t[v] - lse_t)),
 //   c_chosen = -c_rejected = grad_scale (beta / P) (sigmoid(z_p) + e - 1)
+#include <type_traits>
+
 #include "qlora_train_host.h"
 #include "train_device.h"
 
@@ -33,12 +35,12 @@ __device__ __forceinline__ double label_logp(float xl, float m, float s) {
 
 // One workgroup per row and part: one pass with the running maximum and sum of each thread.  A
 // whole row (parts == 1) is finished here, a split one by its readers.
-template <class E>
-__global__ __launch_bounds__(kRowThreads) void k_row_stats(const E* __restrict__ logits,
+template <class E, int T>
+__global__ __launch_bounds__(T) void k_row_stats(const E* __restrict__ logits,
                                                            const int64_t* __restrict__ labels,
                                                            const float* __restrict__ ref, int64_t V, int64_t parts,
                                                            int64_t len, RowStats ws, float* __restrict__ logps) {
-  __shared__ float lm[kRowThreads / 64], ls[kRowThreads / 64];
+  __shared__ float lm[T / 64], ls[T / 64];
   const int64_t row = blockIdx.x / parts, p = blockIdx.x - row * parts;
   const int64_t label = labels[row];
   if (label < 0 || label >= V) {
@@ -65,16 +67,56 @@ __global__ __launch_bounds__(kRowThreads) void k_row_stats(const E* __restrict__
     for (int j = 0; j < 8; ++j) s += exp2_hw((f[j] - base) * kLog2e);
     m = t;
   };
-  const int64_t full = (v1 - v0) >> 3;
+  const int32_t full = (int32_t)((v1 - v0) >> 3), batches = full / (kUnroll * T);
   const E* xp = x + v0;
-  for (int64_t i = threadIdx.x; i < full; i += kUnroll * kRowThreads) {
+  // Batches of 32 elements a thread.  The exponentials are 2^(x log2 e - n) with a whole number n
+  // just above the maximum's x log2 e: the product is not rounded before n leaves it, so this
+  // is one operation for the difference and the factor, and changes of n scale exactly.  n
+  // stays above kLow: elements below it (masked by -inf or the type's lowest value) add zero.
+  constexpr float kLow = -1.5e30f;
+  float n = kLow;
+  for (int32_t i = 0; i < batches; ++i) {
     Raw8<E> r[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (i + u * kRowThreads < full) load_all8(r[u], xp + 8 * (i + u * kRowThreads));
+    for (int u = 0; u < kUnroll; ++u) load_all8(r[u], xp + 8 * ((i * kUnroll + u) * T + (int)threadIdx.x));
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (i + u * kRowThreads < full) take(r[u], 8);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, r[u].get(j));
+    const float to = ceilf(fmaxf(m * kLog2e, kLow));
+    s *= exp2_hw(n - to);
+    n = to;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += exp2_hw(fmaf(r[u].get(j), kLog2e, -n));
+  }
+  // from n to the maximum itself; a thread that met nothing above kLow keeps only a NaN
+  constexpr float kHuge = 1e30f;
+  if (batches) s = fabsf(m) < kHuge ? s * exp2_hw(fmaf(-m, kLog2e, n)) : (s != s ? s : 0.f);
+  // A maximum too large for that (infinite, or of a row that is masked throughout): the batches
+  // once more, each difference before its factor.
+  if (__syncthreads_or(batches && !(fabsf(m) < kHuge))) {
+    float top = m;
+#pragma unroll
+    for (int k = 32; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor(top, k, 64));
+    if ((threadIdx.x & 63) == 0) lm[threadIdx.x >> 6] = top;
+    __syncthreads();
+    for (int w = 0; w < T / 64; ++w) top = fmaxf(top, lm[w]);
+    __syncthreads();
+    if (!(fabsf(top) < kHuge)) {
+      m = -INFINITY, s = 0.f;
+      for (int32_t i = threadIdx.x; i < batches * kUnroll * T; i += T) {
+        Raw8<E> r;
+        load_all8(r, xp + 8 * i);
+        take(r, 8);
+      }
+    }
+  }
+  for (int32_t i = batches * kUnroll * T + (int)threadIdx.x; i < full; i += T) {
+    Raw8<E> r;
+    load_all8(r, xp + 8 * i);
+    take(r, 8);
   }
   if (const int tail = (int)((v1 - v0) & 7); tail && threadIdx.x == 0) {
     Raw8<E> r;
@@ -87,7 +129,7 @@ __global__ __launch_bounds__(kRowThreads) void k_row_stats(const E* __restrict__
   __syncthreads();
   if (threadIdx.x == 0) {
     m = lm[0], s = ls[0];
-    for (int w = 1; w < kRowThreads / 64; ++w) merge(m, s, lm[w], ls[w]);
+    for (int w = 1; w < T / 64; ++w) merge(m, s, lm[w], ls[w]);
     ws.part[row * parts + p] = MaxSum{m, s};
     if (parts == 1) {
       const double lp = label_logp(xl, m, s);
@@ -127,13 +169,14 @@ struct PairArgs {
   float *logps, *log_ratios, *loss;
 };
 struct PairLds {
-  double sum[2][kRowThreads / 64];
-  double mean[kRowThreads / 64];
+  double sum[2][16];  // one for each wavefront of a workgroup
+  double mean[16];
   bool last;
 };
 
 // The pair's log ratios, summed in FP64 in one order by whichever workgroup asks: for whole rows
 // two short sums of what the first pass left, for split rows after joining their parts.
+template <int T>
 __device__ __forceinline__ void pair_sums(const PairArgs& a, int64_t pair, bool write, PairLds& lds, double out[2]) {
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
@@ -141,9 +184,9 @@ __device__ __forceinline__ void pair_sums(const PairArgs& a, int64_t pair, bool 
     double sum = 0.0;
     if (a.parts == 1) {
 #pragma unroll 4
-      for (int64_t t = threadIdx.x; t < a.S; t += kRowThreads) sum += a.ws.ratio[r0 + t];
+      for (int64_t t = threadIdx.x; t < a.S; t += T) sum += a.ws.ratio[r0 + t];
     } else {
-      for (int64_t t = threadIdx.x; t < a.S; t += kRowThreads) {
+      for (int64_t t = threadIdx.x; t < a.S; t += T) {
         const int64_t row = r0 + t, label = a.labels[row];
         double lp = 0.0;
         if (label >= 0 && label < a.V) {
@@ -154,7 +197,7 @@ __device__ __forceinline__ void pair_sums(const PairArgs& a, int64_t pair, bool 
         if (write) a.logps[row] = (float)lp;
       }
     }
-    out[side] = block_sum_f64<kRowThreads>(sum, lds.sum[side]);
+    out[side] = block_sum_f64<T>(sum, lds.sum[side]);
   }
 }
 
@@ -168,6 +211,7 @@ __device__ __forceinline__ float pair_slope(const PairArgs& a, const double d[2]
 // One workgroup of each pair writes its log ratios and its loss; the last of them to arrive adds
 // the losses in the pairs' order.  The losses travel by system-scope (cache-bypassing) stores
 // and loads, and a store has completed before its workgroup is counted.
+template <int T>
 __device__ void finish_pair(const PairArgs& a, int64_t pair, const double d[2], PairLds& lds) {
   if (threadIdx.x == 0) {
     a.log_ratios[pair] = (float)d[0];
@@ -189,9 +233,9 @@ __device__ void finish_pair(const PairArgs& a, int64_t pair, const double d[2], 
   __syncthreads();
   if (!lds.last) return;
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < a.pairs; i += kRowThreads)
+  for (int64_t i = threadIdx.x; i < a.pairs; i += T)
     s += __hip_atomic_load(a.ws.pair_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-  s = block_sum_f64<kRowThreads>(s, lds.mean);
+  s = block_sum_f64<T>(s, lds.mean);
   if (threadIdx.x == 0) *a.loss = (float)(s / (double)a.pairs);
 }
 
@@ -199,15 +243,15 @@ __device__ void finish_pair(const PairArgs& a, int64_t pair, const double d[2], 
 __global__ __launch_bounds__(kRowThreads) void k_pref_loss(PairArgs a) {
   __shared__ PairLds lds;
   double d[2];
-  pair_sums(a, blockIdx.x, true, lds, d);
-  finish_pair(a, blockIdx.x, d, lds);
+  pair_sums<kRowThreads>(a, blockIdx.x, true, lds, d);
+  finish_pair<kRowThreads>(a, blockIdx.x, d, lds);
 }
 
 // The gradient: one workgroup per row and part, each element read and written once.  Each takes
 // its pair's slope from the pair's sums itself, so nothing runs between the two passes.  Rows
 // go from the last to the first: the end of what the first pass read is still in the cache.
-template <class E>
-__global__ __launch_bounds__(kRowThreads) void k_pref_grad(const E* logits, E* dlogits, PairArgs a, int64_t len) {
+template <class E, int T>
+__global__ __launch_bounds__(T) void k_pref_grad(const E* logits, E* dlogits, PairArgs a, int64_t len) {
   __shared__ PairLds lds;
   const int64_t block = (int64_t)gridDim.x - 1 - blockIdx.x;
   const int64_t row = block / a.parts, p = block - row * a.parts;
@@ -216,8 +260,8 @@ __global__ __launch_bounds__(kRowThreads) void k_pref_grad(const E* logits, E* d
   const bool counted = label >= 0 && label < V;
   const bool lead = p == 0 && seq < a.pairs && row == seq * a.S;  // this pair's workgroup
   double d[2];
-  if (counted || lead) pair_sums(a, pair, lead, lds, d);
-  if (lead) finish_pair(a, pair, d, lds);
+  if (counted || lead) pair_sums<T>(a, pair, lead, lds, d);
+  if (lead) finish_pair<T>(a, pair, d, lds);
   float c = 0.f, scale = 0.f, m = 0.f;
   if (counted) {
     c = pair_slope(a, d);
@@ -246,18 +290,18 @@ __global__ __launch_bounds__(kRowThreads) void k_pref_grad(const E* logits, E* d
   const int tail = (int)((v1 - v0) & 7);
   if (!counted) {
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int64_t i = threadIdx.x; i < full; i += kRowThreads) stream8(out + 8 * i, zero);
+    for (int64_t i = threadIdx.x; i < full; i += T) stream8(out + 8 * i, zero);
     if (tail && threadIdx.x == 0) store8(out + 8 * full, zero, tail);
     return;
   }
-  for (int64_t i = threadIdx.x; i < full; i += kUnroll * kRowThreads) {
+  for (int64_t i = threadIdx.x; i < full; i += kUnroll * T) {
     Raw8<E> r[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (i + u * kRowThreads < full) load_all8(r[u], x + 8 * (i + u * kRowThreads));
+      if (i + u * T < full) load_all8(r[u], x + 8 * (i + u * T));
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (i + u * kRowThreads < full) give(r[u], 8 * (i + u * kRowThreads), 8);
+      if (i + u * T < full) give(r[u], 8 * (i + u * T), 8);
   }
   if (tail && threadIdx.x == 0) {
     // in place, a neighbour may have replaced the elements before the tail: they are dropped
@@ -267,11 +311,22 @@ __global__ __launch_bounds__(kRowThreads) void k_pref_grad(const E* logits, E* d
   }
 }
 
+// The threads of a row (or part): as many as have four batches of 32 elements each.
+template <class F>
+void by_threads(int64_t len, F launch) {
+  if (len >= 128 * 1024) launch(std::integral_constant<int, 1024>());
+  else if (len >= 128 * 512) launch(std::integral_constant<int, 512>());
+  else launch(std::integral_constant<int, 256>());
+}
+
 template <class E>
 hipError_t stats(const E* logits, const int64_t* labels, const float* ref, int64_t rows, int64_t V, const RowSplit& sp,
                  float* logps, const RowStats& ws, hipStream_t st) {
-  hipLaunchKernelGGL((k_row_stats<E>), dim3((unsigned)(rows * sp.parts)), dim3(kRowThreads), 0, st, logits, labels, ref,
-                     V, sp.parts, sp.len, ws, logps);
+  by_threads(sp.len, [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    hipLaunchKernelGGL((k_row_stats<E, T>), dim3((unsigned)(rows * sp.parts)), dim3(T), 0, st, logits, labels, ref, V,
+                       sp.parts, sp.len, ws, logps);
+  });
   return hipGetLastError();
 }
 
@@ -296,8 +351,11 @@ hipError_t preference_as(const Preference& p, const RowStats& ws, hipStream_t st
   const PairArgs a{p.labels,    p.ref_logps,  p.pairs, p.S,     p.V,          sp.parts, p.beta,
                    p.smoothing, p.grad_scale, ws,      p.logps, p.log_ratios, p.loss};
   if (p.dlogits) {
-    hipLaunchKernelGGL((k_pref_grad<E>), dim3((unsigned)(rows * sp.parts)), dim3(kRowThreads), 0, st, logits,
-                       static_cast<E*>(p.dlogits), a, sp.len);
+    by_threads(sp.len, [&](auto t) {
+      constexpr int T = decltype(t)::value;
+      hipLaunchKernelGGL((k_pref_grad<E, T>), dim3((unsigned)(rows * sp.parts)), dim3(T), 0, st, logits,
+                         static_cast<E*>(p.dlogits), a, sp.len);
+    });
   } else {
     hipLaunchKernelGGL(k_pref_loss, dim3((unsigned)p.pairs), dim3(kRowThreads), 0, st, a);
   }
