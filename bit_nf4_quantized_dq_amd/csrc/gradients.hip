@@ -27,23 +27,27 @@ __global__ __launch_bounds__(kThreads) void k_grad_table(GradTensors batch, Grad
   }
 }
 
+// Sum of the squares of a wavefront's piece [p, p + n): 64 elements a lane, all in flight at once.
+constexpr int kPiece = 4096, kPieces = (int)(kGradChunk / kPiece), kPieceVecs = kPiece / (8 * 64);
+
 template <class E>
-__device__ __forceinline__ double chunk_sum(const E* __restrict__ p, int32_t n, double sum) {
-  if (n == kGradChunk) {
-    Raw8<E> r[kVecs];
+__device__ __forceinline__ double piece_sum(const E* __restrict__ p, int32_t n, bool wide, double sum) {
+  const int lane = threadIdx.x & 63;
+  if (n >= kPiece) {
+    Raw8<E> r[kPieceVecs];
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) load_all8(r[v], p + 8 * (v * kThreads + (int)threadIdx.x));
+    for (int v = 0; v < kPieceVecs; ++v) load_all8(r[v], p + 8 * (v * 64 + lane));
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v)
+    for (int v = 0; v < kPieceVecs; ++v)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const double g = (double)r[v].get(i);
         sum = fma(g, g, sum);
       }
   } else {
-    for (int e = 8 * (int)threadIdx.x; e < n; e += 8 * kThreads) {
+    for (int e = 8 * lane; e < n; e += 8 * 64) {
       Raw8<E> r;
-      load8(r, p + e, n - e, n >= 8);
+      load8(r, p + e, n - e, wide);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const double g = (double)r.get(i);
@@ -54,21 +58,27 @@ __device__ __forceinline__ double chunk_sum(const E* __restrict__ p, int32_t n, 
   return sum;
 }
 
-__global__ __launch_bounds__(kThreads) void k_grad_norm(const GradChunk* __restrict__ table, int64_t chunks,
-                                                        float* norm, double* part, unsigned int* counter) {
-  __shared__ double lds[2][kThreads / 64];
+// Wavefronts take the pieces in turn.  The partials travel by system-scope (cache-bypassing)
+// stores and loads, and a store has completed before its workgroup is counted; the last
+// workgroup adds them in the workgroups' order.
+template <int T>
+__global__ __launch_bounds__(T) void k_grad_norm(const GradChunk* __restrict__ table, int64_t chunks, float* norm,
+                                                 double* part, unsigned int* counter) {
+  __shared__ double lds[2][T / 64];
   __shared__ bool s_last;
   double sum = 0.0;
-  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const GradChunk e = table[c];
-    sum = e.in_f32 ? chunk_sum(static_cast<const float*>(e.in), e.n, sum)
-                   : chunk_sum(static_cast<const uint16_t*>(e.in), e.n, sum);
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  for (int64_t u = (int64_t)blockIdx.x * (T / 64) + wave; u < chunks * kPieces; u += (int64_t)gridDim.x * (T / 64)) {
+    const GradChunk e = table[u / kPieces];
+    const int32_t at = (int32_t)(u % kPieces) * kPiece, n = e.n - at;
+    if (n <= 0) continue;
+    // a short last vector may reach back into the piece, or the chunk, before it
+    const bool wide = e.n >= 8;
+    sum = e.in_f32 ? piece_sum(static_cast<const float*>(e.in) + at, n, wide, sum)
+                   : piece_sum(static_cast<const uint16_t*>(e.in) + at, n, wide, sum);
   }
-  sum = block_sum_f64<kThreads>(sum, lds[0]);
+  sum = block_sum_f64<T>(sum, lds[0]);
   if (threadIdx.x == 0) {
-    // The partials travel by system-scope (cache-bypassing) stores and loads, and a store has
-    // completed before its workgroup is counted: a release fence here writes back and drops
-    // an L2 for each of the 1024 workgroups (67 us for the 84 MB of 41.9M BF16 gradients).
     __hip_atomic_store(part + blockIdx.x, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
     __builtin_amdgcn_s_waitcnt(0);
     const unsigned int old = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -76,11 +86,10 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(const GradChunk* __restr
   }
   __syncthreads();
   if (!s_last) return;
-  // the last workgroup adds the partials in the workgroups' order
   sum = 0.0;
-  for (unsigned int i = threadIdx.x; i < gridDim.x; i += kThreads)
+  for (unsigned int i = threadIdx.x; i < gridDim.x; i += T)
     sum += __hip_atomic_load(part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-  sum = block_sum_f64<kThreads>(sum, lds[1]);
+  sum = block_sum_f64<T>(sum, lds[1]);
   if (threadIdx.x == 0) {
     *norm = (float)sqrt(sum);
     __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -128,7 +137,13 @@ __global__ __launch_bounds__(kThreads) void k_grad_clip(const GradChunk* __restr
 
 }  // namespace
 
-int64_t grad_norm_parts(int64_t chunks) { return chunks < 1 ? 1 : (chunks < 1024 ? chunks : 1024); }
+// At most one workgroup for each compute unit: each adds one to the counter, and additions to
+// one address take about 8 ns each, one after the other.
+int64_t grad_norm_parts(int64_t chunks) {
+  const int64_t pieces = chunks * kPieces;
+  if (pieces <= 256 * 4) return pieces < 4 ? 1 : (pieces + 3) / 4;  // four wavefronts each
+  return pieces < 256 * 16 ? (pieces + 15) / 16 : 256;              // sixteen
+}
 
 hipError_t launch_grad_table(const GradTensors& batch, int count, GradChunk* table, hipStream_t st) {
   hipLaunchKernelGGL(k_grad_table, dim3((unsigned)count), dim3(kThreads), 0, st, batch, table);
@@ -137,8 +152,12 @@ hipError_t launch_grad_table(const GradTensors& batch, int count, GradChunk* tab
 
 hipError_t launch_grad_norm(const GradChunk* table, int64_t chunks, float* norm, double* part, unsigned int* counter,
                             hipStream_t st) {
-  hipLaunchKernelGGL(k_grad_norm, dim3((unsigned)grad_norm_parts(chunks)), dim3(kThreads), 0, st, table, chunks, norm,
-                     part, counter);
+  const dim3 grid((unsigned)grad_norm_parts(chunks));
+  if (chunks * kPieces <= 256 * 4) {
+    hipLaunchKernelGGL(k_grad_norm<256>, grid, dim3(256), 0, st, table, chunks, norm, part, counter);
+  } else {
+    hipLaunchKernelGGL(k_grad_norm<1024>, grid, dim3(1024), 0, st, table, chunks, norm, part, counter);
+  }
   return hipGetLastError();
 }
 
