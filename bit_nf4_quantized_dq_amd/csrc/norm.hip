@@ -19,8 +19,8 @@ namespace {
 // The gate of a row: none or one gate row for a run of rows (loaded where a run begins), or loaded
 // with each row.
 enum GateKind { kGateRuns, kGateRows };
-// Which outputs: any of them, or both large ones (stored without a branch); the latter also with
-// operands larger than the cache, which are read past it.
+// Which outputs: any of them, or both large ones (stored without a branch); in the backward the
+// latter also with operands larger than the cache, which are read past it.
 enum Outputs { kAny, kBoth, kBothStream };
 
 template <class S>
@@ -41,15 +41,14 @@ struct FwdArgs {
 // on at the same time lie together in memory.)
 template <class S, int T, bool SHORT, GateKind KIND, Outputs OUT>
 __global__ __launch_bounds__(T) void k_norm_fwd(FwdArgs<S> a) {
-  constexpr bool STREAM = OUT == kBothStream;
   __shared__ float lds[2][2][T / 64];
   const int64_t d = a.d;
   const uint32_t rows = (uint32_t)a.M, run = (uint32_t)a.gate_rows;  // below 2^24
   const Columns<SHORT> col((int)d, 8 * threadIdx.x);
   Raw8<S> x, x_next;
   Raw8<uint16_t> y, y_next, g, g_next, w_post, w_pre;
-  load_in<STREAM>(col, x, a.x + blockIdx.x * d);
-  load_in<STREAM>(col, y, a.y + blockIdx.x * d);
+  col.load(x, a.x + blockIdx.x * d);
+  col.load(y, a.y + blockIdx.x * d);
   if (a.gate) col.load(g, a.gate + (KIND == kGateRows ? blockIdx.x / run * d : 0));
   else ones8(g);
   if (a.w_post) col.load(w_post, a.w_post);
@@ -63,8 +62,8 @@ __global__ __launch_bounds__(T) void k_norm_fwd(FwdArgs<S> a) {
   for (uint32_t row = blockIdx.x; row < rows; row += gridDim.x, odd = !odd) {
     // past the last row: once more the last one, so that the loop's loads need no condition
     const uint32_t ahead = row + gridDim.x < rows ? row + gridDim.x : row;
-    load_in<STREAM>(col, x_next, a.x + ahead * d);
-    load_in<STREAM>(col, y_next, a.y + ahead * d);
+    col.load(x_next, a.x + ahead * d);
+    col.load(y_next, a.y + ahead * d);
     if constexpr (KIND == kGateRows) col.load(g_next, a.gate + ahead / run * d);
     and8(y, a.y_bits);
     float r_y = 1.f;
@@ -290,9 +289,6 @@ __global__ __launch_bounds__(kColThreads) void k_norm_cols(const float* __restri
   }
 }
 
-// Whether a call's operands, of so many bytes an element, are more than the cache keeps.
-bool stream(int64_t M, int64_t d, int64_t bytes) { return M * d * bytes > (int64_t)128 << 20; }
-
 template <class S, int T, bool SHORT = false>
 hipError_t fwd_as(const NormFwd& p, hipStream_t st) {
   // all 2048 threads of each of the 256 compute units at once
@@ -312,23 +308,24 @@ hipError_t fwd_as(const NormFwd& p, hipStream_t st) {
                      p.eps,
                      (float)(1.0 / (double)p.d),
                      p.post};
-  const Outputs out = !a.x_out || !a.h ? kAny : (stream(p.M, p.d, 2 * sizeof(S) + 4) ? kBothStream : kBoth);
+  const bool both = a.x_out && a.h;
   const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(T), 0, st, a); };
   if (a.gate && a.gate_rows < a.M) {
-    if (out == kAny) launch(k_norm_fwd<S, T, SHORT, kGateRows, kAny>);
-    else if (out == kBoth) launch(k_norm_fwd<S, T, SHORT, kGateRows, kBoth>);
-    else launch(k_norm_fwd<S, T, SHORT, kGateRows, kBothStream>);
+    if (both) launch(k_norm_fwd<S, T, SHORT, kGateRows, kBoth>);
+    else launch(k_norm_fwd<S, T, SHORT, kGateRows, kAny>);
   } else {
-    if (out == kAny) launch(k_norm_fwd<S, T, SHORT, kGateRuns, kAny>);
-    else if (out == kBoth) launch(k_norm_fwd<S, T, SHORT, kGateRuns, kBoth>);
-    else launch(k_norm_fwd<S, T, SHORT, kGateRuns, kBothStream>);
+    if (both) launch(k_norm_fwd<S, T, SHORT, kGateRuns, kBoth>);
+    else launch(k_norm_fwd<S, T, SHORT, kGateRuns, kAny>);
   }
   return hipGetLastError();
 }
 
 template <class S, int T, bool SHORT>
 hipError_t bwd_rows(const BwdArgs<S>& a, GateKind kind, hipStream_t st) {
-  const Outputs out = !a.dx || !a.dy ? kAny : (stream(a.M, a.d, 3 * sizeof(S) + 6) ? kBothStream : kBoth);
+  // Operands that the 256 MB cache could hold may be there already: at 100 MB (2048 x 4096) reading
+  // past it costs 32 us for 29, at 200 MB nothing, at 400 MB (8192 x 4096) it saves 93 - 79 us.
+  const bool large = a.M * a.d * (int64_t)(3 * sizeof(S) + 6) > (int64_t)256 << 20;
+  const Outputs out = !a.dx || !a.dy ? kAny : (large ? kBothStream : kBoth);
   const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)a.seg.count), dim3(T), 0, st, a); };
   if (kind == kGateRows) {
     if (out == kAny) launch(k_norm_bwd<S, T, SHORT, kGateRows, kAny>);

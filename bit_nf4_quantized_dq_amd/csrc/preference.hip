@@ -258,7 +258,8 @@ __global__ __launch_bounds__(T) void k_pref_grad(const E* logits, E* dlogits, Pa
   const int64_t seq = row / a.S, pair = seq < a.pairs ? seq : seq - a.pairs;
   const int64_t label = a.labels[row], V = a.V;
   const bool counted = label >= 0 && label < V;
-  const bool lead = p == 0 && seq < a.pairs && row == seq * a.S;  // this pair's workgroup
+  // the workgroup that writes the pair's results: among the first to run
+  const bool lead = p == 0 && seq >= a.pairs && row == (seq + 1) * a.S - 1;
   double d[2];
   if (counted || lead) pair_sums<T>(a, pair, lead, lds, d);
   if (lead) finish_pair<T>(a, pair, d, lds);
@@ -311,18 +312,19 @@ __global__ __launch_bounds__(T) void k_pref_grad(const E* logits, E* dlogits, Pa
   }
 }
 
-// The threads of a row (or part): as many as have four batches of 32 elements each.
+// The threads of each of `blocks` rows or parts of `len` elements: as many as have four batches of
+// 32 elements each, and a launch of fewer than 2^32 threads in all.
 template <class F>
-void by_threads(int64_t len, F launch) {
-  if (len >= 128 * 1024) launch(std::integral_constant<int, 1024>());
-  else if (len >= 128 * 512) launch(std::integral_constant<int, 512>());
+void by_threads(int64_t blocks, int64_t len, F launch) {
+  if (len >= 128 * 1024 && blocks < int64_t(1) << 22) launch(std::integral_constant<int, 1024>());
+  else if (len >= 128 * 512 && blocks < int64_t(1) << 23) launch(std::integral_constant<int, 512>());
   else launch(std::integral_constant<int, 256>());
 }
 
 template <class E>
 hipError_t stats(const E* logits, const int64_t* labels, const float* ref, int64_t rows, int64_t V, const RowSplit& sp,
                  float* logps, const RowStats& ws, hipStream_t st) {
-  by_threads(sp.len, [&](auto t) {
+  by_threads(rows * sp.parts, sp.len, [&](auto t) {
     constexpr int T = decltype(t)::value;
     hipLaunchKernelGGL((k_row_stats<E, T>), dim3((unsigned)(rows * sp.parts)), dim3(T), 0, st, logits, labels, ref, V,
                        sp.parts, sp.len, ws, logps);
@@ -351,7 +353,7 @@ hipError_t preference_as(const Preference& p, const RowStats& ws, hipStream_t st
   const PairArgs a{p.labels,    p.ref_logps,  p.pairs, p.S,     p.V,          sp.parts, p.beta,
                    p.smoothing, p.grad_scale, ws,      p.logps, p.log_ratios, p.loss};
   if (p.dlogits) {
-    by_threads(sp.len, [&](auto t) {
+    by_threads(rows * sp.parts, sp.len, [&](auto t) {
       constexpr int T = decltype(t)::value;
       hipLaunchKernelGGL((k_pref_grad<E, T>), dim3((unsigned)(rows * sp.parts)), dim3(T), 0, st, logits,
                          static_cast<E*>(p.dlogits), a, sp.len);
