@@ -68,8 +68,10 @@ def _stream(t: torch.Tensor) -> int:
 def _tensors(specs, device) -> None:
     """_validate, with a quick pass first."""
     if device is not None and device.type == "cuda":
+        index = device.index
         for t, dtype, _, shape in specs:
-            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            # (a tensor on the CPU has the device number -1)
+            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
                     and t.is_contiguous()):
                 break
         else:
@@ -248,16 +250,16 @@ def preference_loss(logits: torch.Tensor, labels: torch.Tensor, ref_logps: torch
             raise ValueError("dlogits: given with need_grad=False")
         specs.append((dlogits, logits.dtype, "dlogits", (n, S, V)))
     _tensors(specs, dev)
-    out = torch.empty(1 + n + n * S, dtype=torch.float32, device=dev)
-    loss, log_ratios, logps = out[:1], out[1:1 + n], out[1 + n:].view(n, S)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    log_ratios = torch.empty(n, dtype=torch.float32, device=dev)
+    logps = torch.empty(n, S, dtype=torch.float32, device=dev)
     if need_grad and dlogits is None:
         dlogits = torch.empty_like(logits)
     st = _stream(logits)
     ws = _workspace(ws, preference_workspace_size(n // 2, S, V), logits, st)
-    at = out.data_ptr()
     _check(_lib().qlora_preference_loss(logits.data_ptr(), labels.data_ptr(), _ptr(ref_logps), n // 2, S, V, kind,
-                                        beta, label_smoothing, grad_scale, at, at + 4, at + 4 * (1 + n), _ptr(dlogits),
-                                        ws.data_ptr(), ws.numel(), st), "preference_loss")
+                                        beta, label_smoothing, grad_scale, loss.data_ptr(), log_ratios.data_ptr(),
+                                        logps.data_ptr(), _ptr(dlogits), ws.data_ptr(), ws.numel(), st), "preference_loss")
     return loss, log_ratios, logps, dlogits
 
 
