@@ -33,6 +33,33 @@ __device__ __forceinline__ double label_logp(float xl, float m, float s) {
   return (double)xl - (double)m - log((double)s);
 }
 
+// A row or part of `count` elements in whole vectors from its first 16-byte boundary on (`at`
+// decides), and what is left over before them and after.  (Rows of an odd width otherwise have
+// every vector across a boundary: log-probabilities of 4096 rows of 50257 58 us, so 48.)
+struct Span {
+  int head, tail;
+  int32_t full;
+  bool wide;
+  template <class E>
+  __device__ __forceinline__ Span(const E* at, int64_t count) {
+    const int to = (int)((16 - (reinterpret_cast<uintptr_t>(at) & 15)) & 15) / (int)sizeof(E);
+    head = to < count ? to : (int)count;
+    full = (int32_t)((count - head) >> 3);
+    tail = (int)((count - head) & 7);
+    wide = count >= 8;
+  }
+  // the first `head` elements (the rest of the vector is to be dropped)
+  template <class E>
+  __device__ __forceinline__ void load_head(Raw8<E>& r, const E* x) const {
+    if (wide) load_all8(r, x);
+    else load8(r, x, head, false);
+  }
+  template <class E>
+  __device__ __forceinline__ void load_tail(Raw8<E>& r, const E* x) const {
+    load8(r, x + head + 8 * full, tail, wide);
+  }
+};
+
 // One workgroup per row and part: one pass with the running maximum and sum of each thread.  A
 // whole row (parts == 1) is finished here, a split one by its readers.
 template <class E, int T>
@@ -67,8 +94,9 @@ __global__ __launch_bounds__(T) void k_row_stats(const E* __restrict__ logits,
     for (int j = 0; j < 8; ++j) s += exp2_hw((f[j] - base) * kLog2e);
     m = t;
   };
-  const int32_t full = (int32_t)((v1 - v0) >> 3), batches = full / (kUnroll * T);
-  const E* xp = x + v0;
+  const Span span(x + v0, v1 - v0);
+  const int32_t full = span.full, batches = full / (kUnroll * T);
+  const E* xp = x + v0 + span.head;
   // Batches of 32 elements a thread.  The exponentials are 2^(x log2 e - n) with a whole number n
   // just above the maximum's x log2 e: the product is not rounded before n leaves it, so this
   // is one operation for the difference and the factor, and changes of n scale exactly.  n
@@ -118,10 +146,15 @@ __global__ __launch_bounds__(T) void k_row_stats(const E* __restrict__ logits,
     load_all8(r, xp + 8 * i);
     take(r, 8);
   }
-  if (const int tail = (int)((v1 - v0) & 7); tail && threadIdx.x == 0) {
+  if (threadIdx.x == 0 && span.head) {
     Raw8<E> r;
-    load8(r, xp + 8 * full, tail, V >= 8);
-    take(r, tail);
+    span.load_head(r, x + v0);
+    take(r, span.head);
+  }
+  if (threadIdx.x == T - 1 && span.tail) {
+    Raw8<E> r;
+    span.load_tail(r, x + v0);
+    take(r, span.tail);
   }
 #pragma unroll
   for (int k = 32; k >= 1; k >>= 1) merge(m, s, __shfl_xor(m, k, 64), __shfl_xor(s, k, 64));
@@ -287,44 +320,56 @@ __global__ __launch_bounds__(T) void k_pref_grad(const E* logits, E* dlogits, Pa
     if (n == 8) stream8(out + at, f);
     else store8(out + at, f, n);
   };
-  const int64_t full = (v1 - v0) >> 3;
-  const int tail = (int)((v1 - v0) & 7);
+  const Span span(out, v1 - v0);
+  const int32_t full = span.full;
   if (!counted) {
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int64_t i = threadIdx.x; i < full; i += T) stream8(out + 8 * i, zero);
-    if (tail && threadIdx.x == 0) store8(out + 8 * full, zero, tail);
+    for (int32_t i = threadIdx.x; i < full; i += T) stream8(out + span.head + 8 * i, zero);
+    if (threadIdx.x == 0) store8(out, zero, span.head);
+    if (threadIdx.x == T - 1) store8(out + span.head + 8 * full, zero, span.tail);
     return;
   }
-  for (int64_t i = threadIdx.x; i < full; i += kUnroll * T) {
+  for (int32_t i = threadIdx.x; i < full; i += kUnroll * T) {
     Raw8<E> r[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (i + u * T < full) load_all8(r[u], x + 8 * (i + u * T));
+      if (i + u * T < full) load_all8(r[u], x + span.head + 8 * (i + u * T));
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (i + u * T < full) give(r[u], 8 * (i + u * T), 8);
+      if (i + u * T < full) give(r[u], span.head + 8 * (i + u * T), 8);
   }
-  if (tail && threadIdx.x == 0) {
-    // in place, a neighbour may have replaced the elements before the tail: they are dropped
+  // (in place, a neighbour may have replaced the elements that these two drop)
+  if (threadIdx.x == 0 && span.head) {
     Raw8<E> r;
-    load8(r, x + 8 * full, tail, V >= 8);
-    give(r, 8 * full, tail);
+    span.load_head(r, x);
+    give(r, 0, span.head);
+  }
+  if (threadIdx.x == T - 1 && span.tail) {
+    Raw8<E> r;
+    span.load_tail(r, x);
+    give(r, span.head + 8 * full, span.tail);
   }
 }
 
-// The threads of each of `blocks` rows or parts of `len` elements: as many as have four batches of
-// 32 elements each, and a launch of fewer than 2^32 threads in all.
-template <class F>
+// The threads of each of `blocks` rows or parts of `len` elements (a launch has fewer than 2^32
+// threads in all).  Short rows take few, so that many rows are under way; 8192 rows of 1000: 10.5 us
+// by 64 threads, 20 by 256; 16384 of 8192: 33 by 128, 37 by 256; 4096 of 32768: 33 by 256, 38 by
+// 128 or 1024; 4096 of 131072: 112 by 1024, 121 by 256.  The gradient (`writes`), which keeps
+// loads and stores in flight, has 256 from 2048 elements on (1600 rows of 16384: 28 us, 29.6 by 128).
+template <bool writes, class F>
 void by_threads(int64_t blocks, int64_t len, F launch) {
   if (len >= 128 * 1024 && blocks < int64_t(1) << 22) launch(std::integral_constant<int, 1024>());
-  else if (len >= 128 * 512 && blocks < int64_t(1) << 23) launch(std::integral_constant<int, 512>());
-  else launch(std::integral_constant<int, 256>());
+  else if (len >= 48 * 1024 && blocks < int64_t(1) << 23) launch(std::integral_constant<int, 512>());
+  else if (len >= (writes ? 2 * 1024 : 24 * 1024)) launch(std::integral_constant<int, 256>());
+  else if constexpr (writes) launch(std::integral_constant<int, 64>());
+  else if (len >= 4 * 1024) launch(std::integral_constant<int, 128>());
+  else launch(std::integral_constant<int, 64>());
 }
 
 template <class E>
 hipError_t stats(const E* logits, const int64_t* labels, const float* ref, int64_t rows, int64_t V, const RowSplit& sp,
                  float* logps, const RowStats& ws, hipStream_t st) {
-  by_threads(rows * sp.parts, sp.len, [&](auto t) {
+  by_threads<false>(rows * sp.parts, sp.len, [&](auto t) {
     constexpr int T = decltype(t)::value;
     hipLaunchKernelGGL((k_row_stats<E, T>), dim3((unsigned)(rows * sp.parts)), dim3(T), 0, st, logits, labels, ref, V,
                        sp.parts, sp.len, ws, logps);
@@ -353,7 +398,7 @@ hipError_t preference_as(const Preference& p, const RowStats& ws, hipStream_t st
   const PairArgs a{p.labels,    p.ref_logps,  p.pairs, p.S,     p.V,          sp.parts, p.beta,
                    p.smoothing, p.grad_scale, ws,      p.logps, p.log_ratios, p.loss};
   if (p.dlogits) {
-    by_threads(rows * sp.parts, sp.len, [&](auto t) {
+    by_threads<true>(rows * sp.parts, sp.len, [&](auto t) {
       constexpr int T = decltype(t)::value;
       hipLaunchKernelGGL((k_pref_grad<E, T>), dim3((unsigned)(rows * sp.parts)), dim3(T), 0, st, logits,
                          static_cast<E*>(p.dlogits), a, sp.len);
