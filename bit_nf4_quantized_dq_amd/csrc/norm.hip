@@ -35,13 +35,13 @@ struct FwdArgs {
   int post;
 };
 
-// One workgroup of T threads for every gridDim.x-th row, one row at a time and eight columns to
+// One workgroup of d / 8 threads (in whole wavefronts; ONE: one) for every gridDim.x-th row, one row at a time and eight columns to
 // a thread: every operand is read once and kept in registers, the weights for all rows, and
 // the next row is loaded while this one's two sums cross the workgroup.  (Rows that are worked
 // on at the same time lie together in memory.)
-template <class S, int T, bool SHORT, GateKind KIND, Outputs OUT>
-__global__ __launch_bounds__(T) void k_norm_fwd(FwdArgs<S> a) {
-  __shared__ float lds[2][2][T / 64];
+template <class S, bool ONE, bool SHORT, GateKind KIND, Outputs OUT>
+__global__ __launch_bounds__(ONE ? 64 : 1024) void k_norm_fwd(FwdArgs<S> a) {
+  __shared__ float lds[2][2][16];
   const int64_t d = a.d;
   const uint32_t rows = (uint32_t)a.M, run = (uint32_t)a.gate_rows;  // below 2^24
   const Columns<SHORT> col((int)d, 8 * threadIdx.x);
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(T) void k_norm_fwd(FwdArgs<S> a) {
       float s[1] = {0.f};
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[0] = fmaf(own.get(i), own.get(i), s[0]);
-      block_sum<T>(s, lds[odd][0]);
+      block_sum<ONE>(s, lds[odd][0]);
       r_y = 1.f / sqrtf(s[0] * a.inv_d + a.eps);
     }
     Raw8<float> xo;
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(T) void k_norm_fwd(FwdArgs<S> a) {
     for (int i = 0; i < 8; ++i) s[0] = fmaf(own.f[i], own.f[i], s[0]);
     // (also where h is not wanted: the exchange lies between the loads of a row and the stores
     // that may replace it)
-    block_sum<T>(s, lds[odd][1]);
+    block_sum<ONE>(s, lds[odd][1]);
     if (OUT != kAny || a.x_out) col.store(a.x_out + row * d, xo.f);
     if (OUT != kAny || a.h) {
       const float r_x = 1.f / sqrtf(s[0] * a.inv_d + a.eps);
@@ -135,9 +135,9 @@ struct RowVec {
 // with q = g w_post y,  sum(b y) = sum(dx' q) + r_x sum(a q) - k sum(x' q),  k = r_x^3 mean(a x').
 // An operand that is not given is zeros, a weight or gate that is not given is ones, so the
 // arithmetic has no cases.
-template <class S, int T, bool SHORT, GateKind KIND, Outputs OUT>
-__global__ __launch_bounds__(T, SHORT ? 1 : 4) void k_norm_bwd(BwdArgs<S> a) {
-  __shared__ float lds[2][6 * (T / 64)];
+template <class S, bool ONE, bool SHORT, GateKind KIND, Outputs OUT>
+__global__ __launch_bounds__(ONE ? 64 : 1024, SHORT ? 1 : 4) void k_norm_bwd(BwdArgs<S> a) {
+  __shared__ float lds[2][6 * 16];
   const int64_t d = a.d, seg = blockIdx.x;
   // a segment of whole gate rows, or one of per_group segments that share a gate row's rows
   int64_t r0 = seg * a.seg.rows, r1 = r0 + a.seg.rows < a.M ? r0 + a.seg.rows : a.M, group;
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(T, SHORT ? 1 : 4) void k_norm_bwd(BwdArgs<S> a) {
       s[4] = fmaf(ai, q, s[4]);
       s[5] = fmaf(xi, q, s[5]);
     }
-    block_sum<T>(s, lds[odd]);
+    block_sum<ONE>(s, lds[odd]);
     opaque(w_pre), opaque(w_post), r.pack();
     const float r_x = a.h_bits ? 1.f / sqrtf(s[0] * a.inv_d + a.eps) : 0.f;
     const float k = a.h_bits ? r_x * r_x * r_x * (s[1] * a.inv_d) : 0.f;
@@ -289,10 +289,12 @@ __global__ __launch_bounds__(kColThreads) void k_norm_cols(const float* __restri
   }
 }
 
-template <class S, int T, bool SHORT = false>
+template <class S, bool ONE, bool SHORT>
 hipError_t fwd_as(const NormFwd& p, hipStream_t st) {
-  // all 2048 threads of each of the 256 compute units at once
-  const unsigned grid = (unsigned)(p.M < 256 * 2048 / T ? p.M : 256 * 2048 / T);
+  // as many workgroups as the 32 wavefronts of each of the 256 compute units hold at once
+  const unsigned threads = norm_threads(p.d);
+  const int64_t slots = 256 * (32 / (threads / 64));
+  const unsigned grid = (unsigned)(p.M < slots ? p.M : slots);
   const FwdArgs<S> a{static_cast<const S*>(p.x),
                      p.y ? p.y : static_cast<const uint16_t*>(p.x),
                      p.w_post,
@@ -309,37 +311,38 @@ hipError_t fwd_as(const NormFwd& p, hipStream_t st) {
                      (float)(1.0 / (double)p.d),
                      p.post};
   const bool both = a.x_out && a.h;
-  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(T), 0, st, a); };
+  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, st, a); };
   if (a.gate && a.gate_rows < a.M) {
-    if (both) launch(k_norm_fwd<S, T, SHORT, kGateRows, kBoth>);
-    else launch(k_norm_fwd<S, T, SHORT, kGateRows, kAny>);
+    if (both) launch(k_norm_fwd<S, ONE, SHORT, kGateRows, kBoth>);
+    else launch(k_norm_fwd<S, ONE, SHORT, kGateRows, kAny>);
   } else {
-    if (both) launch(k_norm_fwd<S, T, SHORT, kGateRuns, kBoth>);
-    else launch(k_norm_fwd<S, T, SHORT, kGateRuns, kAny>);
+    if (both) launch(k_norm_fwd<S, ONE, SHORT, kGateRuns, kBoth>);
+    else launch(k_norm_fwd<S, ONE, SHORT, kGateRuns, kAny>);
   }
   return hipGetLastError();
 }
 
-template <class S, int T, bool SHORT>
+template <class S, bool ONE, bool SHORT>
 hipError_t bwd_rows(const BwdArgs<S>& a, GateKind kind, hipStream_t st) {
   // Operands that the 256 MB cache could hold may be there already: at 100 MB (2048 x 4096) reading
   // past it costs 32 us for 29, at 200 MB nothing, at 400 MB (8192 x 4096) it saves 93 - 79 us.
   const bool large = a.M * a.d * (int64_t)(3 * sizeof(S) + 6) > (int64_t)256 << 20;
   const Outputs out = !a.dx || !a.dy ? kAny : (large ? kBothStream : kBoth);
-  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)a.seg.count), dim3(T), 0, st, a); };
+  const dim3 grid((unsigned)a.seg.count), block(norm_threads(a.d));
+  const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, a); };
   if (kind == kGateRows) {
-    if (out == kAny) launch(k_norm_bwd<S, T, SHORT, kGateRows, kAny>);
-    else if (out == kBoth) launch(k_norm_bwd<S, T, SHORT, kGateRows, kBoth>);
-    else launch(k_norm_bwd<S, T, SHORT, kGateRows, kBothStream>);
+    if (out == kAny) launch(k_norm_bwd<S, ONE, SHORT, kGateRows, kAny>);
+    else if (out == kBoth) launch(k_norm_bwd<S, ONE, SHORT, kGateRows, kBoth>);
+    else launch(k_norm_bwd<S, ONE, SHORT, kGateRows, kBothStream>);
   } else {
-    if (out == kAny) launch(k_norm_bwd<S, T, SHORT, kGateRuns, kAny>);
-    else if (out == kBoth) launch(k_norm_bwd<S, T, SHORT, kGateRuns, kBoth>);
-    else launch(k_norm_bwd<S, T, SHORT, kGateRuns, kBothStream>);
+    if (out == kAny) launch(k_norm_bwd<S, ONE, SHORT, kGateRuns, kAny>);
+    else if (out == kBoth) launch(k_norm_bwd<S, ONE, SHORT, kGateRuns, kBoth>);
+    else launch(k_norm_bwd<S, ONE, SHORT, kGateRuns, kBothStream>);
   }
   return hipGetLastError();
 }
 
-template <class S, int T, bool SHORT = false>
+template <class S, bool ONE, bool SHORT>
 hipError_t bwd_as(const NormBwd& p, hipStream_t st) {
   const NormSegments seg = norm_segments(p.M, p.d, p.gate ? p.gate_rows : 0);
   const int64_t per = seg.count * p.d;
@@ -359,7 +362,7 @@ hipError_t bwd_as(const NormBwd& p, hipStream_t st) {
   if (p.dw_pre) a.p_pre = part, part += per;
   if (p.dw_post) a.p_post = part, part += per;
   if (p.dgate && seg.per_group) a.p_gate = part;
-  const hipError_t e = bwd_rows<S, T, SHORT>(a, p.gate && p.gate_rows == 1 ? kGateRows : kGateRuns, st);
+  const hipError_t e = bwd_rows<S, ONE, SHORT>(a, p.gate && p.gate_rows == 1 ? kGateRows : kGateRuns, st);
   if (e != hipSuccess) return e;
   const int64_t groups = a.p_gate ? (p.M + p.gate_rows - 1) / p.gate_rows : 0;
   const int64_t job0 = a.p_pre ? 0 : (a.p_post ? 1 : 2), jobs = (groups ? 2 + groups : (a.p_post ? 2 : 1)) - job0;
@@ -370,24 +373,15 @@ hipError_t bwd_as(const NormBwd& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The threads of a row: one for each eight columns.
 template <class S>
 hipError_t fwd(const NormFwd& p, hipStream_t st) {
-  if (p.d < 8) return fwd_as<S, 64, true>(p, st);
-  if (p.d <= 512) return fwd_as<S, 64>(p, st);
-  if (p.d <= 1024) return fwd_as<S, 128>(p, st);
-  if (p.d <= 2048) return fwd_as<S, 256>(p, st);
-  if (p.d <= 4096) return fwd_as<S, 512>(p, st);
-  return fwd_as<S, 1024>(p, st);
+  if (p.d < 8) return fwd_as<S, true, true>(p, st);
+  return norm_threads(p.d) == 64 ? fwd_as<S, true, false>(p, st) : fwd_as<S, false, false>(p, st);
 }
 template <class S>
 hipError_t bwd(const NormBwd& p, hipStream_t st) {
-  if (p.d < 8) return bwd_as<S, 64, true>(p, st);
-  if (p.d <= 512) return bwd_as<S, 64>(p, st);
-  if (p.d <= 1024) return bwd_as<S, 128>(p, st);
-  if (p.d <= 2048) return bwd_as<S, 256>(p, st);
-  if (p.d <= 4096) return bwd_as<S, 512>(p, st);
-  return bwd_as<S, 1024>(p, st);
+  if (p.d < 8) return bwd_as<S, true, true>(p, st);
+  return norm_threads(p.d) == 64 ? bwd_as<S, true, false>(p, st) : bwd_as<S, false, false>(p, st);
 }
 
 }  // namespace

@@ -44,6 +44,8 @@ struct NormBwd {
 struct NormSegments {
   int64_t rows, count, per_group;
 };
+// The threads of a row: one for each eight columns, in whole wavefronts.
+inline unsigned norm_threads(int64_t d) { return (unsigned)((d + 511) / 512 * 64); }
 NormSegments norm_segments(int64_t M, int64_t d, int64_t gate_rows);
 hipError_t launch_norm_fwd(const NormFwd& p, hipStream_t st);
 hipError_t launch_norm_bwd(const NormBwd& p, hipStream_t st);

@@ -98,10 +98,11 @@ size_t grad_ws_bytes(int64_t chunks) { return kHead + sizeof(double) * (size_t)g
 namespace qlora {
 
 NormSegments norm_segments(int64_t M, int64_t d, int64_t gate_rows) {
-  // sixteen wavefronts for each of the 256 compute units, and at least four rows a segment:
-  // a segment's partials then cost at most a quarter of what its rows do
-  const int64_t threads = std::max<int64_t>(64, std::min<int64_t>(1024, (d + 7) / 8));
-  int64_t rows = std::max<int64_t>(4, (M * threads + 256 * 1024 - 1) / (256 * 1024));
+  // as many segments as the sixteen wavefronts (of 128 registers) of each of the 256 compute units
+  // hold at once, and at least four rows a segment: its partials then cost at most a quarter
+  // of what its rows do
+  const int64_t slots = 256 * (16 / (norm_threads(d) / 64));
+  int64_t rows = std::max<int64_t>(4, (M + slots - 1) / slots);
   NormSegments s{};
   gate_rows = gate_rows ? std::min(gate_rows, M) : M;
   if (gate_rows <= rows) {

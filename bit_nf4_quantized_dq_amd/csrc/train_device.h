@@ -223,34 +223,32 @@ __device__ __forceinline__ float clip_coefficient(float norm, float max_norm) {
   return c >= 1.f ? 1.f : c;
 }
 
-// Sum over W lanes (a power of two up to 16) of each aligned group of W, the same in them all.
-template <int W>
-__device__ __forceinline__ float group_sum(float v) {
-  if constexpr (W >= 2) v += dpp_partner<0xB1>(v);    // quad_perm [1, 0, 3, 2]
-  if constexpr (W >= 4) v += dpp_partner<0x4E>(v);    // quad_perm [2, 3, 0, 1]
-  if constexpr (W >= 8) v += dpp_partner<0x141>(v);   // row_half_mirror
-  if constexpr (W >= 16) v += dpp_partner<0x140>(v);  // row_mirror
+// Sum over each row of 16 lanes, the same in them all.
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp_partner<0xB1>(v);   // quad_perm [1, 0, 3, 2]
+  v += dpp_partner<0x4E>(v);   // quad_perm [2, 3, 0, 1]
+  v += dpp_partner<0x141>(v);  // row_half_mirror
+  v += dpp_partner<0x140>(v);  // row_mirror
   return v;
 }
 
-// ---- sums of N values over the T threads of a workgroup, the same in every thread: each
-// wavefront, then the wavefronts' sums as a group of lanes.  `lds` holds N * T / 64 floats; a
-// caller that sums again without a barrier of its own in between gives the next call another
-// array.
-template <int T, int N>
+// ---- sums of N values over a workgroup of up to 16 wavefronts (ONE: a single one), the same in
+// every thread: each wavefront, then the wavefronts' sums as a row of lanes.  `lds` holds 16 N
+// floats; a caller that sums again without a barrier of its own in between gives the next call
+// another array.
+template <bool ONE, int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float* lds) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if constexpr (T > 64) {
-    constexpr int W = T / 64;
-    const int wave = threadIdx.x >> 6;
+  if constexpr (!ONE) {
+    const int slot = threadIdx.x & 15, waves = blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) lds[i * W + wave] = v[i];
+      for (int i = 0; i < N; ++i) lds[i * 16 + (threadIdx.x >> 6)] = v[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = group_sum<W>(lds[i * W + (threadIdx.x & (W - 1))]);
+    for (int i = 0; i < N; ++i) v[i] = row_sum(slot < waves ? lds[i * 16 + slot] : 0.f);
   }
 }
 
