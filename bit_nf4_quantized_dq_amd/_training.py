@@ -265,7 +265,8 @@ def preference_loss(logits: torch.Tensor, labels: torch.Tensor, ref_logps: torch
 
 class GradList:
     """A model's gradient tensors, laid out once: a device table that grad_norm and grad_clip go
-    by.  It holds the tensors (their values may change, their memory stays theirs).
+    by.  It holds the tensors (their values may change, their memory stays theirs); the table
+    is written on the stream that is current when the list is made.
 
     tensors: contiguous BF16 or FP32 CUDA tensors.  out: where grad_clip writes, one tensor of
     the same size for each (BF16 or FP32); None clips in place."""

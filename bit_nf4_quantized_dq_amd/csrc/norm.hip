@@ -108,6 +108,8 @@ struct BwdArgs {
   uint16_t* dy;
   uint16_t* dgate;                 // for gate rows whole in a segment, else null
   float *p_pre, *p_post, *p_gate;  // [segment][d] FP32 partials, null where not wanted
+  unsigned int* counter;           // for few partials, which the last workgroup adds (else null)
+  uint16_t *sum_pre, *sum_post, *sum_gate;  // where it writes the sums
   int64_t M, d, gate_rows;
   NormSegments seg;
   uint32_t y_bits, h_bits, o_bits;  // y; x and dh; dx_out
@@ -129,6 +131,42 @@ struct RowVec {
   }
   __device__ __forceinline__ void pack() { opaque(x), opaque(dxo), opaque(y), opaque(dh), opaque(g); }
 };
+
+// Few partials: the last workgroup to finish adds them in the segments' order.  (A second launch
+// takes 3 us of the host and 4 of the device; here each workgroup writes its L2 back once, and
+// one of them reads all partials, which is as long at about 256 KB.)
+constexpr int64_t kFewSegments = 32;
+constexpr size_t kFewBytes = 256 * 1024;
+template <class S, bool SHORT>
+__device__ void add_segments(const BwdArgs<S>& a, const Columns<SHORT>& col) {
+  __shared__ bool last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned int old = __hip_atomic_fetch_add(a.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = old + 1u == gridDim.x;
+    if (last) __hip_atomic_store(a.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  const auto add = [&](const float* p, int64_t first, int64_t count, uint16_t* out) {
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int64_t s = first; s < first + count; ++s) {
+      Raw8<float> r;
+      col.load(r, p + s * a.d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += r.f[i];
+    }
+    col.store(out, sum);
+  };
+  if (a.p_pre) add(a.p_pre, 0, gridDim.x, a.sum_pre);
+  if (a.p_post) add(a.p_post, 0, gridDim.x, a.sum_post);
+  if (a.p_gate)
+    for (int64_t g = 0; g * a.seg.per_group < gridDim.x; ++g)
+      add(a.p_gate, g * a.seg.per_group, a.seg.per_group, a.sum_gate + g * a.d);
+}
 
 // One workgroup per segment of consecutive rows.  Its threads own columns, so the column sums
 // (weights, gate) stay in registers over the segment; the sums over a row are one exchange:
@@ -162,6 +200,7 @@ __global__ __launch_bounds__(ONE ? 64 : 1024, SHORT ? 1 : 4) void k_norm_bwd(Bwd
     if (a.p_pre) col.store(a.p_pre + seg * d, s_pre);
     if (a.p_post) col.store(a.p_post + seg * d, s_post);
     if (a.p_gate) col.store(a.p_gate + seg * d, s_tu);
+    if (a.counter) add_segments(a, col);
     return;
   }
   RowVec<S, SHORT, KIND, OUT == kBothStream> r, next;
@@ -251,6 +290,7 @@ __global__ __launch_bounds__(ONE ? 64 : 1024, SHORT ? 1 : 4) void k_norm_bwd(Bwd
   }
   if (a.p_pre) col.store(a.p_pre + seg * d, s_pre);
   if (a.p_post) col.store(a.p_post + seg * d, s_post);
+  if (a.counter) add_segments(a, col);
 }
 
 // Column sums of the segments' partials, in the segments' order within each of the 16 slices
@@ -362,11 +402,15 @@ hipError_t bwd_as(const NormBwd& p, hipStream_t st) {
   if (p.dw_pre) a.p_pre = part, part += per;
   if (p.dw_post) a.p_post = part, part += per;
   if (p.dgate && seg.per_group) a.p_gate = part;
+  const bool partials = a.p_pre || a.p_post || a.p_gate;
+  if (partials && seg.count <= kFewSegments && 3 * sizeof(float) * (size_t)per <= kFewBytes) {
+    a.counter = p.counter;
+    a.sum_pre = p.dw_pre, a.sum_post = p.dw_post, a.sum_gate = p.dgate;
+  }
   const hipError_t e = bwd_rows<S, ONE, SHORT>(a, p.gate && p.gate_rows == 1 ? kGateRows : kGateRuns, st);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || !partials || a.counter) return e;
   const int64_t groups = a.p_gate ? (p.M + p.gate_rows - 1) / p.gate_rows : 0;
   const int64_t job0 = a.p_pre ? 0 : (a.p_post ? 1 : 2), jobs = (groups ? 2 + groups : (a.p_post ? 2 : 1)) - job0;
-  if (!a.p_pre && !a.p_post && !groups) return hipSuccess;
   hipLaunchKernelGGL(k_norm_cols, dim3((unsigned)((p.d + kCols - 1) / kCols), (unsigned)jobs), dim3(kColThreads), 0,
                      st, a.p_pre, a.p_post, a.p_gate, p.dw_pre, p.dw_post, p.dgate, p.d, seg.count, seg.per_group,
                      job0);

@@ -33,6 +33,7 @@ struct NormBwd {
   void* dx;
   uint16_t *dy, *dw_post, *dgate, *dw_pre;
   float* part;
+  unsigned int* counter;
   int64_t M, d, gate_rows;
   float scale, eps;
   int f32, post;

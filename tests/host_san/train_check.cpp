@@ -56,7 +56,9 @@ void norms() {
                                            at<uint16_t>(12), at<uint16_t>(13), dgate, at<uint16_t>(14), at<void>(15), bytes,
                                            nullptr);
           };
-          run([&] { return bwd(need); }, 2, "norm bwd", M, d);
+          // few partials are added by the first launch itself
+          const size_t partials = need - QLORA_WS_COUNTER_BYTES, segments = partials / (12 * d);
+          run([&] { return bwd(need); }, segments <= 32 && partials <= 262144 ? 1 : 2, "norm bwd", M, d);
           CHECK(bwd(need - 1) == QLORA_ERR_WORKSPACE, "short workspace");
         }
 }

@@ -54,7 +54,8 @@ def _check(x, labels, ref, beta, smoothing, scale, out, grad=True):
     idx = np.where(counted, labels.numpy(), 0)
     np.put_along_axis(hot, idx[..., None], 1.0, axis=2)
     dc = abs(scale * beta) / P * 0.25 * np.concatenate([tol_z, tol_z])[:, None, None]
-    tol = np.abs(c)[:, None, None] * (p * (LP + 4 * U * np.abs(xn - m)) + 4 * U * hot) + (dc + 2 * U * np.abs(c)[:, None, None]) * np.abs(hot - p)
+    far = np.where(p > 0, np.abs(xn - m), 0.0)  # (-inf has probability 0)
+    tol = np.abs(c)[:, None, None] * (p * (LP + 4 * U * far) + 4 * U * hot) + (dc + 2 * U * np.abs(c)[:, None, None]) * np.abs(hot - p)
     rnd = UB if x.dtype == BF else U
     ok = np.abs(dg - d_r) <= tol + rnd * np.abs(d_r) + 1e-37
     assert np.all(ok[counted]) and np.all(dg[~counted] == 0)
@@ -169,6 +170,29 @@ def test_masked_vocabulary_and_extremes(gpu_lib, V, split):
         ref = T.token_logps(xn, labels[:7].numpy())
         assert np.all(np.abs(lp[:7] - ref) <= LP + 2 * U * np.abs(ref)), (dtype, lp[:7], ref)
         assert np.all(np.isnan(lp[7:10])) and np.all(lp[10:] == 0)
+
+
+def test_gradient_under_masked_vocabulary(gpu_lib):
+    """Entries of probability 0 get a gradient of 0, also where most of a row is -inf or the type's
+    lowest value; a row that is the lowest value throughout is uniform."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    for V in (300, 9001):
+        for dtype in (BF, F32):
+            x, labels, ref = _case(1, 4, V, dtype, masked=0.0)
+            low = torch.finfo(dtype).min
+            x[0, 0, 7:] = -float("inf")
+            labels[0, 0] = 3
+            x[0, 1, : V - 2] = low
+            labels[0, 1] = V - 1
+            x[1, 2] = low
+            x[1, 3, ::2] = low
+            labels[1, 3] = 1
+            out = Q.preference_loss(x.cuda(), labels.cuda(), ref.cuda(), 0.25)
+            torch.cuda.synchronize()
+            _check(x, labels, ref, 0.25, 0.0, 1.0, out)
+            d = out[3].float().cpu()
+            assert not d[0, 0, 7:].any() and not d[0, 1, : V - 2].any() and not d[1, 3, ::2].any()
 
 
 def test_infinite_differences(gpu_lib):
