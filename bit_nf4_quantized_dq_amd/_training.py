@@ -299,16 +299,13 @@ class GradList:
         self._ws_bytes = _size("qlora_grad_workspace_size", self._ref)
 
     def _describe(self, tensors, name):
-        kinds, numel = [], []
-        for i, t in enumerate(tensors):
-            kind = TYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
-            if kind is None or not t.is_contiguous():
-                raise ValueError(f"{name}[{i}]: need a contiguous bfloat16 or float32 tensor")
-            if not t.is_cuda or t.device != self.device:
-                raise ValueError(f"{name}[{i}]: need a CUDA tensor on {self.device}, got one on {t.device}")
-            kinds.append(kind)
-            numel.append(t.numel())
-        return kinds, numel
+        index = self.device.index if self.device is not None else None
+        kinds = [TYPES.get(t.dtype) if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == index
+                 and t.is_contiguous() else None for t in tensors]
+        if None in kinds:
+            i = kinds.index(None)
+            raise ValueError(f"{name}[{i}]: need a contiguous bfloat16 or float32 CUDA tensor on {self.device}")
+        return kinds, [t.numel() for t in tensors]
 
 
 def _grad_call(fn, grads, norm, ws, *args):

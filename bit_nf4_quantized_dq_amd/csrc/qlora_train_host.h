@@ -95,7 +95,7 @@ struct GradTensor {
   int64_t n, first;  // elements, first chunk
   int32_t in_f32, out_f32;
 };
-constexpr int kGradBatch = 64;  // tensors described by one launch's arguments
+constexpr int kGradBatch = 96;  // tensors described by one launch's arguments (under 4 KB)
 struct GradTensors {
   GradTensor t[kGradBatch];
 };

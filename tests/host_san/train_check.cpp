@@ -91,7 +91,7 @@ void losses() {
 }
 
 void gradients() {
-  for (int count : {0, 1, 63, 64, 65, 448}) {
+  for (int count : {0, 1, 95, 96, 97, 112, 448}) {
     std::vector<const void*> in(count);
     std::vector<void*> out(count);
     std::vector<int32_t> types(count), out_types(count);
@@ -113,7 +113,7 @@ void gradients() {
       run([&] {
         return qlora_gradlist_init(count, in.data(), types.data(), numel.data(), place ? nullptr : out.data(),
                                    place ? nullptr : out_types.data(), at<void>(3000), bytes, &list, nullptr);
-      }, (size_t)(full + 63) / 64, "list", count, place);
+      }, (size_t)(full + 95) / 96, "list", count, place);
       CHECK((size_t)list.chunks * 24 == bytes, "chunks");
       size_t ws = 0;
       CHECK(qlora_grad_workspace_size(&list, &ws) == QLORA_OK, "workspace");
