@@ -27,8 +27,8 @@ __global__ __launch_bounds__(kThreads) void k_grad_table(GradTensors batch, Grad
   }
 }
 
-// Sum of the squares of a wavefront's piece [p, p + n): 64 elements a lane, all in flight at once.
-constexpr int kPiece = 4096, kPieces = (int)(kGradChunk / kPiece), kPieceVecs = kPiece / (8 * 64);
+// Sum of the squares of a wavefront's piece [p, p + n): 32 elements a lane, all in flight at once.
+constexpr int kPiece = 2048, kPieces = (int)(kGradChunk / kPiece), kPieceVecs = kPiece / (8 * 64);
 
 template <class E>
 __device__ __forceinline__ double piece_sum(const E* __restrict__ p, int32_t n, bool wide, double sum) {
