@@ -119,8 +119,10 @@ NormSegments norm_segments(int64_t M, int64_t d, int64_t gate_rows) {
 }
 
 RowSplit row_split(int64_t rows, int64_t V) {
-  // whole rows from 1024 rows on; below that, parts of at least 8192 elements
-  const int64_t want = rows >= 1024 ? 1 : (2048 + rows - 1) / rows;
+  // Whole rows from 128 rows on: 160 of 131072 entries 24 us with the gradient, 27.6 in parts, 400
+  // of 32768 18.8 and 22.  Fewer leave compute units idle and are split into parts of at least
+  // 8192 elements.
+  const int64_t want = rows >= 128 ? 1 : (2048 + rows - 1) / rows;
   const int64_t parts = std::max<int64_t>(1, std::min(want, V / 8192));
   const int64_t len = ((V + parts - 1) / parts + 7) / 8 * 8;
   return RowSplit{(V + len - 1) / len, len};

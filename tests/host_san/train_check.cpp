@@ -83,7 +83,7 @@ void losses() {
         }
         const int64_t rows = 2 * pairs * S;
         CHECK(qlora_logps_workspace_size(rows, V, &need) == QLORA_OK, "size");
-        const size_t launches = rows >= 1024 || V < 2 * 8192 ? 1 : 2;
+        const size_t launches = rows >= 128 || V < 2 * 8192 ? 1 : 2;
         run([&] {
           return qlora_token_logps(at<void>(1), at<int64_t>(2), rows, V, type, at<float>(3), at<void>(8), need, nullptr);
         }, launches, "logps", rows, V);
