@@ -59,10 +59,13 @@ def _lib() -> ctypes.CDLL:
 # the marshalling below avoids what costs one on the host: the stream's handle is asked for
 # directly (0.1 us; through a Stream object 2 us), and what is right passes a short check.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_BF16, _F32, _I64 = torch.bfloat16, torch.float32, torch.int64
 
 
-def _stream(t: torch.Tensor) -> int:
-    return _raw_stream(t.get_device())
+def _right(t, dtype, shape, index) -> bool:
+    """A contiguous tensor of that dtype and shape on that GPU (one on the CPU has the number -1)."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous())
 
 
 def _tensors(specs, device) -> None:
@@ -70,21 +73,19 @@ def _tensors(specs, device) -> None:
     if device is not None and device.type == "cuda":
         index = device.index
         for t, dtype, _, shape in specs:
-            # (a tensor on the CPU has the device number -1)
-            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
-                    and t.is_contiguous()):
+            if not _right(t, dtype, shape, index):
                 break
         else:
             return
     _validate(specs, device)
 
 
-def _workspace(ws, nbytes: int, t: torch.Tensor, stream: int) -> torch.Tensor:
+def _workspace(ws, nbytes: int, t: torch.Tensor, index: int, stream: int) -> torch.Tensor:
     """The caller's workspace, checked, or the binding's own for this device and stream."""
     if ws is not None:
         _check_ws(ws, t.device)
         return ws
-    buf = _WS._bufs.get((t.get_device(), stream, "train"))
+    buf = _WS._bufs.get((index, stream, "train"))
     return buf if buf is not None and buf.numel() >= nbytes else _WS.get(nbytes, t.device, "train")
 
 
@@ -146,23 +147,32 @@ def norm_residual_fwd(x: torch.Tensor, y: torch.Tensor | None = None, *, post_no
     kind = _type(x, "x")
     if x.dim() != 2:
         raise ValueError("x: need a 2-D [M, d] tensor")
-    M, d = x.shape
-    dev = x.device
-    specs = _norm_specs(x, y, w_post, gate, gate_rows, w_pre, M, d, "x")
-    if x_out is not None:
-        specs.append((x_out, x.dtype, "x_out", (M, d)))
-    if h is not None:
-        if not pre_norm:
-            raise ValueError("h: given without pre_norm")
-        specs.append((h, torch.bfloat16, "h", (M, d)))
-    _tensors(specs, dev)
+    shape = M, d = x.shape
+    index = x.get_device()
+    if not (index >= 0 and x.is_contiguous() and (y is None or _right(y, _BF16, shape, index))
+            and (w_post is None or _right(w_post, _BF16, (d,), index)) and (w_pre is None or _right(w_pre, _BF16, (d,), index))
+            and (gate is None or (gate_rows >= 1 and _right(gate, _BF16, (-(-M // gate_rows), d), index)))
+            and (x_out is None or _right(x_out, x.dtype, shape, index))
+            and (h is None or (pre_norm and _right(h, _BF16, shape, index)))):
+        specs = _norm_specs(x, y, w_post, gate, gate_rows, w_pre, M, d, "x")
+        if x_out is not None:
+            specs.append((x_out, x.dtype, "x_out", (M, d)))
+        if h is not None:
+            if not pre_norm:
+                raise ValueError("h: given without pre_norm")
+            specs.append((h, _BF16, "h", (M, d)))
+        _validate(specs, x.device)
     if x_out is None:
         x_out = torch.empty_like(x)
     if pre_norm and h is None:
-        h = torch.empty(M, d, dtype=torch.bfloat16, device=dev)
-    _check(_lib().qlora_norm_residual_fwd(x.data_ptr(), _ptr(y), M, d, kind, int(post_norm), _ptr(w_post), _ptr(gate),
-                                          int(gate_rows), _ptr(w_pre), res_scale, eps, x_out.data_ptr(), _ptr(h),
-                                          _stream(x)), "norm_residual_fwd")
+        h = torch.empty_like(x, dtype=_BF16) if y is None else torch.empty_like(y)
+    status = _lib().qlora_norm_residual_fwd(
+        x.data_ptr(), None if y is None else y.data_ptr(), M, d, kind, post_norm,
+        None if w_post is None else w_post.data_ptr(), None if gate is None else gate.data_ptr(), gate_rows,
+        None if w_pre is None else w_pre.data_ptr(), res_scale, eps, x_out.data_ptr(),
+        None if h is None else h.data_ptr(), _raw_stream(index))
+    if status:
+        _check(status, "norm_residual_fwd")
     return x_out, h
 
 
@@ -182,13 +192,18 @@ def norm_residual_bwd(x_out: torch.Tensor | None, y: torch.Tensor | None, dh: to
     kind = _type(stream, "x_out")
     if stream.dim() != 2:
         raise ValueError("x_out: need a 2-D [M, d] tensor")
-    M, d = stream.shape
-    dev, bf16 = stream.device, torch.bfloat16
-    specs = _norm_specs(x_out, y, w_post, gate, gate_rows, w_pre, M, d, "x_out")
-    for t, dtype, name in ((dh, bf16, "dh"), (dx_out, stream.dtype, "dx_out"), (dx, stream.dtype, "dx"), (dy, bf16, "dy")):
-        if t is not None:
-            specs.append((t, dtype, name, (M, d)))
-    _tensors(specs, dev)
+    shape = M, d = stream.shape
+    index, dtype = stream.get_device(), stream.dtype
+    if not (index >= 0 and stream.is_contiguous() and (y is None or _right(y, _BF16, shape, index))
+            and (dh is None or _right(dh, _BF16, shape, index)) and (dx_out is None or _right(dx_out, dtype, shape, index))
+            and (w_post is None or _right(w_post, _BF16, (d,), index)) and (w_pre is None or _right(w_pre, _BF16, (d,), index))
+            and (gate is None or (gate_rows >= 1 and _right(gate, _BF16, (-(-M // gate_rows), d), index)))
+            and (dx is None or _right(dx, dtype, shape, index)) and (dy is None or _right(dy, _BF16, shape, index))):
+        specs = _norm_specs(x_out, y, w_post, gate, gate_rows, w_pre, M, d, "x_out")
+        for t, kind_of, name in ((dh, _BF16, "dh"), (dx_out, dtype, "dx_out"), (dx, dtype, "dx"), (dy, _BF16, "dy")):
+            if t is not None:
+                specs.append((t, kind_of, name, (M, d)))
+        _validate(specs, stream.device)
     if dx is None:
         dx = torch.empty_like(stream)
     if y is not None and dy is None:
@@ -196,13 +211,18 @@ def norm_residual_bwd(x_out: torch.Tensor | None, y: torch.Tensor | None, dh: to
     dw_post = torch.empty_like(w_post) if w_post is not None and need_weights else None
     dw_pre = torch.empty_like(w_pre) if w_pre is not None and need_weights else None
     dgate = torch.empty_like(gate) if gate is not None and need_gate else None
-    rows = int(gate_rows) if gate is not None else 0
-    st = _stream(stream)
-    ws = _workspace(ws, norm_residual_workspace_size(M, d, rows), stream, st)
-    _check(_lib().qlora_norm_residual_bwd(_ptr(x_out), _ptr(y), _ptr(dh), _ptr(dx_out), M, d, kind, int(post_norm),
-                                          _ptr(w_post), _ptr(gate), rows, _ptr(w_pre), res_scale, eps, dx.data_ptr(),
-                                          _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), ws.data_ptr(),
-                                          ws.numel(), st), "norm_residual_bwd")
+    rows = gate_rows if gate is not None else 0
+    st = _raw_stream(index)
+    ws = _workspace(ws, norm_residual_workspace_size(M, d, rows), stream, index, st)
+    status = _lib().qlora_norm_residual_bwd(
+        None if x_out is None else x_out.data_ptr(), None if y is None else y.data_ptr(),
+        None if dh is None else dh.data_ptr(), None if dx_out is None else dx_out.data_ptr(), M, d, kind, post_norm,
+        None if w_post is None else w_post.data_ptr(), None if gate is None else gate.data_ptr(), rows,
+        None if w_pre is None else w_pre.data_ptr(), res_scale, eps, dx.data_ptr(), None if dy is None else dy.data_ptr(),
+        None if dw_post is None else dw_post.data_ptr(), None if dgate is None else dgate.data_ptr(),
+        None if dw_pre is None else dw_pre.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check(status, "norm_residual_bwd")
     return dx, dy, dw_post, dgate, dw_pre
 
 
@@ -220,11 +240,14 @@ def token_logps(logits: torch.Tensor, labels: torch.Tensor, logps: torch.Tensor 
     _tensors(specs, dev)
     rows = labels.numel()
     if logps is None:
-        logps = torch.empty(lead, dtype=torch.float32, device=dev)
-    st = _stream(logits)
-    ws = _workspace(ws, logps_workspace_size(rows, V), logits, st)
-    _check(_lib().qlora_token_logps(logits.data_ptr(), labels.data_ptr(), rows, V, kind, logps.data_ptr(),
-                                    ws.data_ptr(), ws.numel(), st), "token_logps")
+        logps = torch.empty_like(labels, dtype=_F32)
+    index = logits.get_device()
+    st = _raw_stream(index)
+    ws = _workspace(ws, logps_workspace_size(rows, V), logits, index, st)
+    status = _lib().qlora_token_logps(logits.data_ptr(), labels.data_ptr(), rows, V, kind, logps.data_ptr(),
+                                      ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check(status, "token_logps")
     return logps
 
 
@@ -242,24 +265,31 @@ def preference_loss(logits: torch.Tensor, labels: torch.Tensor, ref_logps: torch
         raise ValueError("logits: need [2 pairs, S, V]")
     n, S, V = logits.shape
     dev = logits.device
-    specs = [(logits, logits.dtype, "logits", (n, S, V)), (labels, torch.int64, "labels", (n, S))]
-    if ref_logps is not None:
-        specs.append((ref_logps, torch.float32, "ref_logps", (n, S)))
-    if dlogits is not None:
-        if not need_grad:
-            raise ValueError("dlogits: given with need_grad=False")
-        specs.append((dlogits, logits.dtype, "dlogits", (n, S, V)))
-    _tensors(specs, dev)
-    loss = torch.empty(1, dtype=torch.float32, device=dev)
-    log_ratios = torch.empty(n, dtype=torch.float32, device=dev)
-    logps = torch.empty(n, S, dtype=torch.float32, device=dev)
+    index = logits.get_device()
+    if not (index >= 0 and logits.is_contiguous() and _right(labels, _I64, (n, S), index)
+            and (ref_logps is None or _right(ref_logps, _F32, (n, S), index))
+            and (dlogits is None or (need_grad and _right(dlogits, logits.dtype, logits.shape, index)))):
+        specs = [(logits, logits.dtype, "logits", (n, S, V)), (labels, _I64, "labels", (n, S))]
+        if ref_logps is not None:
+            specs.append((ref_logps, _F32, "ref_logps", (n, S)))
+        if dlogits is not None:
+            if not need_grad:
+                raise ValueError("dlogits: given with need_grad=False")
+            specs.append((dlogits, logits.dtype, "dlogits", (n, S, V)))
+        _validate(specs, dev)
+    loss = torch.empty(1, dtype=_F32, device=dev)
+    log_ratios = torch.empty(n, dtype=_F32, device=dev)
+    logps = torch.empty_like(labels, dtype=_F32)
     if need_grad and dlogits is None:
         dlogits = torch.empty_like(logits)
-    st = _stream(logits)
-    ws = _workspace(ws, preference_workspace_size(n // 2, S, V), logits, st)
-    _check(_lib().qlora_preference_loss(logits.data_ptr(), labels.data_ptr(), _ptr(ref_logps), n // 2, S, V, kind,
-                                        beta, label_smoothing, grad_scale, loss.data_ptr(), log_ratios.data_ptr(),
-                                        logps.data_ptr(), _ptr(dlogits), ws.data_ptr(), ws.numel(), st), "preference_loss")
+    st = _raw_stream(index)
+    ws = _workspace(ws, preference_workspace_size(n // 2, S, V), logits, index, st)
+    status = _lib().qlora_preference_loss(
+        logits.data_ptr(), labels.data_ptr(), None if ref_logps is None else ref_logps.data_ptr(), n // 2, S, V, kind, beta,
+        label_smoothing, grad_scale, loss.data_ptr(), log_ratios.data_ptr(), logps.data_ptr(),
+        None if dlogits is None else dlogits.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check(status, "preference_loss")
     return loss, log_ratios, logps, dlogits
 
 
@@ -294,7 +324,7 @@ class GradList:
         self._struct = _GradListStruct()
         _check(_lib().qlora_gradlist_init(n, ptrs, (ctypes.c_int32 * n)(*kinds), sizes, out_ptrs, out_kinds,
                                           self.table.data_ptr() or None, self.table.numel(), ctypes.byref(self._struct),
-                                          _stream(self.table)), "gradlist_init")
+                                          _raw_stream(self.table.get_device())), "gradlist_init")
         self._ref = ctypes.byref(self._struct)
         self._ws_bytes = _size("qlora_grad_workspace_size", self._ref)
 
@@ -313,12 +343,14 @@ def _grad_call(fn, grads, norm, ws, *args):
         raise ValueError("grads: need a GradList")
     dev = grads.device
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        norm = torch.empty(1, dtype=_F32, device=dev)
     else:
-        _tensors([(norm, torch.float32, "norm", (1,))], dev)
-    st = _stream(norm)
-    ws = _workspace(ws, grads._ws_bytes, norm, st)
-    _check(getattr(_lib(), fn)(grads._ref, *args, norm.data_ptr(), ws.data_ptr(), ws.numel(), st), fn[len("qlora_"):])
+        _tensors([(norm, _F32, "norm", (1,))], dev)
+    st = _raw_stream(dev.index)
+    ws = _workspace(ws, grads._ws_bytes, norm, dev.index, st)
+    status = getattr(_lib(), fn)(grads._ref, *args, norm.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    if status:
+        _check(status, fn[len("qlora_"):])
     return norm
 
 
@@ -351,5 +383,6 @@ def adamw_step_clipped(master: torch.Tensor, m: torch.Tensor, v: torch.Tensor, g
         raise ValueError("adamw_step_clipped: all buffers need the same number of elements")
     _check(_lib().qlora_adamw_step_clipped(master.data_ptr(), m.data_ptr(), v.data_ptr(), grad.data_ptr(), _ptr(param),
                                            n, int(step), float(lr), float(beta1), float(beta2), float(eps),
-                                           float(weight_decay), norm.data_ptr(), float(max_norm), _stream(master)),
+                                           float(weight_decay), norm.data_ptr(), float(max_norm),
+                                           _raw_stream(master.get_device())),
            "adamw_step_clipped")

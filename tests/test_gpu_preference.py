@@ -80,7 +80,7 @@ def test_sizes(gpu_lib, P, S, V, dtype):
 
 @pytest.mark.parametrize("V", [33000, 66000, 131072, 140000])
 def test_wide_rows_in_whole(gpu_lib, V):
-    """1024 rows or more are not split: every workgroup size, and the elements after the batches."""
+    """Many rows are not split: every workgroup size, and the elements after the batches."""
     import bit_nf4_quantized_dq_amd as Q
 
     P, S = 2, 256
