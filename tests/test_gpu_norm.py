@@ -230,6 +230,28 @@ def test_special_rows(gpu_lib):
         assert not torch.isfinite(xo[5, 1000]) and torch.isnan(h[5, 1000])
 
 
+@pytest.mark.parametrize("M,d,rows", [(1, 700, 1), (1, 1280, 7), (1, 300, 7), (5, 1280, 5), (11, 700, 11), (11, 300, 4)])
+@pytest.mark.parametrize("what", ["w_post", "gate"])
+def test_infinite_weight_stays_in_its_sums(gpu_lib, what, M, d, rows):
+    """An infinite post-norm weight or gate: the sum it multiplies is infinite in its column (over
+    several rows the terms' signs may differ: not a number), and what does not pass through it is
+    finite, for row counts that leave wavefronts without a row."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    c, _ = _case(M, d, BF, True, rows)
+    g = _cuda(c)
+    g[what].view(-1)[d // 2] = float("inf")
+    kw = dict(post_norm=True, w_post=g["w_post"], gate=g["gate"], gate_rows=rows, w_pre=g["w_pre"])
+    _, _, dw_post, dgate, dw_pre = Q.norm_residual_bwd(g["x"], g["y"], g["dh"], g["dxo"], **kw)
+    torch.cuda.synchronize()
+    at = (slice(None), d // 2)
+    hit, miss = (dgate, dw_post) if what == "w_post" else (dw_post, dgate)
+    hit = hit.view(-1, d)
+    assert torch.isinf(hit[at]).all() if M == 1 else not torch.isfinite(hit[at]).any()
+    hit[at] = 0
+    assert all(torch.isfinite(v).all() for v in (hit, miss, dw_pre))
+
+
 def test_same_bits_again_on_another_stream_and_in_a_graph(gpu_lib):
     import bit_nf4_quantized_dq_amd as Q
 
