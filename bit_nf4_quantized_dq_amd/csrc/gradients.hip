@@ -4,9 +4,9 @@
 // The list is a table in device memory with one entry per 16384 elements of a tensor, so one
 // launch covers any number of tensors and no workgroup searches for its own.
 //
-// HBM bounds both kernels.  Measured (MI355X): the norm of 448 tensors, 41.9M elements, 16 - 23 us
-// in BF16 (84 MB) and 32 us in FP32 (168 MB, 5.3 TB/s; a plain read reaches 7.0), of 14 tensors
-// (2.6 MB) 4.7 us on the device; clipping the FP32 list into BF16 37 us more (6.8 TB/s: the
+// HBM bounds both kernels.  Measured (MI355X): the norm of 448 tensors, 41.9M elements, 17 us
+// in BF16 (84 MB; 23 - 29 right after an optimizer step) and 32 us in FP32 (168 MB, 5.3 TB/s; a
+// plain read reaches 7.0), of 14 tensors (2.6 MB) 4.7 us on the device; clipping the FP32 list into BF16 37 us more (6.8 TB/s: the
 // cache still holds what the norm has read; results are written past it, 70 us for both
 // kernels instead of 80, and 8 us less also with the optimizer step that reads them).
 // Squares and sums are FP64: a conversion and a multiply-add an element stay below the load's
