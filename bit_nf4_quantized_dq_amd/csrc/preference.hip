@@ -112,11 +112,13 @@ __global__ __launch_bounds__(T) void k_row_stats(const E* __restrict__ logits,
   const Span span(x + v0, v1 - v0);
   const int32_t full = span.full, batches = full / (kUnroll * T);
   const E* xp = x + v0 + span.head;
-  // Batches of 32 elements a thread.  The exponentials are 2^(x log2 e - n) with a whole number n
-  // just above the maximum's x log2 e: the product is not rounded before n leaves it, so this
-  // is one operation for the difference and the factor, and changes of n scale exactly.  n
-  // stays above kLow: elements below it (masked by -inf or the type's lowest value) add zero.
-  constexpr float kLow = -1.5e30f;
+  // Batches of 32 elements a thread.  The exponentials are 2^(x log2 e - n) with a whole number n:
+  // the product is not rounded before n leaves it, so this is one operation for the difference
+  // and the factor, and changes of n scale exactly.  n is taken from the rounded product of the
+  // maximum, which below 2^23 is off by at most 1/4: n is the maximum's x log2 e or just above
+  // it.  (From 2^32 on the rounding passes the range of exp2.)  n stays above kLow: elements below
+  // it (masked by a large negative number, -inf or the type's lowest value) add zero.
+  constexpr float kLow = -8388608.f;
   float n = kLow;
   for (int32_t i = 0; i < batches; ++i) {
     Raw8<E> r[kUnroll];
@@ -134,11 +136,12 @@ __global__ __launch_bounds__(T) void k_row_stats(const E* __restrict__ logits,
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += exp2_hw(fmaf(r[u].get(j), kLog2e, -n));
   }
-  // from n to the maximum itself; a thread that met nothing above kLow keeps only a NaN
-  constexpr float kHuge = 1e30f;
+  // From n to the maximum itself.  A thread whose maximum is not within kHuge (times log2 e that
+  // stays below 2^23) keeps only a NaN: beside a row's maximum above -kHuge / 2 it adds zero.
+  constexpr float kHuge = 4194304.f;
   if (batches) s = fabsf(m) < kHuge ? s * exp2_hw(fmaf(-m, kLog2e, n)) : (s != s ? s : 0.f);
-  // A maximum too large for that (infinite, or of a row that is masked throughout): the batches
-  // once more, each difference before its factor.
+  // Any other maximum (large, infinite, or of a row that is masked throughout): the batches once
+  // more, each difference before its factor.
   if (__syncthreads_or(batches && !(fabsf(m) < kHuge))) {
     float top = m;
 #pragma unroll
@@ -147,7 +150,7 @@ __global__ __launch_bounds__(T) void k_row_stats(const E* __restrict__ logits,
     __syncthreads();
     for (int w = 0; w < T / 64; ++w) top = fmaxf(top, lm[w]);
     __syncthreads();
-    if (!(fabsf(top) < kHuge)) {
+    if (!(top > -0.5f * kHuge && top < kHuge)) {
       m = -INFINITY, s = 0.f;
       for (int32_t i = threadIdx.x; i < batches * kUnroll * T; i += T) {
         Raw8<E> r;

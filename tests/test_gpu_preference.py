@@ -306,3 +306,85 @@ def test_slope_of_the_gpu_loss(gpu_lib):
     slope = (f(x + e * v) - f(x - e * v)) / (2 * e)
     torch.cuda.synchronize()
     assert abs(float((d.double() * v.double()).sum()) - slope) <= 4 * U * 5 / (2 * e) + 0.02 * float(d.norm())
+
+
+MASKS = (-1e9, -5e9, -1e10, -1e20, -1e29, -1e30)
+TOPS = (5e9, 1e10, 1e20)
+BASES = tuple(s * b for b in (2e6, 2.0**21, 2.0**22 - 1, 2.0**22, 2.0**22 + 1, 2.0**23, 1e7, 3e9) for s in (1, -1))
+
+
+def _finite_masks(V, gen):
+    """Rows of finite logits of any magnitude, and a label for each: entries masked by a large
+    negative number in the first columns, all but four, every second one, or all; one entry far
+    above the others; whole rows far from zero, in steps of one and in stripes of eight columns
+    that differ by three (neighbouring threads' vectors)."""
+    rows, labels = [], []
+
+    def add(x, label):
+        rows.append(x)
+        labels.append(int(label))
+
+    for k, v in enumerate(MASKS):
+        few = torch.randperm(V, generator=gen)[:4]
+        keeps = (torch.arange(V) >= V - 4, torch.zeros(V, dtype=torch.bool).index_fill(0, few, True),
+                 torch.arange(V) % 2 == 1, torch.zeros(V, dtype=torch.bool))
+        for keep in keeps:
+            x = torch.where(keep, 2 * torch.randn(V, generator=gen), torch.full((V,), v))
+            left = keep.nonzero()[:, 0]
+            add(x, left[k % len(left)] if len(left) else V // 2)
+        add(rows[-4], 1)  # a label that is masked
+    for v in TOPS:
+        x = 2 * torch.randn(V, generator=gen)
+        x[V // 3] = v
+        add(x, V // 3)
+        add(x, 7)
+    for b in BASES:
+        add(b + torch.randint(-6, 7, (V,), generator=gen).float(), V - 1)
+        add(b + 1 - 3 * (torch.arange(V) // 8 % 2).float(), 3)
+    return torch.stack(rows), torch.tensor(labels)
+
+
+@pytest.mark.parametrize("rows,V", [(1024, 2051), (1024, 5000), (256, 40000), (256, 66000), (160, 140000), (100, 20000),
+                                    (100, 140000)])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_finite_logits_of_any_magnitude(gpu_lib, rows, V, dtype):
+    """Finite logits give finite log-probabilities, for every workgroup size, whole rows and split
+    ones (fewer than 128), and masks that leave most threads nothing."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    print(f"token logps rows={rows} V={V}", flush=True)
+    x, at = _finite_masks(V, torch.Generator().manual_seed(V))
+    n = len(x)
+    assert n <= rows
+    x = torch.cat([x, torch.zeros(rows - n, V)]).to(dtype)
+    labels = torch.cat([at, torch.full((rows - n,), -100)])
+    lp = Q.token_logps(x.cuda(), labels.cuda()).double().cpu().numpy()
+    torch.cuda.synchronize()
+    ref = T.token_logps(x[:n].double().numpy(), at.numpy())
+    bad = np.nonzero(~(np.abs(lp[:n] - ref) <= LP + 2 * U * np.abs(ref)))[0]
+    assert len(bad) == 0, [(int(i), lp[i], ref[i]) for i in bad[:5]]
+    assert np.all(lp[n:] == 0)
+
+
+@pytest.mark.parametrize("S,V", [(3, 2051), (80, 2051), (80, 9001), (3, 20000)])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_gradient_under_finite_masks(gpu_lib, S, V, dtype):
+    """The same rows in a pair: loss and gradient, in place too (rows below 128 in all are split)."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    print(f"preference S={S} V={V}", flush=True)
+    rows, at = _finite_masks(V, torch.Generator().manual_seed(V + 1))
+    top = rows.gather(1, at[:, None])[:, 0] >= rows.amax(1) - 30  # labels that are not masked away
+    rows, at = rows[top], at[top]
+    for first in range(0, len(rows), 2 * S):
+        x, labels, ref = _case(1, S, V, F32, masked=0.2)
+        take = rows[first:first + 2 * S]
+        x.view(-1, V)[:len(take)] = take
+        labels.view(-1)[:len(take)] = at[first:first + 2 * S]
+        x = x.to(dtype)
+        out = Q.preference_loss(x.cuda(), labels.cuda(), ref.cuda(), 0.25)
+        y = x.cuda()
+        place = Q.preference_loss(y, labels.cuda(), ref.cuda(), 0.25, dlogits=y)
+        torch.cuda.synchronize()
+        _check(x, labels, ref, 0.25, 0.0, 1.0, out)
+        assert all(torch.equal(a, b) for a, b in zip(out, place))
