@@ -181,7 +181,9 @@ __device__ void add_segments(const BwdArgs<S>& a, const Columns<SHORT>& col) {
 
 // One workgroup per segment of rows.  Its threads own columns, so the column sums (weights, gate)
 // stay in registers over the segment; the sums over a row are one exchange: with q = g w_post y,
-// sum(b y) = sum(dx' q) + r_x sum(a q) - k sum(x' q),  k = r_x^3 mean(a x').
+// sum(b y) = sum(dx' q) + r_x sum(a q) - k r_x sum(x' q),  k = r_x^2 mean(a x').  The third factor
+// r_x goes to x' itself (and r_y's to y): u = r_x x' is of order one, and no cube of a row's
+// norm leaves FP32's range before what it multiplies brings it back.
 // An operand that is not given is zeros, a weight or gate that is not given is ones, so the
 // arithmetic has no cases.
 // What keeps it below the forward's rate: four wavefronts a SIMD (24 sums, two rows and the
@@ -260,24 +262,24 @@ __global__ __launch_bounds__(ONE ? 64 : 1024, SHORT ? 1 : 4) void k_norm_bwd(Bwd
     block_sum<ONE>(s, lds[odd]);
     opaque(w_pre), opaque(w_post), r.pack();
     const float r_x = a.h_bits ? 1.f / sqrtf(s[0] * a.inv_d + a.eps) : 0.f;
-    const float k = a.h_bits ? r_x * r_x * r_x * (s[1] * a.inv_d) : 0.f;
+    const float k = a.h_bits ? r_x * (r_x * (s[1] * a.inv_d)) : 0.f;
     const float r_y = post ? 1.f / sqrtf(s[2] * a.inv_d + a.eps) : 1.f;
-    const float c = post ? r_y * r_y * r_y * ((s[3] + r_x * s[4] - k * s[5]) * a.inv_d) : 0.f;
+    const float c = post ? r_y * (r_y * ((s[3] + r_x * s[4] - k * (r_x * s[5])) * a.inv_d)) : 0.f;
     float t[8], o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float xi = r.x.get(i), dhi = r.dh.get(i);
-      t[i] = r.dxo.get(i) + (r_x * (dhi * w_pre.get(i)) - xi * k);
-      s_pre[i] = fmaf(dhi, xi * r_x, s_pre[i]);
+      const float ui = r.x.get(i) * r_x, dhi = r.dh.get(i);
+      t[i] = r.dxo.get(i) + (r_x * (dhi * w_pre.get(i)) - ui * k);
+      s_pre[i] = fmaf(dhi, ui, s_pre[i]);
       o[i] = a.scale * t[i];
     }
     if (OUT != kAny || a.dx) col.store(a.dx + at, o);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float yi = r.y.get(i);
-      s_tu[i] = fmaf(t[i], yi * r_y, s_tu[i]);
-      o[i] = r_y * (t[i] * r.g.get(i) * w_post.get(i)) - __uint_as_float(__float_as_uint(yi) & post_bits) * c;
+      const float vi = r.y.get(i) * r_y;
+      s_tu[i] = fmaf(t[i], vi, s_tu[i]);
+      o[i] = r_y * (t[i] * r.g.get(i) * w_post.get(i)) - __uint_as_float(__float_as_uint(vi) & post_bits) * c;
     }
     if (OUT != kAny || a.dy) col.store(a.dy + at, o);
     const Raw8<uint16_t> g = r.g;

@@ -33,6 +33,8 @@ enum qlora_type { QLORA_BF16 = 0, QLORA_F32 = 1 };
  *     x' = res_scale * x + g n      the residual stream after the block
  *     h  = x' / rms(x') * w_pre     the next block's input
  * x' is rounded once to the stream's type; h is formed from x' before that rounding.
+ * A row's sum of squares is FP32: exact to rounding while it and its mean lie within 1e-37 .. 1e38
+ * (elements of about 1e-18 to 1e17 at any width); above that a row norms to zeros.
  *   x, x_out: [M, d] of `type` (QLORA_BF16 or QLORA_F32); x_out may be x, or NULL (not written).
  *   y: BF16 [M, d], the block's output, or NULL: the block adds nothing (then no post_norm,
  *      w_post or gate).  h: BF16 [M, d], or NULL: no norm before a next block.

@@ -310,3 +310,25 @@ def test_slope_of_the_gpu_forward(gpu_lib):
     noise = 4 * UB * float((h.double() * g["dh"].double()).square().sum().sqrt()) / e
     scale = float(dx.double().square().sum().sqrt())
     assert abs(float((dx.double() * v.double()).sum()) - slope) <= noise + 0.01 * scale
+
+
+@pytest.mark.parametrize("M,d", [(9, 5), (19, 200), (40, 2051)])
+@pytest.mark.parametrize("scale,eps", [(1e15, 1e-5), (1e17, 0.0), (1e-14, 0.0), (1e-17, 0.0)])
+@pytest.mark.parametrize("stream", [BF, F32], ids=["bf16", "f32"])
+def test_rows_of_any_magnitude(gpu_lib, M, d, scale, eps, stream):
+    """Rows whose squares FP32 holds, whatever the cube of their norm: no gradient's term is lost or
+    overflows, with and without a gradient from later blocks (which would hide small ones)."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    print(f"norm M={M} d={d} scale={scale}", flush=True)
+    for post in (True, False):
+        c, rows = _case(M, d, stream, post, 4, scale=scale)
+        for dxo in (c["dxo"], None):
+            c["dxo"] = dxo
+            g = _cuda(c)
+            kw = dict(post_norm=post, w_post=g["w_post"], gate=g["gate"], gate_rows=rows, w_pre=g["w_pre"], eps=eps)
+            xo, h = Q.norm_residual_fwd(g["x"], g["y"], **kw)
+            got = Q.norm_residual_bwd(g["x"], g["y"], g["dh"], g["dxo"], **kw)
+            torch.cuda.synchronize()
+            _check_fwd(c, rows, post, 1.0, np.float32(eps), xo, h)
+            _check_bwd(c, rows, post, 1.0, np.float32(eps), got)
