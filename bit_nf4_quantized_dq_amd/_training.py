@@ -58,7 +58,8 @@ def _lib() -> ctypes.CDLL:
 # The small calls here take a few microseconds on the device, about as long as their checks, so
 # the marshalling below avoids what costs one on the host: the stream's handle is asked for
 # directly (0.1 us; through a Stream object 2 us), and what is right passes a short check.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (A CPU build of torch lacks it; every call has refused its tensors by then.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _BF16, _F32, _I64 = torch.bfloat16, torch.float32, torch.int64
 
 

@@ -5,6 +5,8 @@ touched: the pointers here are never dereferenced)."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -178,3 +180,15 @@ def test_python_refusals():
         with pytest.raises(ValueError):
             f()
             raise AssertionError(i)
+
+
+def test_package_imports_on_a_torch_without_gpu_support():
+    """A CPU build of torch has no stream functions: the package still imports (its generators and
+    codebooks need no GPU), and the operators refuse as they do for any CPU tensor."""
+    code = ("import torch\n"
+            "del torch._C._cuda_getCurrentRawStream\n"
+            "import bit_nf4_quantized_dq_amd as Q\n"
+            "x = torch.zeros(4, 8)\n"
+            "try:\n    Q.norm_residual_fwd(x)\nexcept ValueError:\n    print('refused')\n")
+    out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "refused", out.stderr
