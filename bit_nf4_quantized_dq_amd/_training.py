@@ -12,7 +12,6 @@ import torch
 from ._binding import _check, _check_ws, _ptr, _validate, _WS, load_library
 
 TYPES = {torch.bfloat16: 0, torch.float32: 1}
-NORM_MAX_WIDTH = 8192
 
 
 class _GradListStruct(ctypes.Structure):
@@ -372,7 +371,8 @@ def adamw_step_clipped(master: torch.Tensor, m: torch.Tensor, v: torch.Tensor, g
                        beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
                        param: torch.Tensor | None = None) -> None:
     """adamw_step with grad scaled by min(1, max_norm / (norm + 1e-6)) as it is read; norm is the
-    FP32 [1] tensor of grad_norm.  A norm that is not finite skips the step."""
+    FP32 [1] tensor of grad_norm.  A norm that is not finite skips the step.  Slices of flat
+    buffers start at multiples of four elements (16-byte aligned FP32, 8-byte aligned BF16)."""
     n = master.numel() if isinstance(master, torch.Tensor) else 0
     dev = master.device if isinstance(master, torch.Tensor) else None
     specs = [(t, torch.float32, name, getattr(t, "shape", None)) for t, name in ((master, "master"), (m, "m"), (v, "v"))]

@@ -9,8 +9,9 @@
  * on `stream` without synchronization, no device memory allocated, and workspaces whose first
  * QLORA_WS_COUNTER_BYTES bytes are zero before their first use and left zero by every call (one
  * workspace serves calls of any kind; calls that share one must not overlap in time).  Every
- * call may be captured in a HIP graph.  Tensors need the alignment of their elements only.
- * Sums are taken in a fixed order: the same inputs give the same bits.
+ * call may be captured in a HIP graph.  Tensors need the alignment of their elements only, but for
+ * the optimizer's buffers (qlora_adamw_step_clipped).  Sums are taken in a fixed order: the same
+ * inputs give the same bits.
  */
 #ifndef QLORA_NF4_TRAIN_H
 #define QLORA_NF4_TRAIN_H
@@ -150,6 +151,8 @@ int qlora_grad_clip(const qlora_gradlist_t *list, float max_norm, float *norm, v
 
 /* qlora_adamw_step on gradients clipped as they are read: grad is multiplied by
  * min(1, max_norm / (norm[0] + 1e-6)) in FP32 (no rounding to BF16 in between, nothing written).
+ * As there, master, m and v are 16-byte aligned, grad and param 8-byte aligned: a slice of a flat
+ * state starts at a multiple of four parameters.
  * norm: device FP32 [1], as qlora_grad_norm gives it.  When it is not finite the whole step
  * is skipped: master, m, v and param keep their values.
  * Errors: as qlora_adamw_step; INVALID_ARG also for norm NULL or max_norm not finite or negative. */

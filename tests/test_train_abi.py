@@ -192,3 +192,19 @@ def test_package_imports_on_a_torch_without_gpu_support():
             "try:\n    Q.norm_residual_fwd(x)\nexcept ValueError:\n    print('refused')\n")
     out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and out.stdout.strip() == "refused", out.stderr
+
+
+def test_alignment_of_each_operand(L):
+    """What the header promises: elements' alignment passes (the call goes on to its next check),
+    the optimizer's buffers need a vector's."""
+    odd16, odd32 = P((1 << 20) + 2), P((1 << 20) + 4)
+    assert _bwd(L, x=odd32, dxo=odd32, dx=odd32, y=odd16, dh=odd16, w_post=odd16, gate=odd16, w_pre=odd16, dy=odd16,
+                dwp=odd16, dg=odd16, dw=odd16, type=1, ws=None) == WORKSPACE
+    assert _pref(L, x=odd16, dx=odd16, ref=odd32, loss=odd32, ratios=odd32, lps=odd32, ws=None) == WORKSPACE
+    assert _list(L, [4], ptrs=[(1 << 20) + 2], table=None) == WORKSPACE
+    step = lambda master=A, m=B, v=C, grad=D, param=E, norm=None: L.qlora_adamw_step_clipped(  # noqa: E731
+        master, m, v, grad, param, 4, 1, 1e-3, 0.9, 0.999, 1e-8, 0.0, norm, 1.0, None)
+    for name in ("master", "m", "v"):
+        assert step(**{name: P((1 << 20) + 8)}, norm=W) == INVALID
+    for name in ("grad", "param"):
+        assert step(**{name: P((1 << 20) + 4)}, norm=W) == INVALID
