@@ -14,6 +14,9 @@ rounding of relative 2^-8.
   beside the terms' own error.
 All together 256u of the oracle's magnitudes for every gradient, and the output's rounding."""
 
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -332,3 +335,33 @@ def test_rows_of_any_magnitude(gpu_lib, M, d, scale, eps, stream):
             torch.cuda.synchronize()
             _check_fwd(c, rows, post, 1.0, np.float32(eps), xo, h)
             _check_bwd(c, rows, post, 1.0, np.float32(eps), got)
+
+
+def test_both_sides_of_the_cache_limit(gpu_lib):
+    """Operands above a limit are read past the cache: one row more than fits below it gives the same
+    bits for the other rows, and on both sides the column sums are the formula's in FP64."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    source = os.path.join(os.path.dirname(Q.__file__), "csrc", "norm.hip")
+    limit = int(re.search(r"> \(int64_t\)(\d+) << 20;", open(source).read()).group(1)) << 20
+    d = 6000
+    M = limit // (12 * d)  # BF16: four operands read, two written, of two bytes
+    print(f"norm M={M}, {M + 1} d={d}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(BF)  # noqa: E731
+    x, y, dh, dxo, w1, w2 = r(M + 1, d), r(M + 1, d), r(M + 1, d), r(M + 1, d), r(d), r(d)
+    D = lambda t: t.double()  # noqa: E731
+    inv = lambda v: (v.square().mean(1, keepdim=True) + float(np.float32(1e-5))).rsqrt()  # noqa: E731
+    u, a = D(x) * inv(D(x)), D(dh) * D(w2)
+    t = D(dxo) + inv(D(x)) * (a - u * (a * u).mean(1, keepdim=True))
+    t_abs = D(dxo).abs() + inv(D(x)) * (a.abs() + u.abs() * (a * u).abs().mean(1, keepdim=True))
+    v = D(y) * inv(D(y))
+    outs = []
+    for m in (M, M + 1):
+        got = Q.norm_residual_bwd(x[:m], y[:m], dh[:m], dxo[:m], post_norm=True, w_post=w1, w_pre=w2)
+        torch.cuda.synchronize()
+        outs.append(got)
+        for k, terms, size in ((2, t * v, t_abs * v.abs()), (4, D(dh) * u, (D(dh) * u).abs())):
+            want, tol = terms[:m].sum(0), 256 * U * size[:m].sum(0)
+            assert torch.all((D(got[k]) - want).abs() <= tol + UB * (want.abs() + tol)), (m, k)
+    assert torch.equal(outs[0][0], outs[1][0][:M]) and torch.equal(outs[0][1], outs[1][1][:M])
