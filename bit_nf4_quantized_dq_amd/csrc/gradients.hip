@@ -67,8 +67,9 @@ __device__ __forceinline__ double piece_sum(const E* __restrict__ p, int32_t n, 
 }
 
 // Wavefronts take the pieces in turn.  The partials travel by system-scope (cache-bypassing)
-// stores and loads, and a store has completed before its workgroup is counted; the last
-// workgroup adds them in the workgroups' order.
+// stores and loads, and a store has completed before its workgroup is counted (the wait orders
+// the two on this chip; no rule of the language does); the last workgroup adds them in the
+// workgroups' order.
 template <int T>
 __global__ __launch_bounds__(T) void k_grad_norm(const GradChunk* __restrict__ table, int64_t chunks, float* norm,
                                                  double* part, unsigned int* counter) {

@@ -13,14 +13,19 @@
 //
 // A row is read once and held in registers, eight columns to a thread, and its sums cross the
 // workgroup through LDS, so the forward moves 8 and the backward 12 bytes an element (BF16
-// stream) and HBM bounds both: a simple copy reaches 6.3 TB/s on this card.  What it takes to
-// come near that is to keep loads in flight during the exchanges: the next row's are issued
+// stream).  HBM bounds the forward: a simple copy reaches 6.3 TB/s on this card.  The backward
+// is bound by HBM and by the issue of vector instructions at once: 579 a wavefront and row, four
+// cycles each, are 62 of the 77 us that its kernel takes at 4096 x 8192 (its bytes, partials
+// included, 68 us), and 24 of 36 us at 8192 x 1280 (bytes 23 us), where 17% of the lanes hold no
+// columns.  What it takes to
+// come near the copy is to keep loads in flight during the exchanges: the next row's are issued
 // before this row's sums (without it 114 us for 4096 x 8192 backward, with it 80), and every
 // load and store is unconditional, so that the compiler's counters tell loads from stores.
 // Measured (MI355X, BF16, post-norm and one gate): forward 8192 x 4096 45 - 50 us (5.4 - 6.0
 // TB/s), 4096 x 8192 46 us, 1 x 4096 2.9 us on the device; backward with every gradient 4096 x
-// 8192 79 - 82 us (5.0 TB/s), 8192 x 4096 82 us.  FP32 sums and statistics; each output is
-// rounded once.
+// 8192 77 - 82 us (5.0 TB/s), 8192 x 4096 77 - 82 us, 8192 x 1280 38 us; without post-norm and gate
+// and with frozen weights 8192 x 4096 42 us forward and 68 us backward, 4096 x 8192 42 and 66,
+// 8192 x 1280 13 and 29.  FP32 sums and statistics; each output is rounded once.
 #include "qlora_train_host.h"
 #include "train_device.h"
 
@@ -186,9 +191,11 @@ __device__ void add_segments(const BwdArgs<S>& a, const Columns<SHORT>& col) {
 // norm leaves FP32's range before what it multiplies brings it back.
 // An operand that is not given is zeros, a weight or gate that is not given is ones, so the
 // arithmetic has no cases.
-// What keeps it below the forward's rate: four wavefronts a SIMD (24 sums, two rows and the
-// weights take 103 - 119 registers), and the partials, 12 bytes a column and segment (25 MB
-// written and read again beside 403 MB at 4096 x 8192).
+// What keeps it below the forward's rate: the instructions (operands are unpacked on both sides
+// of the exchange, each thread takes two square roots and two reciprocals a row, and the next
+// row is copied into this one's registers), four wavefronts a SIMD to hide a row's latency
+// behind (24 sums, two rows and the weights take 103 - 127 registers), and the partials, 12 bytes
+// a column and segment (25 MB written and read again beside 403 MB at 4096 x 8192).
 template <class S, bool ONE, bool SHORT, GateKind KIND, Outputs OUT>
 __global__ __launch_bounds__(ONE ? 64 : 1024, SHORT ? 1 : 4) void k_norm_bwd(BwdArgs<S> a) {
   __shared__ float lds[2][6 * 16];

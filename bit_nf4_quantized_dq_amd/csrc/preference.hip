@@ -261,7 +261,9 @@ __device__ __forceinline__ float pair_slope(const PairArgs& a, const double d[2]
 
 // One workgroup of each pair writes its log ratios and its loss; the last of them to arrive adds
 // the losses in the pairs' order.  The losses travel by system-scope (cache-bypassing) stores
-// and loads, and a store has completed before its workgroup is counted.
+// and loads, and a store has completed before its workgroup is counted: the wait between them
+// is what orders the two on this chip.  (No rule of the language does; a release would write
+// back the L2 too, which took 65 ns a workgroup in the norm backward.)
 template <int T>
 __device__ void finish_pair(const PairArgs& a, int64_t pair, const double d[2], PairLds& lds) {
   if (threadIdx.x == 0) {
@@ -299,8 +301,12 @@ __global__ __launch_bounds__(kRowThreads) void k_pref_loss(PairArgs a) {
 }
 
 // The gradient: one workgroup per row and part, each element read and written once.  Each takes
-// its pair's slope from the pair's sums itself, so nothing runs between the two passes.  Rows
-// go from the last to the first: the end of what the first pass read is still in the cache.
+// its pair's slope from the pair's sums itself, so nothing runs between the two passes.  That is
+// 16 S bytes of FP64 ratios a counted row, mostly from L2, before the row's first load: little
+// beside a wide row (V = 32768, all tokens counted: the gradient adds 80 us to the loss of 4096
+// rows at S = 512, 171 to 8192 at S = 4096, 410 to 16384 at S = 8192), most of the time of a
+// narrow one (V = 1000: 114 us for 16384 rows at S = 8192, whose bytes take about 10).  Rows go
+// from the last to the first: the end of what the first pass read is still in the cache.
 template <class E, int T>
 __global__ __launch_bounds__(T) void k_pref_grad(const E* logits, E* dlogits, PairArgs a, int64_t len) {
   __shared__ PairLds lds;
@@ -372,8 +378,10 @@ __global__ __launch_bounds__(T) void k_pref_grad(const E* logits, E* dlogits, Pa
 // The threads of each of `blocks` rows or parts of `len` elements (a launch has fewer than 2^32
 // threads in all).  Short rows take few, so that many rows are under way; 8192 rows of 1000: 10.5 us
 // by 64 threads, 20 by 256; 16384 of 8192: 33 by 128, 37 by 256; 4096 of 32768: 33 by 256, 38 by
-// 128 or 1024; 4096 of 131072: 112 by 1024, 121 by 256.  The gradient (`writes`), which keeps
-// loads and stores in flight, has 256 from 2048 elements on (1600 rows of 16384: 28 us, 29.6 by 128).
+// 128 or 1024; 4096 of 131072: 112 by 1024, 121 by 256 (all of these the statistics).  The gradient
+// (`writes`), which keeps loads and stores in flight, has 256 from 2048 elements on (1600 rows of
+// 16384: 28 us, 29.6 by 128); from 48 K on it follows the statistics, which is not measured for it
+// by itself (by 1024 threads its 88 registers leave one workgroup to a compute unit).
 template <bool writes, class F>
 void by_threads(int64_t blocks, int64_t len, F launch) {
   if (len >= 128 * 1024 && blocks < int64_t(1) << 22) launch(std::integral_constant<int, 1024>());

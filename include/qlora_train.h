@@ -101,6 +101,8 @@ int qlora_token_logps(const void *logits, const int64_t *labels, int64_t rows, i
  *   loss FP32 [1], log_ratios FP32 [2 pairs] (D), logps FP32 [2 pairs, S]: all written.
  *   dlogits: [2 pairs, S, V] of `type`, may be logits itself (then overwritten), or NULL: no
  *   gradient.  A sequence without counted tokens has D = 0 and no gradient.
+ * Each counted token's gradient reads its pair's 2 S log ratios (16 S bytes): from S of about
+ * V / 4 on that is more than its logits (BF16).
  * ws: qlora_preference_workspace_size() bytes.
  * Errors: INVALID_ARG (null or misaligned pointer, pairs outside [1, 2^22), 2 pairs S outside
  * [1, 2^24), beta, label_smoothing or grad_scale not finite, label_smoothing outside [0, 1],
@@ -129,7 +131,8 @@ int qlora_gradlist_size(int count, const int64_t *numel, size_t *table_bytes);
  *   grads[i]: device pointer to numel[i] elements of types[i] (QLORA_BF16 or QLORA_F32).
  *   out, out_types: where qlora_grad_clip writes tensor i, and in which type; out NULL (out_types
  *   ignored), or out[i] == grads[i] with the same type: in place.  The arrays are host memory,
- *   read before the call returns; an empty tensor's pointers may be NULL.
+ *   read before the call returns; an empty tensor's pointers may be NULL.  Otherwise no out
+ *   tensor overlaps a gradient or another out tensor.
  * Errors: INVALID_ARG (null or misaligned pointer, count or a size negative, in place with
  * another type), BAD_SHAPE, UNSUPPORTED (unknown type), WORKSPACE (table too small), HIP. */
 int qlora_gradlist_init(int count, const void *const *grads, const int32_t *types, const int64_t *numel,
