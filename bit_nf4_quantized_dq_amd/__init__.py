@@ -1,9 +1,9 @@
 """MI355X (gfx950) NF4 + double-quantized frozen linear with a 16-bit LoRA side path.
 
 The compute runs in the HIP library ``libqlora_nf4.so`` (C ABI in ``include/qlora.h``
-and, for the operators of a training step beside the linears, ``include/qlora_train.h``); this
-package only marshals arguments.  ``lib`` raises if the library is missing -- there is
-no CPU fallback.
+and, for the operators of a training step beside the linears and for linears with many adapters,
+``include/qlora_train.h`` and ``include/qlora_adapters.h``); this package only marshals arguments.
+``lib`` raises if the library is missing -- there is no CPU fallback.
 """
 
 from ._binding import (  # noqa: F401
@@ -39,6 +39,12 @@ from ._binding import (  # noqa: F401
     OP_QUANTIZE,
     OP_FWD,
     OP_BWD,
+)
+from ._adapters import (  # noqa: F401
+    AdapterSet,
+    dropout,
+    linear_adapters_bwd,
+    linear_adapters_fwd,
 )
 from ._training import (  # noqa: F401
     GradList,

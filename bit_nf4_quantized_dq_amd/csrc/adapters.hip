@@ -1,0 +1,680 @@
+// The kernels of a frozen linear with many adapters ("QLoRA -- Fine-Tuning a 65B Model on One
+// GPU", "Prerequisite: LoRA's low-rank update": one shared frozen base, small pairs A, B beside
+// it): each row m of a batch names its adapter a = ids[m].
+//
+// shrink : T[m] = drop(X[m]) A_a^T  and  G[m] = dY[m] B_a           (FP32 [M, width])
+// stream : Y = X w_hat^T + s_a T B_a^T for few rows, the weight decoded as it is read
+// grads  : dA_a = s_a sum of G[m]^T drop(X[m]),  dB_a = s_a sum of dY[m]^T T[m]
+// (many rows' Y and dX: gemm_nt.hip)
+//
+// Rows come in any order.  A workgroup finds the distinct adapters of its rows by ballots, loads
+// each one's operand once and takes the result for the rows that name it: a select, not a
+// multiplication by zero, so that an adapter with infinite values reaches its own rows only.
+#include "adapters_device.h"
+#include "decode_tiles.h"
+
+namespace qlora {
+namespace {
+
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+
+// 8 consecutive rows 8 (lane >> 4) .. +7 of column (lane & 15) of an LDS tile of BF16 rows of 32
+// bytes, by two transposing reads (as in lora.hip: within 16 lanes, lane i receives element
+// i % 4 of the 8 bytes that lanes i/4, i/4 + 4, i/4 + 8, i/4 + 12 address).
+__device__ __forceinline__ bf16x8_t tr_operand(const char* tile, int lane) {
+  const int j = lane & 15, g = lane >> 4;
+  const char* p0 = tile + (8 * g + (j >> 2)) * 32 + 8 * (j & 3);
+  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p0));
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p0 + 4 * 32));
+  bf16x8_t r;
+  r[0] = lo[0]; r[1] = lo[1]; r[2] = lo[2]; r[3] = lo[3];
+  r[4] = hi[0]; r[5] = hi[1]; r[6] = hi[2]; r[7] = hi[3];
+  return r;
+}
+
+__device__ __forceinline__ int lowest(uint64_t mask) { return __builtin_ctzll(mask); }
+__device__ __forceinline__ uint64_t readlane64(uint64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// ---------------------------------------------------------------- the table
+__global__ __launch_bounds__(128) void k_adapter_table(AdapterBatch batch, int count, AdapterEntry* __restrict__ table) {
+  const int i = threadIdx.x;
+  if (i < count) table[i] = batch.e[i];
+}
+
+// ---------------------------------------------------------------- T and G
+constexpr int kShrinkThreads = 512;
+constexpr int kShrinkWaves = kShrinkThreads / 64;
+constexpr int kRowTile = 16;
+
+struct ShrinkArgs {
+  AdapterRows rows;
+  const uint16_t* P;  // X [M, Kd] or dY
+  int64_t Kd;
+  DropMask drop;
+  float* out;  // [M, width]
+  float* part;
+  unsigned int* counters;
+  int32_t split;
+};
+
+// One workgroup per 16 rows and slice of the reduction.  An item is a 32-wide slab of the slice
+// and one of the rows' adapters; the wavefronts take the items in turn, D in flight each.  JT:
+// 16-rank tiles.  QT: the operand is B_a [Kd, r] (transposed through LDS), else A_a [r, Kd].
+template <int JT, bool QT, bool DROP, bool VEC, int D>
+__global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a, ShrinkDecode dec, uint32_t n_shrink,
+                                                                   Nf4Tables tab) {
+  __shared__ __attribute__((aligned(16))) char smem[kShrinkWaves * JT * 1024];
+  __shared__ bool s_last;
+  if (blockIdx.x >= n_shrink) {  // the weight's decode, beside the products
+    if (!QT) {
+      decode_words<kDqE4M3, kShrinkThreads>(dec.codes, dec.code8, dec.c2s, dec.mu, reinterpret_cast<uint4*>(dec.out),
+                                            (int64_t)(blockIdx.x - n_shrink), threadIdx.x, dec.N * dec.K / 8, tab);
+    } else {
+      const uint32_t groups_k = (uint32_t)((dec.K / 64 + kShrinkWaves - 1) / kShrinkWaves);
+      const uint32_t grp = blockIdx.x - n_shrink, gn = grp / groups_k;
+      decode_pairs_t<kDqE4M3, kShrinkThreads>(dec.codes, dec.code8, dec.c2s, dec.mu, dec.out, dec.N, dec.K, tab,
+                                              (int64_t)gn, (int64_t)(grp - gn * groups_k), threadIdx.x);
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const uint32_t split = (uint32_t)a.split, tile = blockIdx.x / split, slice = blockIdx.x - tile * split;
+  const int64_t m0 = (int64_t)tile * kRowTile, M = a.rows.M, Kd = a.Kd, width = a.rows.width;
+  // each lane its row's adapter; the four groups of 16 lanes hold the same rows
+  const int id = adapter_of(a.rows, m0 + l16);
+  uint64_t base = 0;
+  int rank = 0;
+  if (id >= 0) {
+    const AdapterEntry* e = a.rows.table + id;
+    base = reinterpret_cast<uint64_t>(QT ? e->B : e->A);
+    rank = e->r;
+  }
+  RngKey key{};
+  uint32_t t2 = 0;
+  if (DROP) key = load_rng(a.drop.rng), t2 = threshold_halves(a.drop.threshold);
+  const rsrc_t rp = make_rsrc(a.P + m0 * Kd, (M - m0) * Kd * 2);
+  const uint64_t block0 = (uint64_t)(m0 + l16) * (uint64_t)(Kd / 8);
+
+  const int nslab = (int)((Kd + 31) / 32), per = (nslab + (int)split - 1) / (int)split;
+  const int sbeg = (int)slice * per, send = sbeg + per < nslab ? sbeg + per : nslab, len = send - sbeg;
+  f32x4_t acc[JT];
+#pragma unroll
+  for (int t = 0; t < JT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  char* qs = smem + wave * JT * 1024;
+
+  uint64_t pending = __ballot(id >= 0);
+  int cur = -1, at = wave;  // the adapter's lane, and the slab within the slice
+  if (len > 0 && pending) {
+    cur = lowest(pending);
+    const auto step = [&](int by) {  // to the item `by` further on
+      at += by;
+      while (cur >= 0 && at >= len) {
+        at -= len;
+        pending &= ~__ballot(id == __builtin_amdgcn_readlane(id, cur));
+        cur = pending ? lowest(pending) : -1;
+      }
+    };
+    step(0);
+    while (cur >= 0) {
+      uint4 pv[D], qv[D][JT];
+      int which[D], slab[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const bool live = cur >= 0;
+        const int from = live ? cur : 0;
+        which[d] = live ? __builtin_amdgcn_readlane(id, from) : -2;
+        slab[d] = sbeg + at;
+        const int r = __builtin_amdgcn_readlane(rank, from);
+        const rsrc_t rq = make_rsrc(reinterpret_cast<const void*>(readlane64(base, from)), live ? (int64_t)r * Kd * 2 : 0);
+        const int64_t k = 32 * (int64_t)slab[d] + 8 * g;
+        pv[d] = bload16(rp, (id == which[d] && k < Kd) ? (uint32_t)((l16 * Kd + k) * 2) : kOOB);
+        if (!QT) {
+#pragma unroll
+          for (int t = 0; t < JT; ++t) {
+            const int j = 16 * t + l16;
+            qv[d][t] = bload16(rq, (k < Kd && j < r) ? (uint32_t)(((int64_t)j * Kd + k) * 2) : kOOB);
+          }
+        } else {
+          // rows 32 slab + (lane >> 1), columns 8 (lane & 1) .. +7 of every tile
+          const int64_t kr = 32 * (int64_t)slab[d] + (lane >> 1);
+#pragma unroll
+          for (int t = 0; t < JT; ++t) {
+            const int j = 16 * t + 8 * (lane & 1);
+            if (VEC) {
+              qv[d][t] = bload16(rq, (kr < Kd && j < r) ? (uint32_t)((kr * r + j) * 2) : kOOB);
+            } else {
+              uint32_t e[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                e[q] = __builtin_amdgcn_raw_buffer_load_b16(rq, (kr < Kd && j + q < r) ? (int)((kr * r + j + q) * 2) : (int)kOOB, 0, 0);
+              qv[d][t] = make_uint4((e[0] & 0xFFFFu) | (e[1] << 16), (e[2] & 0xFFFFu) | (e[3] << 16),
+                                    (e[4] & 0xFFFFu) | (e[5] << 16), (e[6] & 0xFFFFu) | (e[7] << 16));
+            }
+          }
+        }
+        if (live) step(kShrinkWaves);
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const bool mine = id == which[d];
+        bf16x8_t qa[JT];
+        if (!QT) {
+#pragma unroll
+          for (int t = 0; t < JT; ++t) qa[t] = as_bf16x8(qv[d][t]);
+        } else {
+          // the wavefront's LDS tiles are reused item after item; its LDS accesses run in order
+          asm volatile("" ::: "memory");
+#pragma unroll
+          for (int t = 0; t < JT; ++t) *reinterpret_cast<uint4*>(qs + t * 1024 + (lane >> 1) * 32 + 16 * (lane & 1)) = qv[d][t];
+          asm volatile("" ::: "memory");
+#pragma unroll
+          for (int t = 0; t < JT; ++t) qa[t] = tr_operand(qs + t * 1024, lane);
+          asm volatile("" ::: "memory");
+        }
+        const uint4 p = DROP ? drop8(pv[d], key, block0 + (uint64_t)(4 * slab[d] + g), t2) : pv[d];
+#pragma unroll
+        for (int t = 0; t < JT; ++t) {
+          const f32x4_t v = mfma16x16x32(qa[t], as_bf16x8(p), f32x4_t{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][i] += mine ? v[i] : 0.f;
+        }
+      }
+    }
+  }
+  // fixed-order sum over the wavefronts; D[j][m]: lane l holds ranks 4 (l >> 4) + v of row l & 15
+  __syncthreads();
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(smem);
+#pragma unroll
+  for (int t = 0; t < JT; ++t) red[(wave * JT + t) * 64 + lane] = acc[t];
+  __syncthreads();
+  const int64_t m = m0 + l16;
+  const float keep = DROP ? a.drop.scale : 1.f;
+  for (int t = wave; t < JT; t += kShrinkWaves) {
+    f32x4_t sum = red[t * 64 + lane];
+    for (int w = 1; w < kShrinkWaves; ++w) {
+      const f32x4_t v = red[(w * JT + t) * 64 + lane];
+      sum[0] += v[0]; sum[1] += v[1]; sum[2] += v[2]; sum[3] += v[3];
+    }
+    const int j = 16 * t + 4 * g;
+    if (m >= M || j >= width) continue;
+    if (split == 1) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) sum[v] = j + v < rank ? sum[v] * keep : 0.f;
+      *reinterpret_cast<f32x4_t*>(a.out + m * width + j) = sum;
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        __hip_atomic_store(a.part + ((int64_t)slice * M + m) * width + j + v, sum[v], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+    }
+  }
+  if (split == 1) return;
+  // every partial store of this workgroup has completed before its counter increment
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned int old = __hip_atomic_fetch_add(&a.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = old + 1u == split;
+    if (s_last) __hip_atomic_store(&a.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!s_last) return;
+  for (int t = wave; t < JT; t += kShrinkWaves) {
+    const int j = 16 * t + 4 * g;
+    if (m >= M || j >= width) continue;
+    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t s0 = 0; s0 < split; s0 += 4) {
+      float v[4][4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[u][i] = s0 + u < split ? __hip_atomic_load(a.part + ((int64_t)(s0 + u) * M + m) * width + j + i, __ATOMIC_RELAXED,
+                                                       __HIP_MEMORY_SCOPE_SYSTEM)
+                                   : 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += v[u][i];
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) sum[v] = j + v < rank ? sum[v] * keep : 0.f;
+    *reinterpret_cast<f32x4_t*>(a.out + m * width + j) = sum;
+  }
+}
+
+template <int JT, bool QT, bool DROP, bool VEC>
+hipError_t shrink_as(const ShrinkArgs& a, const ShrinkDecode* dec, const Nf4Tables& tab, hipStream_t st) {
+  constexpr int kMost = JT == 1 ? 8 : (JT == 2 ? 4 : 2);
+  const int64_t tiles = (a.rows.M + kRowTile - 1) / kRowTile;
+  const int64_t n = tiles * a.split;
+  int64_t n_dec = 0;
+  if (dec)
+    n_dec = QT ? ((dec->K / 64 + kShrinkWaves - 1) / kShrinkWaves) * ((dec->N + kTRows - 1) / kTRows)
+               : (dec->N * dec->K / 8 + kShrinkThreads * kDecWords - 1) / (kShrinkThreads * kDecWords);
+  const ShrinkDecode d = dec ? *dec : ShrinkDecode{};
+  hipLaunchKernelGGL((k_adapter_shrink<JT, QT, DROP, VEC, kMost>), dim3((unsigned)(n + n_dec)), dim3(kShrinkThreads), 0, st, a,
+                     d, (uint32_t)n, tab);
+  return hipGetLastError();
+}
+template <bool QT, bool DROP, bool VEC>
+hipError_t shrink_by_rank(const ShrinkArgs& a, const ShrinkDecode* dec, const Nf4Tables& tab, hipStream_t st) {
+  if (a.rows.max_rank <= 16) return shrink_as<1, QT, DROP, VEC>(a, dec, tab, st);
+  if (a.rows.max_rank <= 32) return shrink_as<2, QT, DROP, VEC>(a, dec, tab, st);
+  if (a.rows.max_rank <= 64) return shrink_as<4, QT, DROP, VEC>(a, dec, tab, st);
+  return shrink_as<8, QT, DROP, VEC>(a, dec, tab, st);
+}
+
+// ---------------------------------------------------------------- few rows: the weight's stream
+constexpr int kStreamThreads = 512;
+constexpr int kStreamWaves = kStreamThreads / 64;
+constexpr int kStreamRows = 16;  // weight rows per workgroup
+
+struct StreamArgs {
+  const uint8_t *codes, *code8;
+  const float *c2s, *mu;
+  int64_t N, K;
+  const uint16_t* X;
+  AdapterRows rows;
+  const float* T;
+  uint16_t* Y;
+};
+
+// 16 weight rows over the whole reduction.  A wavefront takes groups of four 64-weight blocks;
+// lane (l16, g) decodes block 4 group + g of row l16 (32 bytes of codes, one level table scaled by
+// the block's constant: exactly w_hat), so word i of the four blocks is one MFMA 16x16x32 operand
+// whose reduction indices are 64 (4 group + g) + 8 i .. +7, and X is read in the same order.
+template <int MT>
+__global__ __launch_bounds__(kStreamThreads) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
+  __shared__ f32x4_t red[kStreamWaves][MT][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int64_t K = a.K, N = a.N, row0 = (int64_t)blockIdx.x * kStreamRows;
+  const int M = (int)a.rows.M;
+  const uint32_t nb = (uint32_t)(K / 64), ng = (nb + 3) / 4;
+  const rsrc_t rx = make_rsrc(a.X, (int64_t)M * K * 2);
+  const rsrc_t rc = make_rsrc(a.codes + row0 * (K / 2), kStreamRows * (K / 2));
+  const rsrc_t r8 = make_rsrc(a.code8 + row0 * nb, (int64_t)kStreamRows * nb);
+  const rsrc_t r2 = make_rsrc(a.c2s, ((N * nb + 255) / 256) * 4);
+  const uint32_t blk_row = (uint32_t)(row0 + l16) * nb;
+  struct Codes {
+    uint4 c0, c1;
+    uint32_t c8, c2;
+  };
+  const auto load = [&](uint32_t group) {
+    const uint32_t b = 4 * group + g;
+    const bool ok = group < ng && b < nb;
+    Codes c;
+    const uint32_t off = (uint32_t)(l16 * (K / 2)) + 32 * b;
+    c.c0 = bload16(rc, ok ? off : kOOB);
+    c.c1 = bload16(rc, ok ? off + 16 : kOOB);
+    c.c8 = bload1(r8, ok ? l16 * nb + b : kOOB);
+    c.c2 = bload4(r2, ok ? ((blk_row + b) >> 8) * 4 : kOOB);
+    return c;
+  };
+  Codes cur = load(wave), next = load(wave + kStreamWaves);
+  const float mu = a.mu[0];
+  f32x4_t acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (uint32_t group = wave; group < ng; group += kStreamWaves) {
+    const uint32_t b = 4 * group + g;
+    uint32_t xoff[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int m = 16 * t + l16;
+      xoff[t] = (m < M && b < nb) ? (uint32_t)((m * K + 64 * (int64_t)b) * 2) : kOOB;
+    }
+    const Codes c = cur;
+    cur = next;
+    next = load(group + 2 * kStreamWaves);
+    Lut L;
+    build_scaled_lut(tab, block_scale(c.c8, __uint_as_float(c.c2), mu), L);
+    const uint32_t words[8] = {c.c0.x, c.c0.y, c.c0.z, c.c0.w, c.c1.x, c.c1.y, c.c1.z, c.c1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint4 x[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) x[t] = bload16(rx, xoff[t] == kOOB ? kOOB : xoff[t] + 16 * i);
+      uint32_t w[4];
+      decode8(words[i], L, w);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[t] = mfma16x16x32(as_bf16x8(w), as_bf16x8(x[t]), acc[t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
+  __syncthreads();
+  // lane l of item t: row 16 t + (l & 15) of X, weight rows 4 (l >> 4) + v
+  for (int t = wave; t < MT; t += kStreamWaves) {
+    const int m = 16 * t + l16;
+    if (m >= M) continue;
+    f32x4_t y = red[0][t][lane];
+#pragma unroll
+    for (int w = 1; w < kStreamWaves; ++w) {
+      const f32x4_t v = red[w][t][lane];
+      y[0] += v[0]; y[1] += v[1]; y[2] += v[2]; y[3] += v[3];
+    }
+    const int64_t n = row0 + 4 * g;
+    const int id = adapter_of(a.rows, m);
+    if (id >= 0) {
+      const AdapterEntry e = a.rows.table[id];
+      const float* T = a.T + (int64_t)m * a.rows.width;
+      const uint16_t* B = e.B + n * e.r;
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      if (a.rows.whole) {
+        for (int j = 0; j < e.r; j += 8) {
+          const f32x4_t t0 = *reinterpret_cast<const f32x4_t*>(T + j), t1 = *reinterpret_cast<const f32x4_t*>(T + j + 4);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const uint4 b = *reinterpret_cast<const uint4*>(B + v * e.r + j);
+            s[v] = fmaf(t0[0], bf16lo_to_f32(b.x), s[v]); s[v] = fmaf(t0[1], bf16hi_to_f32(b.x), s[v]);
+            s[v] = fmaf(t0[2], bf16lo_to_f32(b.y), s[v]); s[v] = fmaf(t0[3], bf16hi_to_f32(b.y), s[v]);
+            s[v] = fmaf(t1[0], bf16lo_to_f32(b.z), s[v]); s[v] = fmaf(t1[1], bf16hi_to_f32(b.z), s[v]);
+            s[v] = fmaf(t1[2], bf16lo_to_f32(b.w), s[v]); s[v] = fmaf(t1[3], bf16hi_to_f32(b.w), s[v]);
+          }
+        }
+      } else {
+        for (int j = 0; j < e.r; ++j) {
+          const float t0 = T[j];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) s[v] = fmaf(t0, __uint_as_float((uint32_t)B[v * e.r + j] << 16), s[v]);
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v) y[v] = fmaf(e.s, s[v], y[v]);
+    }
+    *reinterpret_cast<uint2*>(a.Y + (int64_t)m * N + n) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+  }
+}
+
+// ---------------------------------------------------------------- dA and dB
+constexpr int kGradThreads = 256;
+constexpr int kGradWaves = kGradThreads / 64;
+constexpr int kGradCols = 64;         // columns per workgroup
+constexpr int kGradRanks = 64;        // ranks per workgroup
+constexpr int kSpan = 256;            // rows that a wavefront looks through at once
+constexpr int kVTile = 32 * 32 + 64;  // bytes of a staged [32][16] BF16 tile, padded (bank offset)
+constexpr int kSumU = 16;             // partials loaded together before they are added
+
+struct GradsArgs {
+  AdapterRows rows;
+  const uint16_t *X, *dY;
+  const float *T, *G;
+  int64_t K, N;
+  DropMask drop;
+  float* part;
+  unsigned int* counters;
+  uint32_t tiles_a;
+  int32_t blocks, split;
+  int64_t mps;  // rows per slice
+};
+
+// Workgroup (x, y, z): 64 columns of dA (or of dB), a slice of the rows, an adapter and up to 64 of
+// its ranks.  A wavefront takes every fourth run of 256 rows, lists those of its adapter (ballots
+// over ids) and multiplies them 32 at a time: U [32 rows][ranks] as hi and lo
+// BF16 parts and V [32 rows][64 columns], both transposed through LDS.
+template <int JT>
+struct GradsLds {
+  static constexpr int kWaveBytes = (4 + 2 * JT) * kVTile;
+  static constexpr int kRedBytes = kGradWaves * JT * 4 * 64 * 16;
+  __attribute__((aligned(16))) char tiles[kGradWaves * kWaveBytes > kRedBytes ? kGradWaves * kWaveBytes : kRedBytes];
+  uint16_t lists[kGradWaves][kSpan];
+  bool last;
+};
+template <int JT, int D, bool DROP, bool IS_B>
+__device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds) {
+  constexpr int kWaveBytes = GradsLds<JT>::kWaveBytes;
+  char* smem = lds.tiles;
+  const int adapter = (int)(blockIdx.z / (unsigned)a.blocks), block = (int)blockIdx.z - adapter * a.blocks;
+  const AdapterEntry e = a.rows.table[adapter];
+  const int j_first = block * kGradRanks;
+  if (j_first >= e.r) return;  // all slices alike: no counter is touched
+  const uint16_t* __restrict__ V = IS_B ? a.dY : a.X;
+  const float* __restrict__ U = IS_B ? a.T : a.G;
+  const int64_t C = IS_B ? a.N : a.K, width = a.rows.width;
+  const int64_t c0 = (int64_t)(IS_B ? blockIdx.x - a.tiles_a : blockIdx.x) * kGradCols;
+  const int64_t mbeg = (int64_t)blockIdx.y * a.mps, mend = mbeg + a.mps < a.rows.M ? mbeg + a.mps : a.rows.M;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RngKey key{};
+  uint32_t t2 = 0;
+  if (DROP) key = load_rng(a.drop.rng), t2 = threshold_halves(a.drop.threshold);
+  char* vt = smem + wave * kWaveBytes;  // 4 V tiles, JT hi tiles, JT lo tiles
+  char* ut = vt + 4 * kVTile;
+  uint16_t* list = lds.lists[wave];
+  const int32_t* __restrict__ ids = a.rows.ids;
+  const uint64_t below = lane ? ~0ull >> (64 - lane) : 0ull;
+  f32x4_t acc[JT][4];
+#pragma unroll
+  for (int t = 0; t < JT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int64_t first = mbeg + kSpan * wave; first < mend; first += (int64_t)kSpan * kGradWaves) {
+    const int n = (int)(mend - first < kSpan ? mend - first : kSpan);
+    int count = 0, id[kSpan / 64];
+#pragma unroll
+    for (int q = 0; q < kSpan / 64; ++q) id[q] = 64 * q + lane < n ? (ids ? ids[first + 64 * q + lane] : 0) : -1;
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int q = 0; q < kSpan / 64; ++q) {
+      const bool hit = id[q] == adapter;
+      const uint64_t mask = __ballot(hit);
+      if (hit) list[count + __popcll(mask & below)] = (uint16_t)(64 * q + lane);
+      count += __popcll(mask);
+    }
+    asm volatile("" ::: "memory");
+    const rsrc_t rv = make_rsrc(V + first * C, n * C * 2);
+    const rsrc_t ru = make_rsrc(U + first * width, n * width * 4);
+    const auto row = [&](int i) { return i < count ? (int)list[i] : -1; };
+    for (int i0 = 0; i0 < count; i0 += 32 * D) {
+      uint4 vv[D][4], uw[D][JT][2];
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = row(i0 + 32 * d + 8 * i + (lane >> 3));
+          const int64_t c = c0 + 8 * (lane & 7);
+          vv[d][i] = bload16(rv, (m >= 0 && c < C) ? (uint32_t)((m * C + c) * 2) : kOOB);
+        }
+        const int m = row(i0 + 32 * d + (lane >> 1));
+#pragma unroll
+        for (int t = 0; t < JT; ++t) {
+          const int j = j_first + 16 * t + 8 * (lane & 1);
+          const uint32_t off = (m >= 0 && j < width) ? (uint32_t)((m * width + j) * 4) : kOOB;
+          uw[d][t][0] = bload16(ru, off);
+          uw[d][t][1] = bload16(ru, off == kOOB ? kOOB : off + 16);
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        // the wavefront's LDS tiles are reused chunk after chunk; its LDS accesses run in order
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int in = 8 * i + (lane >> 3), ct = (lane & 7) >> 1, half = lane & 1;
+          uint4 v = vv[d][i];
+          if (DROP) {
+            const int m = row(i0 + 32 * d + in);
+            v = drop8(v, key, (uint64_t)((first + (m < 0 ? 0 : m)) * (C / 8) + c0 / 8 + (lane & 7)), t2);
+            __builtin_amdgcn_sched_barrier(0);  // one vector's words at a time
+          }
+          *reinterpret_cast<uint4*>(vt + ct * kVTile + in * 32 + 16 * half) = v;
+        }
+#pragma unroll
+        for (int t = 0; t < JT; ++t) {
+          const uint4 x = uw[d][t][0], y = uw[d][t][1];
+          const float f[8] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w),
+                              __uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z), __uint_as_float(y.w)};
+          uint4 hi, lo;
+          split_bf16(f, hi, lo);
+          *reinterpret_cast<uint4*>(ut + t * kVTile + (lane >> 1) * 32 + 16 * (lane & 1)) = hi;
+          *reinterpret_cast<uint4*>(ut + (JT + t) * kVTile + (lane >> 1) * 32 + 16 * (lane & 1)) = lo;
+        }
+        asm volatile("" ::: "memory");
+        bf16x8_t b[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) b[q] = tr_operand(vt + q * kVTile, lane);
+#pragma unroll
+        for (int t = 0; t < JT; ++t) {
+          const bf16x8_t hi = tr_operand(ut + t * kVTile, lane), lo = tr_operand(ut + (JT + t) * kVTile, lane);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[t][q] = mfma16x16x32(lo, b[q], mfma16x16x32(hi, b[q], acc[t][q]));
+        }
+        asm volatile("" ::: "memory");
+      }
+    }
+  }
+  // fixed-order sum over the wavefronts: D[j][c], lane l holds j = 4 (l >> 4) + v, c = l & 15
+  __syncthreads();
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(smem);
+#pragma unroll
+  for (int t = 0; t < JT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) red[((wave * JT + t) * 4 + q) * 64 + lane] = acc[t][q];
+  __syncthreads();
+  const float scale = DROP ? e.s * a.drop.scale : e.s;
+  const int32_t split = a.split;
+  const int64_t CT = a.K + a.N;
+  float* part = a.part + ((int64_t)blockIdx.z * split * kGradRanks) * CT + (IS_B ? a.K : 0);
+  uint16_t* out = IS_B ? e.dB : e.dA;
+  const auto store = [&](int j, int64_t c, float v) {
+    const uint16_t h = (uint16_t)(pack_bf16x2(v * scale, 0.f) & 0xFFFFu);
+    if (IS_B) out[c * e.r + j] = h;
+    else out[(int64_t)j * C + c] = h;
+  };
+  for (int i = threadIdx.x; i < JT * 4 * 64; i += kGradThreads) {
+    const int l = i & 63, q = (i >> 6) & 3, t = i >> 8;
+    f32x4_t sum = red[(t * 4 + q) * 64 + l];
+    for (int w = 1; w < kGradWaves; ++w) {
+      const f32x4_t v = red[((w * JT + t) * 4 + q) * 64 + l];
+      sum[0] += v[0]; sum[1] += v[1]; sum[2] += v[2]; sum[3] += v[3];
+    }
+    const int64_t c = c0 + 16 * q + (l & 15);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int j = 16 * t + 4 * (l >> 4) + v;
+      if (j_first + j >= e.r || c >= C) continue;
+      if (split == 1) store(j_first + j, c, sum[v]);
+      else
+        __hip_atomic_store(part + ((int64_t)blockIdx.y * kGradRanks + j) * CT + c, sum[v], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+    }
+  }
+  if (split == 1) return;
+  // every partial store of this workgroup has completed before its counter increment
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned int* counter = a.counters + (uint32_t)blockIdx.z * gridDim.x + blockIdx.x;
+    const unsigned int old = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    lds.last = old + 1u == (unsigned int)split;
+    if (lds.last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!lds.last) return;
+  const int ranks = e.r - j_first < 16 * JT ? e.r - j_first : 16 * JT;
+  for (int i = threadIdx.x; i < ranks * kGradCols; i += kGradThreads) {
+    const int j = i >> 6;
+    const int64_t c = c0 + (i & 63);
+    if (c >= C) continue;
+    const float* p = part + (int64_t)j * CT + c;
+    float s = 0.f;
+    for (int32_t k0 = 0; k0 < split; k0 += kSumU) {
+      float v[kSumU];
+#pragma unroll
+      for (int u = 0; u < kSumU; ++u)
+        v[u] = (k0 + u < split) ? __hip_atomic_load(p + (int64_t)(k0 + u) * kGradRanks * CT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM)
+                                : 0.f;
+#pragma unroll
+      for (int u = 0; u < kSumU; ++u) s += v[u];
+    }
+    store(j_first + j, c, s);
+  }
+}
+
+template <int JT, int D, bool DROP>
+__global__ __launch_bounds__(kGradThreads) void k_adapter_grads(GradsArgs a) {
+  __shared__ GradsLds<JT> lds;
+  if (blockIdx.x < a.tiles_a) grads_body<JT, D, DROP, false>(a, lds);
+  else grads_body<JT, D, false, true>(a, lds);
+}
+
+template <int JT>
+hipError_t grads_as(const GradsArgs& a, const GradPlan& plan, hipStream_t st) {
+  constexpr int D = JT <= 2 ? 4 : 2;
+  const dim3 grid((unsigned)(plan.tiles_a + plan.tiles_b), (unsigned)plan.split, (unsigned)(a.rows.count * plan.blocks));
+  if (a.drop.threshold) hipLaunchKernelGGL((k_adapter_grads<JT, D, true>), grid, dim3(kGradThreads), 0, st, a);
+  else hipLaunchKernelGGL((k_adapter_grads<JT, D, false>), grid, dim3(kGradThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_adapter_table(const AdapterBatch& batch, int count, AdapterEntry* table, hipStream_t st) {
+  hipLaunchKernelGGL(k_adapter_table, dim3(1), dim3(128), 0, st, batch, count, table);
+  return hipGetLastError();
+}
+
+int32_t shrink_split(int64_t M, int64_t Kd) {
+  const int64_t tiles = (M + kRowTile - 1) / kRowTile, slabs = (Kd + 31) / 32;
+  const int64_t split = std::min<int64_t>({int64_t(16), 256 / tiles, slabs / kShrinkWaves});
+  return (int32_t)std::max<int64_t>(split, 1);
+}
+
+hipError_t launch_shrink_a(const AdapterRows& rows, const uint16_t* X, int64_t K, const DropMask& drop, float* T,
+                           float* part, unsigned int* counters, const ShrinkDecode* decode, const Nf4Tables& tab,
+                           hipStream_t st) {
+  const ShrinkArgs a{rows, X, K, drop, T, part, counters, shrink_split(rows.M, K)};
+  return drop.threshold ? shrink_by_rank<false, true, true>(a, decode, tab, st)
+                        : shrink_by_rank<false, false, true>(a, decode, tab, st);
+}
+
+hipError_t launch_shrink_b(const AdapterRows& rows, const uint16_t* dY, int64_t N, float* G, float* part,
+                           unsigned int* counters, const ShrinkDecode* decode, const Nf4Tables& tab, hipStream_t st) {
+  const ShrinkArgs a{rows, dY, N, DropMask{}, G, part, counters, shrink_split(rows.M, N)};
+  return rows.whole ? shrink_by_rank<true, false, true>(a, decode, tab, st)
+                    : shrink_by_rank<true, false, false>(a, decode, tab, st);
+}
+
+hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, const float* c2s, const float* mu,
+                                 int64_t N, int64_t K, const uint16_t* X, const AdapterRows& rows, const float* T,
+                                 uint16_t* Y, const Nf4Tables& tab, hipStream_t st) {
+  if (rows.M > kStreamMaxRows) return hipErrorInvalidValue;
+  const StreamArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, rows, T, Y};
+  const dim3 grid((unsigned)(N / kStreamRows));
+  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kStreamThreads), 0, st, a, tab); };
+  if (rows.M <= 16) go(k_adapter_stream<1>);
+  else if (rows.M <= 32) go(k_adapter_stream<2>);
+  else if (rows.M <= 64) go(k_adapter_stream<4>);
+  else go(k_adapter_stream<8>);
+  return hipGetLastError();
+}
+
+GradPlan adapter_grad_plan(int64_t M, int64_t N, int64_t K, int32_t count, int32_t max_rank) {
+  GradPlan p{};
+  p.tiles_a = (K + kGradCols - 1) / kGradCols;
+  p.tiles_b = (N + kGradCols - 1) / kGradCols;
+  p.blocks = (max_rank + kGradRanks - 1) / kGradRanks;
+  p.split = 1;
+  const int64_t groups = (p.tiles_a + p.tiles_b) * count * p.blocks;
+  while (groups * p.split < 512 && (int64_t)p.split * 2 * 128 <= M && p.split < 64) p.split *= 2;
+  if (p.split > 1) p.part_bytes = sizeof(float) * (size_t)count * p.blocks * p.split * kGradRanks * (size_t)(K + N);
+  return p;
+}
+
+hipError_t launch_adapter_grads(const AdapterRows& rows, const uint16_t* X, int64_t K, const uint16_t* dY, int64_t N,
+                                const float* T, const float* G, const DropMask& drop, float* part,
+                                unsigned int* counters, hipStream_t st) {
+  const GradPlan plan = adapter_grad_plan(rows.M, N, K, rows.count, rows.max_rank);
+  GradsArgs a{rows, X, dY, T, G, K, N, drop, part, counters, (uint32_t)plan.tiles_a, plan.blocks, plan.split, 0};
+  a.mps = ((rows.M + plan.split - 1) / plan.split + 31) / 32 * 32;
+  if (rows.max_rank <= 16) return grads_as<1>(a, plan, st);
+  if (rows.max_rank <= 32) return grads_as<2>(a, plan, st);
+  return grads_as<4>(a, plan, st);
+}
+
+}  // namespace qlora

@@ -262,6 +262,10 @@ TimingState& timing() {
 
 namespace qlora {
 
+int check_weight(const qlora_nf4dq_t* Wq) { return check_wq(Wq); }
+bool linear_shape_ok(int64_t d_out, int64_t d_in) { return shape_ok(d_out, d_in); }
+const Nf4Tables& weight_tables(const qlora_nf4dq_t* Wq) { return tables_of(Wq); }
+
 // ---- exact mean: value = sum_e S_e * 2^(e-150) (e >= 1), folded in a big integer and
 // rounded once to double (nearest, ties to even).
 double exact_sum_to_double(const unsigned long long hist[256]) {

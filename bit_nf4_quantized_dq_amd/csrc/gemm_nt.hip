@@ -29,6 +29,7 @@
 // ksplit workgroups per tile (blockIdx.z).  Each writes its FP32 partial tile to the
 // workspace; k_sum_parts then adds the ksplit partials in a fixed order and rounds to BF16.
 // The adapter slices run in split 0 only.
+#include "adapters_device.h"
 #include "qlora_device.h"
 #include "qlora_host.h"
 
@@ -219,6 +220,108 @@ __device__ __forceinline__ void adapter(const uint16_t* __restrict__ wl, int64_t
   }
 }
 
+// The adapters' term where each row of B names its own adapter a (AdapterHead): acc[f][m] = sum_j
+// W_a(f, j) scale s_a U[m][j], under the mask of drop.  A wavefront finds the distinct adapters of
+// its 64 tokens by ballots; each one's W_a rows go from memory to the operand registers (8
+// ranks per lane: one vector of B_a, or eight strided elements of A_a), its tokens' U as hi and lo
+// BF16 parts, other tokens' as zeros.  The products of one adapter are summed apart and added for
+// its tokens only, so that values that are not finite stay with the rows that name them.
+// Registers only: no LDS and no barrier while the ring's first loads are in flight.
+template <bool WT>
+__device__ __forceinline__ void adapter_rows(const AdapterHead& h, int64_t F, int64_t f0, int64_t m0, int l32, int h32,
+                                             Acc& acc) {
+  const int32_t width = h.rows.width;
+  const rsrc_t ru = make_rsrc(h.U + m0 * width, (h.rows.M - m0) * width * 4);
+  int id[TJ];
+  uint64_t pending[TJ];
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    id[j] = adapter_of(h.rows, m0 + 32 * j + l32);
+    pending[j] = __ballot(id[j] >= 0);
+  }
+  while (pending[0] | pending[1]) {
+    const int cur = pending[0] ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(pending[0]))
+                               : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(pending[1]));
+    const AdapterEntry e = h.rows.table[cur];
+    const rsrc_t rw = make_rsrc(WT ? e.A : e.B, F * e.r * 2);
+    const float scale = e.s * h.scale;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) pending[j] &= ~__ballot(id[j] == cur);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const bool mine = id[j] == cur;
+      if (!__ballot(mine)) continue;
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        f32x16_t t = {};
+        for (int r0 = 0; r0 < e.r; r0 += 16) {
+          // formed anew at each step, so that no tile's offsets are held in registers
+          uint32_t f = (uint32_t)f0 + 32 * i + l32;
+          int r = r0 + 8 * h32;
+          asm volatile("" : "+v"(f), "+v"(r));
+          uint4 w;
+          if (!WT && h.rows.whole) {
+            w = bload16(rw, (f < F && r < e.r) ? (f * e.r + r) * 2 : kOOB);
+          } else {
+            uint32_t x[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const uint32_t off = WT ? ((r + q) * (uint32_t)F + f) * 2 : (f * e.r + r + q) * 2;
+              x[q] = __builtin_amdgcn_raw_buffer_load_b16(rw, (f < F && r + q < e.r) ? (int)off : (int)kOOB, 0, 0);
+            }
+            w = make_uint4((x[0] & 0xFFFFu) | (x[1] << 16), (x[2] & 0xFFFFu) | (x[3] << 16), (x[4] & 0xFFFFu) | (x[5] << 16),
+                           (x[6] & 0xFFFFu) | (x[7] << 16));
+          }
+          const uint32_t off = (mine && r < width) ? (uint32_t)(((32 * j + l32) * width + r) * 4) : kOOB;
+          const uint4 a = bload16(ru, off), b = bload16(ru, off == kOOB ? kOOB : off + 16);
+          const float v[8] = {__uint_as_float(a.x) * scale, __uint_as_float(a.y) * scale, __uint_as_float(a.z) * scale,
+                              __uint_as_float(a.w) * scale, __uint_as_float(b.x) * scale, __uint_as_float(b.y) * scale,
+                              __uint_as_float(b.z) * scale, __uint_as_float(b.w) * scale};
+          uint4 hi, lo;
+          split_bf16(v, hi, lo);
+          t = mfma32(as_bf16x8(w), as_bf16x8(hi), t);
+          t = mfma32(as_bf16x8(w), as_bf16x8(lo), t);
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] += mine ? t[q] : 0.f;
+        __builtin_amdgcn_sched_barrier(0);  // one tile's temporaries at a time
+      }
+    }
+  }
+}
+
+// The mask over acc (the adapters' term): register 4q + v of tile (i, j) is element (m0 + 32 j +
+// l32, f0 + 32 i + 8 q + 4 h32 + v), so the lanes l and l + 32 share the generator's blocks of
+// eight: lane half h computes the block of q = 2p + h and the halves swap two of its four words.
+__device__ __forceinline__ void drop_acc(const DropMask& drop, int64_t F, int64_t f0, int64_t m0, int l32, int h32,
+                                         Acc& acc) {
+  const RngKey key = load_rng(drop.rng);
+  const uint32_t t2 = threshold_halves(drop.threshold);
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    const uint64_t row = (uint64_t)(m0 + 32 * j + l32) * (uint64_t)(F / 8) + (uint64_t)(f0 / 8);
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint4 w = philox(key, row + (uint64_t)(4 * i + 2 * p + h32));
+        // the upper half's first and the lower half's second argument change places
+        const auto s0 = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
+        const uint32_t k[4] = {keep_halves(s0[0], t2), keep_halves(s1[0], t2), keep_halves(s0[1], t2), keep_halves(s1[1], t2)};
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const uint32_t bits = (v & 1) ? k[2 * q + (v >> 1)] >> 16 : k[2 * q + (v >> 1)] & 0xFFFFu;
+            const int at = 4 * (2 * p + q) + v;
+            acc[i][j][at] = bits ? acc[i][j][at] : 0.f;
+          }
+        __builtin_amdgcn_sched_barrier(0);  // one block's words at a time
+      }
+  }
+}
+
 // Epilogue.  C is [M, F] BF16 (token-major).  Register 4q + v of tile (i, j) holds feature
 // 32 i + 8 q + 4 h32 + v of token 32 j + l32 within the wavefront's 128 x 64 tile.  The tile
 // is staged in 16 KB of LDS as 64 token rows of 256 bytes (32 units of 8 bytes; unit u of
@@ -399,13 +502,20 @@ __device__ __forceinline__ void nt_step(const Ring& ra, const Ring& rb, uint32_t
   }
 }
 
-template <bool SPLIT, bool FULLK>
-__global__ __launch_bounds__(kThreads, 1) void k_gemm_nt(const uint16_t* __restrict__ A, int64_t F,
-                                                         const uint16_t* __restrict__ B, int64_t M, int64_t Kr,
-                                                         const uint16_t* __restrict__ wl, int64_t wl_fs,
-                                                         int64_t wl_js, const uint16_t* __restrict__ Lm, int32_t r,
-                                                         uint16_t* __restrict__ C, float* __restrict__ part,
-                                                         uint32_t kb_per) {
+// Whose adapter term starts the accumulators: one adapter's for all rows (adapter()), or each
+// row's own (adapter_rows(), W_a = B_a or A_a^T).
+enum HeadKind { kOneAdapter, kRowsB, kRowsA };
+struct OneAdapter {
+  const uint16_t* wl;
+  int64_t wl_fs, wl_js;
+  const uint16_t* Lm;
+  int32_t r;
+};
+
+template <bool SPLIT, bool FULLK, HeadKind HEAD, class Head>
+__device__ __forceinline__ void gemm_nt_body(const uint16_t* __restrict__ A, int64_t F,
+                                             const uint16_t* __restrict__ B, int64_t M, int64_t Kr, const Head& head,
+                                             uint16_t* __restrict__ C, float* __restrict__ part, uint32_t kb_per) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, h32 = lane >> 5;
   const int wf = (wave & 1) * 128, wmt = (wave >> 1) * 64;
@@ -436,7 +546,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_nt(const uint16_t* __restr
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x16_t{};
-  if (!SPLIT || blockIdx.z == 0) adapter(wl, wl_fs, wl_js, F, Lm, M, r, f0, m0, tid, wf, wmt, l32, h32, acc);
+  if (!SPLIT || blockIdx.z == 0) {
+    if constexpr (HEAD == kOneAdapter) {
+      adapter(head.wl, head.wl_fs, head.wl_js, F, head.Lm, M, head.r, f0, m0, tid, wf, wmt, l32, h32, acc);
+    } else {
+      adapter_rows<HEAD == kRowsA>(head, F, f0 + wf, m0 + wmt, l32, h32, acc);
+      if (HEAD == kRowsA && head.drop.threshold) drop_acc(head.drop, F, f0 + wf, m0 + wmt, l32, h32, acc);
+    }
+  }
   wait_vm<0>();
   lds_barrier();  // steps 0, 1 landed everywhere; the adapter's reads of slot 4 are done
 
@@ -475,6 +592,33 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_nt(const uint16_t* __restr
     store_tile(C, M, F, f0 + wf, m0 + wmt, wave, lane, l32, h32, acc);
 }
 
+template <bool SPLIT, bool FULLK>
+__global__ __launch_bounds__(kThreads, 1) void k_gemm_nt(const uint16_t* __restrict__ A, int64_t F,
+                                                         const uint16_t* __restrict__ B, int64_t M, int64_t Kr,
+                                                         const uint16_t* __restrict__ wl, int64_t wl_fs,
+                                                         int64_t wl_js, const uint16_t* __restrict__ Lm, int32_t r,
+                                                         uint16_t* __restrict__ C, float* __restrict__ part,
+                                                         uint32_t kb_per) {
+  gemm_nt_body<SPLIT, FULLK, kOneAdapter>(A, F, B, M, Kr, OneAdapter{wl, wl_fs, wl_js, Lm, r}, C, part, kb_per);
+}
+
+template <bool SPLIT, bool FULLK, HeadKind HEAD>
+__global__ __launch_bounds__(kThreads, 1) void k_gemm_nt_rows(const uint16_t* __restrict__ A, int64_t F,
+                                                              const uint16_t* __restrict__ B, int64_t M, int64_t Kr,
+                                                              AdapterHead head, uint16_t* __restrict__ C,
+                                                              float* __restrict__ part, uint32_t kb_per) {
+  gemm_nt_body<SPLIT, FULLK, HEAD>(A, F, B, M, Kr, head, C, part, kb_per);
+}
+
+}  // namespace
+
+namespace {
+hipError_t sum_parts(const float* part, int32_t ksplit, int64_t M, int64_t F, uint16_t* C, hipStream_t st) {
+  const int64_t n8 = M * F / 8;
+  const int64_t blocks = std::min<int64_t>((n8 + 255) / 256, 2048);
+  hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)blocks), dim3(256), 0, st, part, ksplit, M, F, C);
+  return hipGetLastError();
+}
 }  // namespace
 
 int32_t gemm_nt_ksplit(int64_t F, int64_t M, int64_t Kr) {
@@ -507,10 +651,31 @@ hipError_t launch_gemm_nt(const uint16_t* A, int64_t F, const uint16_t* B, int64
 #undef GEMM_ARGS
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || ksplit <= 1) return e;
-  const int64_t n8 = M * F / 8;
-  const int64_t blocks = std::min<int64_t>((n8 + 255) / 256, 2048);
-  hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)blocks), dim3(256), 0, st, part, ksplit, M, F, C);
-  return hipGetLastError();
+  return sum_parts(part, ksplit, M, F, C, st);
+}
+
+hipError_t launch_gemm_nt_adapters(const uint16_t* A, int64_t F, const uint16_t* B, int64_t M, int64_t Kr,
+                                   const AdapterHead& head, uint16_t* C, int kernel_id, hipStream_t st, float* part,
+                                   int32_t ksplit) {
+  const int64_t nk = (Kr + BK - 1) / BK;
+  if (ksplit > 1 && (!part || F % 16 != 0)) return hipErrorInvalidValue;
+  const uint32_t kb_per = ksplit > 1 ? (uint32_t)((nk + ksplit - 1) / ksplit) : (uint32_t)nk;
+  const dim3 grid((unsigned)((F + BF - 1) / BF), (unsigned)((M + BMT - 1) / BMT), (unsigned)(ksplit > 1 ? ksplit : 1));
+  LaunchTimer t(kernel_id, st);
+  const auto go = [&](auto kernel) {
+    hipExtLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, t.start, t.stop, 0, A, F, B, M, Kr, head, C, part, kb_per);
+  };
+  const bool fullk = Kr % BK == 0;
+  if (head.transposed) {
+    if (ksplit > 1) fullk ? go(k_gemm_nt_rows<true, true, kRowsA>) : go(k_gemm_nt_rows<true, false, kRowsA>);
+    else fullk ? go(k_gemm_nt_rows<false, true, kRowsA>) : go(k_gemm_nt_rows<false, false, kRowsA>);
+  } else {
+    if (ksplit > 1) fullk ? go(k_gemm_nt_rows<true, true, kRowsB>) : go(k_gemm_nt_rows<true, false, kRowsB>);
+    else fullk ? go(k_gemm_nt_rows<false, true, kRowsB>) : go(k_gemm_nt_rows<false, false, kRowsB>);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || ksplit <= 1) return e;
+  return sum_parts(part, ksplit, M, F, C, st);
 }
 
 }  // namespace qlora
