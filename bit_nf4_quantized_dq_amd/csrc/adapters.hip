@@ -16,29 +16,7 @@
 namespace qlora {
 namespace {
 
-typedef short v4i16 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
-
-// 8 consecutive rows 8 (lane >> 4) .. +7 of column (lane & 15) of an LDS tile of BF16 rows of 32
-// bytes, by two transposing reads (as in lora.hip: within 16 lanes, lane i receives element
-// i % 4 of the 8 bytes that lanes i/4, i/4 + 4, i/4 + 8, i/4 + 12 address).
-__device__ __forceinline__ bf16x8_t tr_operand(const char* tile, int lane) {
-  const int j = lane & 15, g = lane >> 4;
-  const char* p0 = tile + (8 * g + (j >> 2)) * 32 + 8 * (j & 3);
-  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p0));
-  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p0 + 4 * 32));
-  bf16x8_t r;
-  r[0] = lo[0]; r[1] = lo[1]; r[2] = lo[2]; r[3] = lo[3];
-  r[4] = hi[0]; r[5] = hi[1]; r[6] = hi[2]; r[7] = hi[3];
-  return r;
-}
-
 __device__ __forceinline__ int lowest(uint64_t mask) { return __builtin_ctzll(mask); }
-__device__ __forceinline__ uint64_t readlane64(uint64_t v, int lane) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
-  return ((uint64_t)hi << 32) | lo;
-}
 
 // ---------------------------------------------------------------- the table
 __global__ __launch_bounds__(128) void k_adapter_table(AdapterBatch batch, int count, AdapterEntry* __restrict__ table) {
@@ -174,7 +152,7 @@ __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a,
           for (int t = 0; t < JT; ++t) *reinterpret_cast<uint4*>(qs + t * 1024 + (lane >> 1) * 32 + 16 * (lane & 1)) = qv[d][t];
           asm volatile("" ::: "memory");
 #pragma unroll
-          for (int t = 0; t < JT; ++t) qa[t] = tr_operand(qs + t * 1024, lane);
+          for (int t = 0; t < JT; ++t) qa[t] = tr_operand(qs + t * 1024, l16, 8 * g);
           asm volatile("" ::: "memory");
         }
         const uint4 p = DROP ? drop8(pv[d], key, block0 + (uint64_t)(4 * slab[d] + g), t2) : pv[d];
@@ -518,10 +496,10 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
         asm volatile("" ::: "memory");
         bf16x8_t b[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) b[q] = tr_operand(vt + q * kVTile, lane);
+        for (int q = 0; q < 4; ++q) b[q] = tr_operand(vt + q * kVTile, lane & 15, 8 * (lane >> 4));
 #pragma unroll
         for (int t = 0; t < JT; ++t) {
-          const bf16x8_t hi = tr_operand(ut + t * kVTile, lane), lo = tr_operand(ut + (JT + t) * kVTile, lane);
+          const bf16x8_t hi = tr_operand(ut + t * kVTile, lane & 15, 8 * (lane >> 4)), lo = tr_operand(ut + (JT + t) * kVTile, lane & 15, 8 * (lane >> 4));
 #pragma unroll
           for (int q = 0; q < 4; ++q) acc[t][q] = mfma16x16x32(lo, b[q], mfma16x16x32(hi, b[q], acc[t][q]));
         }

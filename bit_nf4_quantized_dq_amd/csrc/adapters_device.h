@@ -69,6 +69,49 @@ __device__ __forceinline__ void split_bf16(const float f[8], uint4& hi, uint4& l
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// ---- operands
+typedef short lds_i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) lds_i16x4 lds_i16x4_t;
+
+// 8 consecutive rows k .. k + 7 of column i (0..15) of an LDS tile of BF16 rows of 32 bytes, by two
+// transposing reads (as in lora.hip: within 16 lanes, lane i receives element i % 4 of the 8
+// bytes that lanes i/4, i/4 + 4, i/4 + 8, i/4 + 12 address).
+__device__ __forceinline__ bf16x8_t tr_operand(const char* tile, int i, int k) {
+  const char* p0 = tile + (k + (i >> 2)) * 32 + 8 * (i & 3);
+  const lds_i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p0));
+  const lds_i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p0 + 4 * 32));
+  bf16x8_t r;
+  r[0] = lo[0]; r[1] = lo[1]; r[2] = lo[2]; r[3] = lo[3];
+  r[4] = hi[0]; r[5] = hi[1]; r[6] = hi[2]; r[7] = hi[3];
+  return r;
+}
+
+__device__ __forceinline__ uint64_t readlane64(uint64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// Elements at .. at + 7 of a row that starts at `row` of a matrix of `total` BF16 (at least 8) and
+// has n: zeros from n on.  Rows of any width, so the vector may start at any element; near the
+// matrix's end it starts early enough to stay inside and is shifted.
+__device__ __forceinline__ uint4 load_row8(const uint16_t* __restrict__ p, int64_t total, int64_t row, int at, int n) {
+  typedef uint32_t u32x4_e2 __attribute__((ext_vector_type(4), aligned(2)));
+  const int left = n - at;  // elements of the row
+  const int64_t first = row + (left > 0 ? at : 0), start = first < total - 8 ? first : total - 8;
+  u32x4_e2 v = *reinterpret_cast<const u32x4_e2*>(p + start);
+  const int shift = (int)(first - start);
+  if (__ballot(shift)) {
+    uint64_t a = ((uint64_t)v.y << 32) | v.x, b = ((uint64_t)v.w << 32) | v.z;
+    const int bits = 16 * shift;
+    if (bits >= 64) a = b >> (bits - 64), b = 0;
+    else if (bits) a = (a >> bits) | (b << (64 - bits)), b >>= bits;
+    v.x = (uint32_t)a, v.y = (uint32_t)(a >> 32), v.z = (uint32_t)b, v.w = (uint32_t)(b >> 32);
+  }
+  const auto keep = [&](int i) { return left >= 2 * i + 2 ? ~0u : (left == 2 * i + 1 ? 0xFFFFu : 0u); };
+  return make_uint4(v.x & keep(0), v.y & keep(1), v.z & keep(2), v.w & keep(3));
+}
+
 // Row m's adapter, -1 for none (also past the rows).
 __device__ __forceinline__ int adapter_of(const AdapterRows& rows, int64_t m) {
   if (m >= rows.M) return -1;

@@ -29,7 +29,7 @@
 // ksplit workgroups per tile (blockIdx.z).  Each writes its FP32 partial tile to the
 // workspace; k_sum_parts then adds the ksplit partials in a fixed order and rounds to BF16.
 // The adapter slices run in split 0 only.
-#include "adapters_device.h"
+#include "adapter_head.h"
 #include "qlora_device.h"
 #include "qlora_host.h"
 
@@ -43,8 +43,8 @@ constexpr int BK = 32;                // reduction step
 constexpr int kChunks = BK / 8;       // 16-byte chunks per LDS row
 constexpr int kSlot = 256 * kChunks;  // 16-byte chunks per ring slot (16 KB)
 constexpr int TI = 4, TJ = 2;         // 32x32 MFMA tiles per wavefront
-typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
-typedef f32x16_t Acc[TI][TJ];
+static_assert(TI == kHeadTI && TJ == kHeadTJ, "adapter_head.h starts these accumulators");
+typedef HeadAcc Acc;
 typedef __attribute__((address_space(3))) void lds_void;
 
 // Two rings of five 16 KB slots (160 KB, all of a CU's LDS).
@@ -60,10 +60,6 @@ template <int I> __device__ __forceinline__ uint4* abuf() {
 }
 template <int I> __device__ __forceinline__ uint4* bbuf() {
   return I == 0 ? s_b0 : (I == 1 ? s_b1 : (I == 2 ? s_b2 : (I == 3 ? s_b3 : s_b4)));
-}
-
-__device__ __forceinline__ f32x16_t mfma32(const bf16x8_t& a, const bf16x8_t& b, const f32x16_t& c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
 __device__ __forceinline__ int swz(int row, int chunk) {
@@ -217,108 +213,6 @@ __device__ __forceinline__ void adapter(const uint16_t* __restrict__ wl, int64_t
     for (int c = 0; c < kChunks; ++c) dst[swz(row, c)] = c4[c];
     lds_barrier();
     mma_step(abuf<4>(), bbuf<4>(), wf, wmt, l32, h32, acc);
-  }
-}
-
-// The adapters' term where each row of B names its own adapter a (AdapterHead): acc[f][m] = sum_j
-// W_a(f, j) scale s_a U[m][j], under the mask of drop.  A wavefront finds the distinct adapters of
-// its 64 tokens by ballots; each one's W_a rows go from memory to the operand registers (8
-// ranks per lane: one vector of B_a, or eight strided elements of A_a), its tokens' U as hi and lo
-// BF16 parts, other tokens' as zeros.  The products of one adapter are summed apart and added for
-// its tokens only, so that values that are not finite stay with the rows that name them.
-// Registers only: no LDS and no barrier while the ring's first loads are in flight.
-template <bool WT>
-__device__ __forceinline__ void adapter_rows(const AdapterHead& h, int64_t F, int64_t f0, int64_t m0, int l32, int h32,
-                                             Acc& acc) {
-  const int32_t width = h.rows.width;
-  const rsrc_t ru = make_rsrc(h.U + m0 * width, (h.rows.M - m0) * width * 4);
-  int id[TJ];
-  uint64_t pending[TJ];
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    id[j] = adapter_of(h.rows, m0 + 32 * j + l32);
-    pending[j] = __ballot(id[j] >= 0);
-  }
-  while (pending[0] | pending[1]) {
-    const int cur = pending[0] ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(pending[0]))
-                               : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(pending[1]));
-    const AdapterEntry e = h.rows.table[cur];
-    const rsrc_t rw = make_rsrc(WT ? e.A : e.B, F * e.r * 2);
-    const float scale = e.s * h.scale;
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) pending[j] &= ~__ballot(id[j] == cur);
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      const bool mine = id[j] == cur;
-      if (!__ballot(mine)) continue;
-#pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        f32x16_t t = {};
-        for (int r0 = 0; r0 < e.r; r0 += 16) {
-          // formed anew at each step, so that no tile's offsets are held in registers
-          uint32_t f = (uint32_t)f0 + 32 * i + l32;
-          int r = r0 + 8 * h32;
-          asm volatile("" : "+v"(f), "+v"(r));
-          uint4 w;
-          if (!WT && h.rows.whole) {
-            w = bload16(rw, (f < F && r < e.r) ? (f * e.r + r) * 2 : kOOB);
-          } else {
-            uint32_t x[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const uint32_t off = WT ? ((r + q) * (uint32_t)F + f) * 2 : (f * e.r + r + q) * 2;
-              x[q] = __builtin_amdgcn_raw_buffer_load_b16(rw, (f < F && r + q < e.r) ? (int)off : (int)kOOB, 0, 0);
-            }
-            w = make_uint4((x[0] & 0xFFFFu) | (x[1] << 16), (x[2] & 0xFFFFu) | (x[3] << 16), (x[4] & 0xFFFFu) | (x[5] << 16),
-                           (x[6] & 0xFFFFu) | (x[7] << 16));
-          }
-          const uint32_t off = (mine && r < width) ? (uint32_t)(((32 * j + l32) * width + r) * 4) : kOOB;
-          const uint4 a = bload16(ru, off), b = bload16(ru, off == kOOB ? kOOB : off + 16);
-          const float v[8] = {__uint_as_float(a.x) * scale, __uint_as_float(a.y) * scale, __uint_as_float(a.z) * scale,
-                              __uint_as_float(a.w) * scale, __uint_as_float(b.x) * scale, __uint_as_float(b.y) * scale,
-                              __uint_as_float(b.z) * scale, __uint_as_float(b.w) * scale};
-          uint4 hi, lo;
-          split_bf16(v, hi, lo);
-          t = mfma32(as_bf16x8(w), as_bf16x8(hi), t);
-          t = mfma32(as_bf16x8(w), as_bf16x8(lo), t);
-        }
-#pragma unroll
-        for (int q = 0; q < 16; ++q) acc[i][j][q] += mine ? t[q] : 0.f;
-        __builtin_amdgcn_sched_barrier(0);  // one tile's temporaries at a time
-      }
-    }
-  }
-}
-
-// The mask over acc (the adapters' term): register 4q + v of tile (i, j) is element (m0 + 32 j +
-// l32, f0 + 32 i + 8 q + 4 h32 + v), so the lanes l and l + 32 share the generator's blocks of
-// eight: lane half h computes the block of q = 2p + h and the halves swap two of its four words.
-__device__ __forceinline__ void drop_acc(const DropMask& drop, int64_t F, int64_t f0, int64_t m0, int l32, int h32,
-                                         Acc& acc) {
-  const RngKey key = load_rng(drop.rng);
-  const uint32_t t2 = threshold_halves(drop.threshold);
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    const uint64_t row = (uint64_t)(m0 + 32 * j + l32) * (uint64_t)(F / 8) + (uint64_t)(f0 / 8);
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const uint4 w = philox(key, row + (uint64_t)(4 * i + 2 * p + h32));
-        // the upper half's first and the lower half's second argument change places
-        const auto s0 = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);
-        const auto s1 = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
-        const uint32_t k[4] = {keep_halves(s0[0], t2), keep_halves(s1[0], t2), keep_halves(s0[1], t2), keep_halves(s1[1], t2)};
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const uint32_t bits = (v & 1) ? k[2 * q + (v >> 1)] >> 16 : k[2 * q + (v >> 1)] & 0xFFFFu;
-            const int at = 4 * (2 * p + q) + v;
-            acc[i][j][at] = bits ? acc[i][j][at] : 0.f;
-          }
-        __builtin_amdgcn_sched_barrier(0);  // one block's words at a time
-      }
   }
 }
 
@@ -546,13 +440,15 @@ __device__ __forceinline__ void gemm_nt_body(const uint16_t* __restrict__ A, int
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x16_t{};
-  if (!SPLIT || blockIdx.z == 0) {
-    if constexpr (HEAD == kOneAdapter) {
+  if constexpr (HEAD == kOneAdapter) {
+    if (!SPLIT || blockIdx.z == 0)
       adapter(head.wl, head.wl_fs, head.wl_js, F, head.Lm, M, head.r, f0, m0, tid, wf, wmt, l32, h32, acc);
-    } else {
-      adapter_rows<HEAD == kRowsA>(head, F, f0 + wf, m0 + wmt, l32, h32, acc);
-      if (HEAD == kRowsA && head.drop.threshold) drop_acc(head.drop, F, f0 + wf, m0 + wmt, l32, h32, acc);
-    }
+  } else {
+    // slots 3 and 4 are free until the first barrier
+    char* lds = reinterpret_cast<char*>(wave < 4 ? (wave < 2 ? s_a3 : s_a4) : (wave < 6 ? s_b3 : s_b4)) + (wave & 1) * 8192;
+    const bool any = adapter_rows<HEAD == kRowsA>(head, F, f0 + wf, m0 + wmt, lane, lds, SPLIT ? blockIdx.z : 0u,
+                                                  SPLIT ? gridDim.z : 1u, acc);
+    if (HEAD == kRowsA && any && head.drop.threshold) drop_acc(head.drop, F, f0 + wf, m0 + wmt, l32, h32, acc);
   }
   wait_vm<0>();
   lds_barrier();  // steps 0, 1 landed everywhere; the adapter's reads of slot 4 are done
