@@ -87,7 +87,7 @@ __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a,
   char* qs = smem + wave * JT * 1024;
 
   uint64_t pending = __ballot(id >= 0);
-  int cur = -1, at = wave;  // the adapter's lane, and the slab within the slice
+  int cur = -1, from = 0, at = wave;  // the adapter's lane (`from`: the last one's), the slab within the slice
   if (len > 0 && pending) {
     cur = lowest(pending);
     const auto step = [&](int by) {  // to the item `by` further on
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a,
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         const bool live = cur >= 0;
-        const int from = live ? cur : 0;
+        from = live ? cur : from;
         which[d] = live ? __builtin_amdgcn_readlane(id, from) : -2;
         slab[d] = sbeg + at;
         const int r = __builtin_amdgcn_readlane(rank, from);
@@ -124,16 +124,10 @@ __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a,
 #pragma unroll
           for (int t = 0; t < JT; ++t) {
             const int j = 16 * t + 8 * (lane & 1);
-            if (VEC) {
+            if (VEC)
               qv[d][t] = bload16(rq, (kr < Kd && j < r) ? (uint32_t)((kr * r + j) * 2) : kOOB);
-            } else {
-              uint32_t e[8];
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                e[q] = __builtin_amdgcn_raw_buffer_load_b16(rq, (kr < Kd && j + q < r) ? (int)((kr * r + j + q) * 2) : (int)kOOB, 0, 0);
-              qv[d][t] = make_uint4((e[0] & 0xFFFFu) | (e[1] << 16), (e[2] & 0xFFFFu) | (e[3] << 16),
-                                    (e[4] & 0xFFFFu) | (e[5] << 16), (e[6] & 0xFFFFu) | (e[7] << 16));
-            }
+            else  // past the rows (or without an item) the last row again, whose product with zeros is not taken
+              qv[d][t] = load_row8(reinterpret_cast<const uint16_t*>(readlane64(base, from)), Kd * r, (kr < Kd ? kr : Kd - 1) * r, j, r);
           }
         }
         if (live) step(kShrinkWaves);
@@ -249,6 +243,17 @@ hipError_t shrink_by_rank(const ShrinkArgs& a, const ShrinkDecode* dec, const Nf
 }
 
 // ---------------------------------------------------------------- few rows: the weight's stream
+// Rows of 16 lanes 1 and 3 of a change places with rows 0 and 2 of b; the upper 32 lanes of a with
+// the lower 32 of b.
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto s = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = s[0], b = s[1];
+}
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto s = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = s[0], b = s[1];
+}
+
 constexpr int kStreamThreads = 512;
 constexpr int kStreamWaves = kStreamThreads / 64;
 constexpr int kStreamRows = 16;  // weight rows per workgroup
@@ -265,9 +270,15 @@ struct StreamArgs {
 
 // 16 weight rows over the whole reduction.  A wavefront takes groups of four 64-weight blocks;
 // lane (l16, g) decodes block 4 group + g of row l16 (32 bytes of codes, one level table scaled by
-// the block's constant: exactly w_hat), so word i of the four blocks is one MFMA 16x16x32 operand
-// whose reduction indices are 64 (4 group + g) + 8 i .. +7, and X is read in the same order.
-template <int MT>
+// the block's constant: exactly w_hat).  The four lanes of a row then exchange their words (a 4 x 4
+// transpose by lane swaps), so that an MFMA 16x16x32 operand holds 32 consecutive columns and X is
+// read in whole 64-byte pieces of a row (in the blocks' order every lane of a load of X fell into
+// a cache line of its own: 37 rows at 14336 x 4096 91 us).
+//
+// The adapters' term is more of the same sum: the wavefronts deal the distinct adapters of all rows
+// among themselves, and each multiplies its ones' 16 rows of B with T (hi and lo BF16 parts) into
+// its accumulators, before its codes have landed.
+template <int MT, bool WHOLE>
 __global__ __launch_bounds__(kStreamThreads) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
   __shared__ f32x4_t red[kStreamWaves][MT][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -295,40 +306,111 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_stream(StreamArgs a,
     c.c2 = bload4(r2, ok ? ((blk_row + b) >> 8) * 4 : kOOB);
     return c;
   };
+  // each lane its rows' adapters (asked for first: what follows depends on them)
+  int id[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) id[t] = adapter_of(a.rows, 16 * t + l16);
   Codes cur = load(wave), next = load(wave + kStreamWaves);
   const float mu = a.mu[0];
   f32x4_t acc[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (uint32_t group = wave; group < ng; group += kStreamWaves) {
-    const uint32_t b = 4 * group + g;
-    uint32_t xoff[MT];
+
+  // ---- this wavefront's adapters: every eighth distinct one, lane k holding the k-th
+  int mine = 0, count = 0;
+  {
+    uint64_t pending[MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int m = 16 * t + l16;
-      xoff[t] = (m < M && b < nb) ? (uint32_t)((m * K + 64 * (int64_t)b) * 2) : kOOB;
+    for (int t = 0; t < MT; ++t) pending[t] = __ballot(id[t] >= 0);
+    uint32_t skip = wave;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      while (pending[t]) {
+        const int one = __builtin_amdgcn_readlane(id[t], lowest(pending[t]));
+#pragma unroll
+        for (int u = t; u < MT; ++u) pending[u] &= ~__ballot(id[u] == one);
+        if (skip) {
+          --skip;
+        } else {
+          mine = lane == count ? one : mine;
+          ++count;
+          skip = kStreamWaves - 1;
+        }
+      }
+  }
+  if (count) {
+    const AdapterEntry* e = a.rows.table + mine;
+    const uint64_t base_l = reinterpret_cast<uint64_t>(e->B);
+    const int rank_l = e->r;
+    const float scale_l = e->s;
+    const int width = a.rows.width;
+    const rsrc_t rt = make_rsrc(a.T, (int64_t)M * width * 4);
+    for (int k = 0; k < count; ++k) {
+      const int one = __builtin_amdgcn_readlane(mine, k), r = __builtin_amdgcn_readlane(rank_l, k);
+      const uint16_t* B = reinterpret_cast<const uint16_t*>(readlane64(base_l, k));
+      const float s = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_l), k));
+      const rsrc_t rb = make_rsrc(B + row0 * r, (int64_t)kStreamRows * r * 2);
+      for (int r0 = 0; r0 < r; r0 += 32) {
+        const int at = r0 + 8 * g;
+        const uint4 w = WHOLE ? bload16(rb, at < r ? (uint32_t)((l16 * r + at) * 2) : kOOB)
+                              : load_row8(B, N * r, (row0 + l16) * r, at, r);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const bool has = id[t] == one;
+          if (!__ballot(has)) continue;
+          const uint32_t off = (has && at < width) ? (uint32_t)(((16 * t + l16) * width + at) * 4) : kOOB;
+          const uint4 x = bload16(rt, off), y = bload16(rt, off == kOOB ? kOOB : off + 16);
+          const float v[8] = {__uint_as_float(x.x) * s, __uint_as_float(x.y) * s, __uint_as_float(x.z) * s,
+                              __uint_as_float(x.w) * s, __uint_as_float(y.x) * s, __uint_as_float(y.y) * s,
+                              __uint_as_float(y.z) * s, __uint_as_float(y.w) * s};
+          uint4 hi, lo;
+          split_bf16(v, hi, lo);
+          const f32x4_t p = mfma16x16x32(as_bf16x8(w), as_bf16x8(lo),
+                                         mfma16x16x32(as_bf16x8(w), as_bf16x8(hi), f32x4_t{0.f, 0.f, 0.f, 0.f}));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][i] += has ? p[i] : 0.f;
+        }
+      }
     }
+  }
+
+  // ---- the base product
+  uint32_t row_at[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) row_at[t] = 16 * t + l16 < M ? (uint32_t)((16 * t + l16) * K * 2) : kOOB;
+  for (uint32_t group = wave; group < ng; group += kStreamWaves) {
     const Codes c = cur;
     cur = next;
     next = load(group + 2 * kStreamWaves);
     Lut L;
     build_scaled_lut(tab, block_scale(c.c8, __uint_as_float(c.c2), mu), L);
     const uint32_t words[8] = {c.c0.x, c.c0.y, c.c0.z, c.c0.w, c.c1.x, c.c1.y, c.c1.z, c.c1.w};
+    uint32_t w[8][4];  // word i of this lane's block; then, of block i % 4, word 4 (i / 4) + g
+#pragma unroll
+    for (int i = 0; i < 8; ++i) decode8(words[i], L, w[i]);
+#pragma unroll
+    for (int h = 0; h < 8; h += 4)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        swap16(w[h][q], w[h + 1][q]);
+        swap16(w[h + 2][q], w[h + 3][q]);
+        swap32(w[h][q], w[h + 2][q]);
+        swap32(w[h + 1][q], w[h + 3][q]);
+      }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      const uint32_t k = 64 * (4 * group + (i & 3)) + 32 * (i >> 2) + 8 * g;
       uint4 x[MT];
 #pragma unroll
-      for (int t = 0; t < MT; ++t) x[t] = bload16(rx, xoff[t] == kOOB ? kOOB : xoff[t] + 16 * i);
-      uint32_t w[4];
-      decode8(words[i], L, w);
+      for (int t = 0; t < MT; ++t) x[t] = bload16(rx, (row_at[t] != kOOB && k < K) ? row_at[t] + 2 * k : kOOB);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) acc[t] = mfma16x16x32(as_bf16x8(w), as_bf16x8(x[t]), acc[t]);
+      for (int t = 0; t < MT; ++t) acc[t] = mfma16x16x32(as_bf16x8(w[i]), as_bf16x8(x[t]), acc[t]);
     }
   }
 #pragma unroll
   for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
   __syncthreads();
-  // lane l of item t: row 16 t + (l & 15) of X, weight rows 4 (l >> 4) + v
+  // the wavefronts' sums in order; lane l of tile t: row 16 t + (l & 15) of X, weight rows 4 (l >> 4) + v
   for (int t = wave; t < MT; t += kStreamWaves) {
     const int m = 16 * t + l16;
     if (m >= M) continue;
@@ -338,36 +420,8 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_stream(StreamArgs a,
       const f32x4_t v = red[w][t][lane];
       y[0] += v[0]; y[1] += v[1]; y[2] += v[2]; y[3] += v[3];
     }
-    const int64_t n = row0 + 4 * g;
-    const int id = adapter_of(a.rows, m);
-    if (id >= 0) {
-      const AdapterEntry e = a.rows.table[id];
-      const float* T = a.T + (int64_t)m * a.rows.width;
-      const uint16_t* B = e.B + n * e.r;
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      if (a.rows.whole) {
-        for (int j = 0; j < e.r; j += 8) {
-          const f32x4_t t0 = *reinterpret_cast<const f32x4_t*>(T + j), t1 = *reinterpret_cast<const f32x4_t*>(T + j + 4);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const uint4 b = *reinterpret_cast<const uint4*>(B + v * e.r + j);
-            s[v] = fmaf(t0[0], bf16lo_to_f32(b.x), s[v]); s[v] = fmaf(t0[1], bf16hi_to_f32(b.x), s[v]);
-            s[v] = fmaf(t0[2], bf16lo_to_f32(b.y), s[v]); s[v] = fmaf(t0[3], bf16hi_to_f32(b.y), s[v]);
-            s[v] = fmaf(t1[0], bf16lo_to_f32(b.z), s[v]); s[v] = fmaf(t1[1], bf16hi_to_f32(b.z), s[v]);
-            s[v] = fmaf(t1[2], bf16lo_to_f32(b.w), s[v]); s[v] = fmaf(t1[3], bf16hi_to_f32(b.w), s[v]);
-          }
-        }
-      } else {
-        for (int j = 0; j < e.r; ++j) {
-          const float t0 = T[j];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) s[v] = fmaf(t0, __uint_as_float((uint32_t)B[v * e.r + j] << 16), s[v]);
-        }
-      }
-#pragma unroll
-      for (int v = 0; v < 4; ++v) y[v] = fmaf(e.s, s[v], y[v]);
-    }
-    *reinterpret_cast<uint2*>(a.Y + (int64_t)m * N + n) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    *reinterpret_cast<uint2*>(a.Y + (int64_t)m * N + row0 + 4 * g) =
+        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
   }
 }
 
@@ -624,11 +678,16 @@ hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, co
   if (rows.M > kStreamMaxRows) return hipErrorInvalidValue;
   const StreamArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, rows, T, Y};
   const dim3 grid((unsigned)(N / kStreamRows));
-  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kStreamThreads), 0, st, a, tab); };
-  if (rows.M <= 16) go(k_adapter_stream<1>);
-  else if (rows.M <= 32) go(k_adapter_stream<2>);
-  else if (rows.M <= 64) go(k_adapter_stream<4>);
-  else go(k_adapter_stream<8>);
+  const auto go = [&](auto whole, auto not_whole) {
+    if (rows.whole) hipLaunchKernelGGL(whole, grid, dim3(kStreamThreads), 0, st, a, tab);
+    else hipLaunchKernelGGL(not_whole, grid, dim3(kStreamThreads), 0, st, a, tab);
+  };
+  if (rows.M <= 16) go(k_adapter_stream<1, true>, k_adapter_stream<1, false>);
+  else if (rows.M <= 32) go(k_adapter_stream<2, true>, k_adapter_stream<2, false>);
+  else if (rows.M <= 48) go(k_adapter_stream<3, true>, k_adapter_stream<3, false>);
+  else if (rows.M <= 64) go(k_adapter_stream<4, true>, k_adapter_stream<4, false>);
+  else if (rows.M <= 96) go(k_adapter_stream<6, true>, k_adapter_stream<6, false>);
+  else go(k_adapter_stream<8, true>, k_adapter_stream<8, false>);
   return hipGetLastError();
 }
 
