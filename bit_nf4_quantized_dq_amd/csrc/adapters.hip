@@ -271,16 +271,20 @@ struct StreamArgs {
 // 16 weight rows over the whole reduction.  A wavefront takes groups of four 64-weight blocks;
 // lane (l16, g) decodes block 4 group + g of row l16 (32 bytes of codes, one level table scaled by
 // the block's constant: exactly w_hat).  The four lanes of a row then exchange their words (a 4 x 4
-// transpose by lane swaps), so that an MFMA 16x16x32 operand holds 32 consecutive columns and X is
-// read in whole 64-byte pieces of a row (in the blocks' order every lane of a load of X fell into
-// a cache line of its own: 37 rows at 14336 x 4096 91 us).
+// transpose by lane swaps), so that an MFMA 16x16x32 operand holds 32 consecutive columns.  X comes
+// block by block in whole cache lines (eight lanes to a row's 128 bytes), PD blocks ahead in
+// registers, and through LDS of the wavefront's own into operand order; 16-byte chunk c of row r
+// lies at c ^ (r / 2 % 8), so that reads and writes meet all banks.  (Operands straight from memory
+// have neighbouring lanes in 16 rows: 37 rows at 14336 x 4096 91 us in the blocks' order, 56 in
+// 64-byte pieces.)
 //
 // The adapters' term is more of the same sum: the wavefronts deal the distinct adapters of all rows
 // among themselves, and each multiplies its ones' 16 rows of B with T (hi and lo BF16 parts) into
 // its accumulators, before its codes have landed.
-template <int MT, bool WHOLE>
-__global__ __launch_bounds__(kStreamThreads) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
-  __shared__ f32x4_t red[kStreamWaves][MT][64];
+template <int MT, int PD, bool WHOLE>
+__global__ __launch_bounds__(kStreamThreads, MT <= 3 ? 4 : 2) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
+  __shared__ uint4 smem[kStreamWaves * MT * 128];  // a block of X for each wavefront; then the sums
+  f32x4_t(*red)[MT][64] = reinterpret_cast<f32x4_t(*)[MT][64]>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int64_t K = a.K, N = a.N, row0 = (int64_t)blockIdx.x * kStreamRows;
@@ -375,9 +379,20 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_stream(StreamArgs a,
   }
 
   // ---- the base product
-  uint32_t row_at[MT];
+  uint4* xs = smem + wave * MT * 128;
+  uint4 xr[PD][MT][2];
+  // block blk of X: lane p takes chunk (p & 7) ^ (row / 2 % 8) of rows p >> 3 and 8 + (p >> 3) of a tile
+  const auto load_x = [&](uint4 (&x)[MT][2], uint32_t blk) {
 #pragma unroll
-  for (int t = 0; t < MT; ++t) row_at[t] = 16 * t + l16 < M ? (uint32_t)((16 * t + l16) * K * 2) : kOOB;
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int m = 16 * t + 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((4 * i + (lane >> 4)) & 7);
+        x[t][i] = bload16(rx, (m < M && blk < nb) ? (uint32_t)((m * K + 64 * (int64_t)blk + 8 * chunk) * 2) : kOOB);
+      }
+  };
+#pragma unroll
+  for (int d = 0; d < PD; ++d) load_x(xr[d], 4 * wave + d);
   for (uint32_t group = wave; group < ng; group += kStreamWaves) {
     const Codes c = cur;
     cur = next;
@@ -398,15 +413,24 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_stream(StreamArgs a,
         swap32(w[h + 1][q], w[h + 3][q]);
       }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t k = 64 * (4 * group + (i & 3)) + 32 * (i >> 2) + 8 * g;
-      uint4 x[MT];
+    for (int b = 0; b < 4; ++b) {
+      // the wavefront's LDS accesses run in order
+      asm volatile("" ::: "memory");
 #pragma unroll
-      for (int t = 0; t < MT; ++t) x[t] = bload16(rx, (row_at[t] != kOOB && k < K) ? row_at[t] + 2 * k : kOOB);
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int t = 0; t < MT; ++t) acc[t] = mfma16x16x32(as_bf16x8(w[i]), as_bf16x8(x[t]), acc[t]);
+        for (int i = 0; i < 2; ++i) xs[128 * t + 64 * i + lane] = xr[b % PD][t][i];
+      asm volatile("" ::: "memory");
+      load_x(xr[b % PD], 4 * (group + kStreamWaves * ((b + PD) / 4)) + (b + PD) % 4);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          acc[t] = mfma16x16x32(as_bf16x8(w[b + 4 * h]), as_bf16x8(xs[128 * t + 8 * l16 + ((4 * h + g) ^ (l16 >> 1))]), acc[t]);
+      asm volatile("" ::: "memory");
     }
   }
+  __syncthreads();  // the sums take the place of every wavefront's X
 #pragma unroll
   for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
   __syncthreads();
@@ -682,12 +706,12 @@ hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, co
     if (rows.whole) hipLaunchKernelGGL(whole, grid, dim3(kStreamThreads), 0, st, a, tab);
     else hipLaunchKernelGGL(not_whole, grid, dim3(kStreamThreads), 0, st, a, tab);
   };
-  if (rows.M <= 16) go(k_adapter_stream<1, true>, k_adapter_stream<1, false>);
-  else if (rows.M <= 32) go(k_adapter_stream<2, true>, k_adapter_stream<2, false>);
-  else if (rows.M <= 48) go(k_adapter_stream<3, true>, k_adapter_stream<3, false>);
-  else if (rows.M <= 64) go(k_adapter_stream<4, true>, k_adapter_stream<4, false>);
-  else if (rows.M <= 96) go(k_adapter_stream<6, true>, k_adapter_stream<6, false>);
-  else go(k_adapter_stream<8, true>, k_adapter_stream<8, false>);
+  if (rows.M <= 16) go(k_adapter_stream<1, 4, true>, k_adapter_stream<1, 4, false>);
+  else if (rows.M <= 32) go(k_adapter_stream<2, 2, true>, k_adapter_stream<2, 2, false>);
+  else if (rows.M <= 48) go(k_adapter_stream<3, 1, true>, k_adapter_stream<3, 1, false>);
+  else if (rows.M <= 64) go(k_adapter_stream<4, 1, true>, k_adapter_stream<4, 1, false>);
+  else if (rows.M <= 96) go(k_adapter_stream<6, 1, true>, k_adapter_stream<6, 1, false>);
+  else go(k_adapter_stream<8, 1, true>, k_adapter_stream<8, 1, false>);
   return hipGetLastError();
 }
 
