@@ -264,9 +264,93 @@ struct StreamArgs {
   int64_t N, K;
   const uint16_t* X;
   AdapterRows rows;
-  const float* T;
+  DropMask drop;
+  float* T;  // read; where a workgroup forms T itself, written (null: not wanted)
   uint16_t* Y;
+  int32_t lists;
 };
+
+// T for the stream: 16 rows, 16 ranks and every `lists`-th of the rows' distinct adapters, over the
+// whole reduction.  No partial sums cross workgroups (with the reduction split over 16 workgroups
+// and added up by the last of them, 37 rows of 24 adapters took 20 us).  Zeros past a row's rank;
+// list 0 also writes the zeros of rows without an adapter.
+template <bool DROP>
+__global__ __launch_bounds__(kStreamThreads) void k_adapter_t(StreamArgs a) {
+  constexpr int D = 16;
+  __shared__ f32x4_t red[kStreamWaves * 64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int width = a.rows.width, ranks = (width + 15) / 16;
+  const int list = (int)blockIdx.x % a.lists, rest = (int)blockIdx.x / a.lists, jt = rest % ranks, m0 = rest / ranks * kRowTile;
+  const int64_t K = a.K;
+  const int id = adapter_of(a.rows, m0 + l16);
+  uint64_t base = 0;
+  int rank = 0;
+  if (id >= 0) {
+    const AdapterEntry* e = a.rows.table + id;
+    base = reinterpret_cast<uint64_t>(e->A);
+    rank = e->r;
+  }
+  RngKey key{};
+  if (DROP) key = load_rng(a.drop.rng);
+  const uint32_t t2 = threshold_halves(a.drop.threshold);
+  const rsrc_t rp = make_rsrc(a.X + (int64_t)m0 * K, (a.rows.M - m0) * K * 2);
+  const int nslab = (int)(K / 32);
+  f32x4_t out = {0.f, 0.f, 0.f, 0.f};
+  bool write = id < 0 && list == 0;
+  uint64_t pending = __ballot(id >= 0);
+  int skip = list;
+  while (pending) {
+    const int from = lowest(pending), one = __builtin_amdgcn_readlane(id, from), r = __builtin_amdgcn_readlane(rank, from);
+    const bool mine = id == one;
+    pending &= ~__ballot(mine);
+    if (skip) {
+      --skip;
+      continue;
+    }
+    skip = a.lists - 1;
+    write |= mine;
+    if (16 * jt >= r) continue;
+    const rsrc_t rq = make_rsrc(reinterpret_cast<const void*>(readlane64(base, from)), (int64_t)r * K * 2);
+    const int j = 16 * jt + l16;
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = wave; s0 < nslab; s0 += kStreamWaves * D) {
+      uint4 pv[D], qv[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const int slab = s0 + kStreamWaves * d;
+        const int64_t k = 32 * (int64_t)slab + 8 * g;
+        pv[d] = bload16(rp, (mine && slab < nslab) ? (uint32_t)((l16 * K + k) * 2) : kOOB);
+        qv[d] = bload16(rq, (j < r && slab < nslab) ? (uint32_t)((j * K + k) * 2) : kOOB);
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        uint4 p = pv[d];
+        if (DROP) p = drop8(p, key, (uint64_t)(m0 + l16) * (uint64_t)(K / 8) + (uint64_t)(4 * (s0 + kStreamWaves * d) + g), t2);
+        acc = mfma16x16x32(as_bf16x8(qv[d]), as_bf16x8(p), acc);
+      }
+    }
+    // the wavefronts' sums in order; D[j][m]: ranks 4 g + v of row l16
+    red[wave * 64 + lane] = acc;
+    __syncthreads();
+    if (wave == 0) {
+      f32x4_t sum = red[lane];
+#pragma unroll
+      for (int w = 1; w < kStreamWaves; ++w) {
+        const f32x4_t v = red[w * 64 + lane];
+        sum[0] += v[0]; sum[1] += v[1]; sum[2] += v[2]; sum[3] += v[3];
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v) out[v] = mine ? sum[v] : out[v];
+    }
+    __syncthreads();
+  }
+  const int j = 16 * jt + 4 * g;
+  if (wave != 0 || !write || m0 + l16 >= a.rows.M || j >= width) return;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) out[v] = j + v < rank ? out[v] * a.drop.scale : 0.f;
+  *reinterpret_cast<f32x4_t*>(a.T + (int64_t)(m0 + l16) * width + j) = out;
+}
 
 // 16 weight rows over the whole reduction.  A wavefront takes groups of four 64-weight blocks;
 // lane (l16, g) decodes block 4 group + g of row l16 (32 bytes of codes, one level table scaled by
@@ -278,17 +362,21 @@ struct StreamArgs {
 // have neighbouring lanes in 16 rows: 37 rows at 14336 x 4096 91 us in the blocks' order, 56 in
 // 64-byte pieces.)
 //
-// The adapters' term is more of the same sum: the wavefronts deal the distinct adapters of all rows
-// among themselves, and each multiplies its ones' 16 rows of B with T (hi and lo BF16 parts) into
-// its accumulators, before its codes have landed.
-template <int MT, int PD, bool WHOLE>
-__global__ __launch_bounds__(kStreamThreads, MT <= 3 ? 4 : 2) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
-  __shared__ uint4 smem[kStreamWaves * MT * 128];  // a block of X for each wavefront; then the sums
-  f32x4_t(*red)[MT][64] = reinterpret_cast<f32x4_t(*)[MT][64]>(smem);
+// The adapters' term is more of the same sum.  E == 0: T is there; the wavefronts deal the distinct
+// adapters of all rows among themselves, and each multiplies its ones' 16 rows of B with T (hi and
+// lo BF16 parts) into its accumulators.  E > 0 (a row or a few, up to E tiles of 16 ranks in all):
+// every workgroup forms T itself, A's rows passing beside X's as E more tiles, which costs less
+// than a launch before this one.
+template <int MT, int E, int PD, bool WHOLE>
+__global__ __launch_bounds__(kStreamThreads, MT + E <= 3 ? 4 : 2) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
+  static_assert(E == 0 || MT == 1, "T is formed for one tile of rows");
+  constexpr int XT = MT + E;  // tiles that pass through LDS
+  __shared__ uint4 smem[kStreamWaves * XT * 128];  // a block of them for each wavefront; then the sums
+  f32x4_t(*red)[XT][64] = reinterpret_cast<f32x4_t(*)[XT][64]>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int64_t K = a.K, N = a.N, row0 = (int64_t)blockIdx.x * kStreamRows;
-  const int M = (int)a.rows.M;
+  const int M = (int)a.rows.M, width = a.rows.width;
   const uint32_t nb = (uint32_t)(K / 64), ng = (nb + 3) / 4;
   const rsrc_t rx = make_rsrc(a.X, (int64_t)M * K * 2);
   const rsrc_t rc = make_rsrc(a.codes + row0 * (K / 2), kStreamRows * (K / 2));
@@ -316,13 +404,28 @@ __global__ __launch_bounds__(kStreamThreads, MT <= 3 ? 4 : 2) void k_adapter_str
   for (int t = 0; t < MT; ++t) id[t] = adapter_of(a.rows, 16 * t + l16);
   Codes cur = load(wave), next = load(wave + kStreamWaves);
   const float mu = a.mu[0];
-  f32x4_t acc[MT];
+  f32x4_t acc[XT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < XT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  uint4* xs = smem + wave * XT * 128;
+  uint4 xr[PD][XT][2];
+  const auto load_x = [&](uint4 (&x)[XT][2], uint32_t blk) {
+    // lane p takes chunk (p & 7) ^ (row / 2 % 8) of rows p >> 3 and 8 + (p >> 3) of a tile
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int m = 16 * t + 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((4 * i + (lane >> 4)) & 7);
+        x[t][i] = bload16(rx, (m < M && blk < nb) ? (uint32_t)((m * K + 64 * (int64_t)blk + 8 * chunk) * 2) : kOOB);
+      }
+  };
+#pragma unroll
+  for (int d = 0; d < PD; ++d) load_x(xr[d], 4 * wave + d);
 
-  // ---- this wavefront's adapters: every eighth distinct one, lane k holding the k-th
+  // E == 0: this wavefront's adapters, every eighth distinct one, lane k holding the k-th.  E > 0: lane
+  // m holds row m's, and tile MT + e is ranks 16 (e % ranks) .. of row e / ranks.
   int mine = 0, count = 0;
-  {
+  if (E == 0) {
     uint64_t pending[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) pending[t] = __ballot(id[t] >= 0);
@@ -341,17 +444,112 @@ __global__ __launch_bounds__(kStreamThreads, MT <= 3 ? 4 : 2) void k_adapter_str
           skip = kStreamWaves - 1;
         }
       }
+  } else {
+    mine = id[0] < 0 ? 0 : id[0];
+    count = M;
   }
+  uint64_t base_a = 0, base_b = 0;
+  int rank_l = 0;
+  float scale_l = 0.f;
   if (count) {
     const AdapterEntry* e = a.rows.table + mine;
-    const uint64_t base_l = reinterpret_cast<uint64_t>(e->B);
-    const int rank_l = e->r;
-    const float scale_l = e->s;
-    const int width = a.rows.width;
+    base_b = reinterpret_cast<uint64_t>(e->B);
+    rank_l = e->r;
+    scale_l = e->s;
+    if (E > 0) {
+      base_a = reinterpret_cast<uint64_t>(e->A);
+      if (id[0] < 0) rank_l = 0;  // no tile of its has a rank
+    }
+  }
+  const int ranks = (width + 15) / 16;
+  uint64_t tile_a[E ? E : 1];  // A of tile MT + e, and the ranks that it has from the tile's first on
+  int tile_r[E ? E : 1];
+  if (E > 0) {
+    int m = 0, jt = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      tile_a[e] = readlane64(base_a, m) + (uint64_t)(16 * jt) * (uint64_t)K * 2;
+      tile_r[e] = m < M ? __builtin_amdgcn_readlane(rank_l, m) - 16 * jt : 0;
+      if (++jt == ranks) jt = 0, ++m;
+    }
+  }
+  const auto load_a = [&](uint4 (&x)[XT][2], uint32_t blk) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int have = tile_r[e] < 0 ? 0 : tile_r[e];
+      const rsrc_t ra = make_rsrc(reinterpret_cast<const void*>(tile_a[e]), have * K * 2);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((4 * i + (lane >> 4)) & 7);
+        x[MT + e][i] = bload16(ra, (j < have && blk < nb) ? (uint32_t)((j * K + 64 * (int64_t)blk + 8 * chunk) * 2) : kOOB);
+      }
+    }
+  };
+  if (E > 0) {
+#pragma unroll
+    for (int d = 0; d < PD; ++d) load_a(xr[d], 4 * wave + d);
+  }
+  const bool drop = E > 0 && a.drop.threshold != 0;
+  RngKey key{};
+  if (drop) key = load_rng(a.drop.rng);
+  const uint32_t t2 = threshold_halves(a.drop.threshold);
+
+  // ---- the base product, and T beside it
+  for (uint32_t group = wave; group < ng; group += kStreamWaves) {
+    const Codes c = cur;
+    cur = next;
+    next = load(group + 2 * kStreamWaves);
+    Lut L;
+    build_scaled_lut(tab, block_scale(c.c8, __uint_as_float(c.c2), mu), L);
+    const uint32_t words[8] = {c.c0.x, c.c0.y, c.c0.z, c.c0.w, c.c1.x, c.c1.y, c.c1.z, c.c1.w};
+    uint32_t w[8][4];  // word i of this lane's block; then, of block i % 4, word 4 (i / 4) + g
+#pragma unroll
+    for (int i = 0; i < 8; ++i) decode8(words[i], L, w[i]);
+#pragma unroll
+    for (int h = 0; h < 8; h += 4)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        swap16(w[h][q], w[h + 1][q]);
+        swap16(w[h + 2][q], w[h + 3][q]);
+        swap32(w[h][q], w[h + 2][q]);
+        swap32(w[h + 1][q], w[h + 3][q]);
+      }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      // the wavefront's LDS accesses run in order
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int t = 0; t < XT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) xs[128 * t + 64 * i + lane] = xr[b % PD][t][i];
+      asm volatile("" ::: "memory");
+      const uint32_t ahead = 4 * (group + kStreamWaves * ((b + PD) / 4)) + (b + PD) % 4;
+      load_x(xr[b % PD], ahead);
+      if (E > 0) load_a(xr[b % PD], ahead);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = 8 * l16 + ((4 * h + g) ^ (l16 >> 1));
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          uint4 x = xs[128 * t + at];
+          acc[t] = mfma16x16x32(as_bf16x8(w[b + 4 * h]), as_bf16x8(x), acc[t]);
+          if (E > 0) {
+            if (drop) x = drop8(x, key, (uint64_t)l16 * (uint64_t)(K / 8) + (uint64_t)(8 * (4 * group + b) + 4 * h + g), t2);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[MT + e] = mfma16x16x32(as_bf16x8(xs[128 * (MT + e) + at]), as_bf16x8(x), acc[MT + e]);
+          }
+        }
+      }
+      asm volatile("" ::: "memory");
+    }
+  }
+
+  if (E == 0) {
+    // ---- this wavefront's adapters
     const rsrc_t rt = make_rsrc(a.T, (int64_t)M * width * 4);
     for (int k = 0; k < count; ++k) {
       const int one = __builtin_amdgcn_readlane(mine, k), r = __builtin_amdgcn_readlane(rank_l, k);
-      const uint16_t* B = reinterpret_cast<const uint16_t*>(readlane64(base_l, k));
+      const uint16_t* B = reinterpret_cast<const uint16_t*>(readlane64(base_b, k));
       const float s = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_l), k));
       const rsrc_t rb = make_rsrc(B + row0 * r, (int64_t)kStreamRows * r * 2);
       for (int r0 = 0; r0 < r; r0 += 32) {
@@ -377,76 +575,75 @@ __global__ __launch_bounds__(kStreamThreads, MT <= 3 ? 4 : 2) void k_adapter_str
       }
     }
   }
-
-  // ---- the base product
-  uint4* xs = smem + wave * MT * 128;
-  uint4 xr[PD][MT][2];
-  // block blk of X: lane p takes chunk (p & 7) ^ (row / 2 % 8) of rows p >> 3 and 8 + (p >> 3) of a tile
-  const auto load_x = [&](uint4 (&x)[MT][2], uint32_t blk) {
+  __syncthreads();  // the sums take the place of every wavefront's tiles
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int m = 16 * t + 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((4 * i + (lane >> 4)) & 7);
-        x[t][i] = bload16(rx, (m < M && blk < nb) ? (uint32_t)((m * K + 64 * (int64_t)blk + 8 * chunk) * 2) : kOOB);
-      }
-  };
-#pragma unroll
-  for (int d = 0; d < PD; ++d) load_x(xr[d], 4 * wave + d);
-  for (uint32_t group = wave; group < ng; group += kStreamWaves) {
-    const Codes c = cur;
-    cur = next;
-    next = load(group + 2 * kStreamWaves);
-    Lut L;
-    build_scaled_lut(tab, block_scale(c.c8, __uint_as_float(c.c2), mu), L);
-    const uint32_t words[8] = {c.c0.x, c.c0.y, c.c0.z, c.c0.w, c.c1.x, c.c1.y, c.c1.z, c.c1.w};
-    uint32_t w[8][4];  // word i of this lane's block; then, of block i % 4, word 4 (i / 4) + g
-#pragma unroll
-    for (int i = 0; i < 8; ++i) decode8(words[i], L, w[i]);
-#pragma unroll
-    for (int h = 0; h < 8; h += 4)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        swap16(w[h][q], w[h + 1][q]);
-        swap16(w[h + 2][q], w[h + 3][q]);
-        swap32(w[h][q], w[h + 2][q]);
-        swap32(w[h + 1][q], w[h + 3][q]);
-      }
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      // the wavefront's LDS accesses run in order
-      asm volatile("" ::: "memory");
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) xs[128 * t + 64 * i + lane] = xr[b % PD][t][i];
-      asm volatile("" ::: "memory");
-      load_x(xr[b % PD], 4 * (group + kStreamWaves * ((b + PD) / 4)) + (b + PD) % 4);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          acc[t] = mfma16x16x32(as_bf16x8(w[b + 4 * h]), as_bf16x8(xs[128 * t + 8 * l16 + ((4 * h + g) ^ (l16 >> 1))]), acc[t]);
-      asm volatile("" ::: "memory");
-    }
-  }
-  __syncthreads();  // the sums take the place of every wavefront's X
-#pragma unroll
-  for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
+  for (int t = 0; t < XT; ++t) red[wave][t][lane] = acc[t];
   __syncthreads();
   // the wavefronts' sums in order; lane l of tile t: row 16 t + (l & 15) of X, weight rows 4 (l >> 4) + v
-  for (int t = wave; t < MT; t += kStreamWaves) {
-    const int m = 16 * t + l16;
-    if (m >= M) continue;
+  const auto summed = [&](int t) {
     f32x4_t y = red[0][t][lane];
 #pragma unroll
     for (int w = 1; w < kStreamWaves; ++w) {
       const f32x4_t v = red[w][t][lane];
       y[0] += v[0]; y[1] += v[1]; y[2] += v[2]; y[3] += v[3];
     }
-    *reinterpret_cast<uint2*>(a.Y + (int64_t)m * N + row0 + 4 * g) =
-        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    return y;
+  };
+  if (E == 0) {
+    for (int t = wave; t < MT; t += kStreamWaves) {
+      const int m = 16 * t + l16;
+      if (m >= M) continue;
+      const f32x4_t y = summed(t);
+      *reinterpret_cast<uint2*>(a.Y + (int64_t)m * N + row0 + 4 * g) =
+          make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    }
+    return;
   }
+  if (wave != 0) return;
+  // ---- E > 0: T's tiles, each one column m of its sum, then their products with B's 16 rows
+  __shared__ float ts[E ? E * 16 : 1];  // [row][ranks * 16]
+  f32x4_t y = summed(0);
+  int m = 0, jt = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (m < M) {
+      f32x4_t t = summed(MT + e);
+      if (l16 == m) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) t[v] = 4 * g + v < tile_r[e] ? t[v] * a.drop.scale : 0.f;
+        *reinterpret_cast<f32x4_t*>(ts + 16 * e + 4 * g) = t;
+        if (a.T && blockIdx.x == 0 && 16 * jt + 4 * g < width)
+          *reinterpret_cast<f32x4_t*>(a.T + (int64_t)m * width + 16 * jt + 4 * g) = t;
+      }
+    }
+    if (++jt == ranks) jt = 0, ++m;
+  }
+  asm volatile("" ::: "memory");
+  for (int k = 0; k < M; ++k) {
+    const int r = __builtin_amdgcn_readlane(rank_l, k);
+    const uint16_t* B = reinterpret_cast<const uint16_t*>(readlane64(base_b, k));
+    const float s = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_l), k));
+    const rsrc_t rb = make_rsrc(B + row0 * r, (int64_t)kStreamRows * r * 2);
+    for (int r0 = 0; r0 < r; r0 += 32) {
+      const int at = r0 + 8 * g;
+      const uint4 w = WHOLE ? bload16(rb, at < r ? (uint32_t)((l16 * r + at) * 2) : kOOB)
+                            : load_row8(B, N * r, (row0 + l16) * r, at, r);
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (l16 == k && at < r) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = ts[16 * ranks * k + at + i] * s;
+      }
+      uint4 hi, lo;
+      split_bf16(v, hi, lo);
+      const f32x4_t p = mfma16x16x32(as_bf16x8(w), as_bf16x8(lo),
+                                     mfma16x16x32(as_bf16x8(w), as_bf16x8(hi), f32x4_t{0.f, 0.f, 0.f, 0.f}));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] += l16 == k ? p[i] : 0.f;
+    }
+  }
+  if (l16 < M)
+    *reinterpret_cast<uint2*>(a.Y + (int64_t)l16 * N + row0 + 4 * g) =
+        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
 }
 
 // ---------------------------------------------------------------- dA and dB
@@ -696,22 +893,45 @@ hipError_t launch_shrink_b(const AdapterRows& rows, const uint16_t* dY, int64_t 
                     : shrink_by_rank<true, false, false>(a, decode, tab, st);
 }
 
+// Tiles of 16 ranks in all up to which every workgroup of the stream forms T itself.
+constexpr int kSelfTiles = 4;
+constexpr int64_t kSelfBytes = int64_t(1) << 19;  // of A that each of them reads
+
+bool stream_forms_t(int64_t M, int64_t K, int32_t width) {
+  const int64_t tiles = M * ((width + 15) / 16);
+  return tiles <= kSelfTiles && tiles * 16 * K * 2 <= kSelfBytes;
+}
+
 hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, const float* c2s, const float* mu,
-                                 int64_t N, int64_t K, const uint16_t* X, const AdapterRows& rows, const float* T,
-                                 uint16_t* Y, const Nf4Tables& tab, hipStream_t st) {
+                                 int64_t N, int64_t K, const uint16_t* X, const AdapterRows& rows, const DropMask& drop,
+                                 float* T, uint16_t* Y, const Nf4Tables& tab, hipStream_t st) {
   if (rows.M > kStreamMaxRows) return hipErrorInvalidValue;
-  const StreamArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, rows, T, Y};
+  const int tiles = (int)((rows.M + kRowTile - 1) / kRowTile), ranks = (rows.width + 15) / 16;
+  const StreamArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, rows, drop, T, Y,
+                     std::min((int)rows.count, kRowTile)};
   const dim3 grid((unsigned)(N / kStreamRows));
   const auto go = [&](auto whole, auto not_whole) {
     if (rows.whole) hipLaunchKernelGGL(whole, grid, dim3(kStreamThreads), 0, st, a, tab);
     else hipLaunchKernelGGL(not_whole, grid, dim3(kStreamThreads), 0, st, a, tab);
   };
-  if (rows.M <= 16) go(k_adapter_stream<1, 4, true>, k_adapter_stream<1, 4, false>);
-  else if (rows.M <= 32) go(k_adapter_stream<2, 2, true>, k_adapter_stream<2, 2, false>);
-  else if (rows.M <= 48) go(k_adapter_stream<3, 1, true>, k_adapter_stream<3, 1, false>);
-  else if (rows.M <= 64) go(k_adapter_stream<4, 1, true>, k_adapter_stream<4, 1, false>);
-  else if (rows.M <= 96) go(k_adapter_stream<6, 1, true>, k_adapter_stream<6, 1, false>);
-  else go(k_adapter_stream<8, 1, true>, k_adapter_stream<8, 1, false>);
+  if (stream_forms_t(rows.M, K, rows.width)) {
+    const int64_t e = rows.M * ranks;
+    if (e <= 1) go(k_adapter_stream<1, 1, 2, true>, k_adapter_stream<1, 1, 2, false>);
+    else if (e <= 2) go(k_adapter_stream<1, 2, 1, true>, k_adapter_stream<1, 2, 1, false>);
+    else go(k_adapter_stream<1, 4, 1, true>, k_adapter_stream<1, 4, 1, false>);
+    return hipGetLastError();
+  }
+  const dim3 grid_t((unsigned)(tiles * ranks * a.lists));
+  if (drop.threshold) hipLaunchKernelGGL(k_adapter_t<true>, grid_t, dim3(kStreamThreads), 0, st, a);
+  else hipLaunchKernelGGL(k_adapter_t<false>, grid_t, dim3(kStreamThreads), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (rows.M <= 16) go(k_adapter_stream<1, 0, 4, true>, k_adapter_stream<1, 0, 4, false>);
+  else if (rows.M <= 32) go(k_adapter_stream<2, 0, 2, true>, k_adapter_stream<2, 0, 2, false>);
+  else if (rows.M <= 48) go(k_adapter_stream<3, 0, 1, true>, k_adapter_stream<3, 0, 1, false>);
+  else if (rows.M <= 64) go(k_adapter_stream<4, 0, 1, true>, k_adapter_stream<4, 0, 1, false>);
+  else if (rows.M <= 96) go(k_adapter_stream<6, 0, 1, true>, k_adapter_stream<6, 0, 1, false>);
+  else go(k_adapter_stream<8, 0, 1, true>, k_adapter_stream<8, 0, 1, false>);
   return hipGetLastError();
 }
 

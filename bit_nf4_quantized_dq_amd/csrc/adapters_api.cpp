@@ -76,9 +76,9 @@ Layout layout(bool bwd, int64_t M, const qlora_adapters_t* set, int dq) {
   const size_t t_bytes = sizeof(float) * (size_t)M * width;
   w.t = take(t_bytes);
   if (bwd) w.g = take(t_bytes);
-  const int32_t split = std::max(shrink_split(M, K), bwd ? shrink_split(M, N) : 1);
-  w.spart = take(split > 1 ? t_bytes * split : 0);
   if (bwd || !stream_path(M, dq)) {
+    const int32_t split = std::max(shrink_split(M, K), bwd ? shrink_split(M, N) : 1);
+    w.spart = take(split > 1 ? t_bytes * split : 0);
     w.wcopy = take(2 * (size_t)N * K);
     w.gsplit = bwd ? gemm_nt_ksplit(K, M, N) : gemm_nt_ksplit(N, M, K);
     w.gpart = take(w.gsplit > 1 ? sizeof(float) * (size_t)w.gsplit * M * (bwd ? K : N) : 0);
@@ -169,10 +169,9 @@ int qlora_adapters_fwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   float* part = reinterpret_cast<float*>(base + L.spart);
   unsigned int* counters = static_cast<unsigned int*>(ws);
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(Wq->codes);
-  if (stream_path(M, dq)) {
-    if (launch_shrink_a(rows, X, K, drop, T, part, counters, nullptr, tab, stream) != hipSuccess) return QLORA_ERR_HIP;
-    return hip_status(launch_adapter_stream(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, X, rows, T, Y, tab, stream));
-  }
+  if (stream_path(M, dq))
+    return hip_status(launch_adapter_stream(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, X, rows, drop,
+                                            stream_forms_t(M, K, rows.width) ? T_save : T, Y, tab, stream));
   uint16_t* wcopy = reinterpret_cast<uint16_t*>(base + L.wcopy);
   const ShrinkDecode dec = decode_args(Wq, wcopy);
   if (launch_shrink_a(rows, X, K, drop, T, part, counters, dq == QLORA_DQ_E4M3 ? &dec : nullptr, tab, stream) != hipSuccess)

@@ -79,7 +79,8 @@ def check_fwd(c, p=0.0, save=True, ws=None):
     return Y[:M], None if T is None else T[:M]
 
 
-def check_bwd(c, p=0.0, T=None, need_dx=True, ws=None):
+def check_bwd(c, p=0.0, T=None, need_dx=True, ws=None, T_of_oracle=False):
+    """T_of_oracle: T is the forward's, and the gradients are those of the oracle's own T."""
     import bit_nf4_quantized_dq_amd as Q
 
     M, K, N = c["X"].shape[0], c["q"].d_in, c["q"].d_out
@@ -87,7 +88,8 @@ def check_bwd(c, p=0.0, T=None, need_dx=True, ws=None):
     got = Q.linear_adapters_bwd(c["q"], c["set"], c["X"], c["dY"], c["ids"], dropout=p, rng=c["rng"] if p else None, T_saved=T,
                                 need_dx=need_dx, dX=dX[:M] if need_dx else None, ws=ws)
     torch.cuda.synchronize()
-    ref = AO.bwd(c["what"], c["A"], c["B"], c["alpha"], c["X"], c["dY"], c["ids"], p, RNG, T)
+    ref = AO.bwd(c["what"], c["A"], c["B"], c["alpha"], c["X"], c["dY"], c["ids"], p, RNG,
+                 None if T_of_oracle else T)
     r = c["set"].t_width
     assert (got is None) == (not need_dx) and (dX[M:] == 5).all()
     if need_dx:
@@ -141,11 +143,12 @@ def test_backward(gpu_lib, i, p):
     c = make(100 + i, *SHAPES[i])
     dX = check_bwd(c, p)
     dA, dB = [t.clone() for t in c["set"].dA], [t.clone() for t in c["set"].dB]
-    _, T = check_fwd(c, p)
-    again = check_bwd(c, p, T=T)  # T of the forward is what the backward recomputes
-    assert torch.equal(dX, again)
+    assert torch.equal(dX, check_bwd(c, p))
     assert all(map(torch.equal, dA, c["set"].dA)) and all(map(torch.equal, dB, c["set"].dB))
-    check_bwd(c, p, T=T, need_dx=False)
+    # with the forward's T (its sums may be taken in another order than the backward's own)
+    _, T = check_fwd(c, p)
+    assert torch.equal(dX, check_bwd(c, p, T=T)) and all(map(torch.equal, dA, c["set"].dA))
+    check_bwd(c, p, T=T, need_dx=False, T_of_oracle=True)
 
 
 @pytest.mark.parametrize("dq,codebook", [("none", "nf4"), ("int8", "nf4"), ("e5m2", "fp4"), ("e4m3", "int4"), ("e4m3", "fp4")])
