@@ -276,8 +276,9 @@ struct StreamArgs {
 // list 0 also writes the zeros of rows without an adapter.
 template <bool DROP>
 __global__ __launch_bounds__(kStreamThreads) void k_adapter_t(StreamArgs a) {
-  constexpr int D = 16;
-  __shared__ f32x4_t red[kStreamWaves * 64];
+  constexpr int D = 4;  // blocks of 64 columns in flight
+  __shared__ uint4 smem[kStreamWaves * 256];
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(smem);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int width = a.rows.width, ranks = (width + 15) / 16;
@@ -295,7 +296,8 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_t(StreamArgs a) {
   if (DROP) key = load_rng(a.drop.rng);
   const uint32_t t2 = threshold_halves(a.drop.threshold);
   const rsrc_t rp = make_rsrc(a.X + (int64_t)m0 * K, (a.rows.M - m0) * K * 2);
-  const int nslab = (int)(K / 32);
+  const int nb = (int)(K / 64);
+  uint4* xs = smem + wave * 256;  // this wavefront's tiles of X and A (as in the stream below)
   f32x4_t out = {0.f, 0.f, 0.f, 0.f};
   bool write = id < 0 && list == 0;
   uint64_t pending = __ballot(id >= 0);
@@ -312,24 +314,41 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_t(StreamArgs a) {
     write |= mine;
     if (16 * jt >= r) continue;
     const rsrc_t rq = make_rsrc(reinterpret_cast<const void*>(readlane64(base, from)), (int64_t)r * K * 2);
-    const int j = 16 * jt + l16;
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    for (int s0 = wave; s0 < nslab; s0 += kStreamWaves * D) {
-      uint4 pv[D], qv[D];
+    const uint64_t rows_mine = __ballot(mine);  // bit m: row m of the tile (in every group of 16 lanes)
+    uint4 x[D][2], q[D][2];
+    const auto load = [&](int d, int blk) {
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        const int slab = s0 + kStreamWaves * d;
-        const int64_t k = 32 * (int64_t)slab + 8 * g;
-        pv[d] = bload16(rp, (mine && slab < nslab) ? (uint32_t)((l16 * K + k) * 2) : kOOB);
-        qv[d] = bload16(rq, (j < r && slab < nslab) ? (uint32_t)((j * K + k) * 2) : kOOB);
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((4 * i + (lane >> 4)) & 7);
+        const uint32_t off = (uint32_t)(row * K + 64 * (int64_t)blk + 8 * chunk) * 2;
+        x[d][i] = bload16(rp, (blk < nb && ((rows_mine >> row) & 1)) ? off : kOOB);
+        q[d][i] = bload16(rq, (blk < nb && 16 * jt + row < r) ? off + (uint32_t)(32 * jt * K) : kOOB);
       }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d, wave + kStreamWaves * d);
+    for (int b0 = wave; b0 < nb; b0 += kStreamWaves * D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        uint4 p = pv[d];
-        if (DROP) p = drop8(p, key, (uint64_t)(m0 + l16) * (uint64_t)(K / 8) + (uint64_t)(4 * (s0 + kStreamWaves * d) + g), t2);
-        acc = mfma16x16x32(as_bf16x8(qv[d]), as_bf16x8(p), acc);
+        // blocks past the end are zeros; the wavefront's LDS accesses run in order
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 2; ++i) xs[64 * i + lane] = x[d][i], xs[128 + 64 * i + lane] = q[d][i];
+        asm volatile("" ::: "memory");
+        const int blk = b0 + kStreamWaves * d;
+        load(d, blk + kStreamWaves * D);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int at = 8 * l16 + ((4 * h + g) ^ (l16 >> 1));
+          uint4 p = xs[at];
+          if (DROP) p = drop8(p, key, (uint64_t)(m0 + l16) * (uint64_t)(K / 8) + (uint64_t)(8 * blk + 4 * h + g), t2);
+          acc = mfma16x16x32(as_bf16x8(xs[128 + at]), as_bf16x8(p), acc);
+        }
+        asm volatile("" ::: "memory");
       }
     }
+    __syncthreads();  // the sums take the place of the tiles
     // the wavefronts' sums in order; D[j][m]: ranks 4 g + v of row l16
     red[wave * 64 + lane] = acc;
     __syncthreads();
@@ -343,7 +362,7 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_t(StreamArgs a) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) out[v] = mine ? sum[v] : out[v];
     }
-    __syncthreads();
+    __syncthreads();  // before the next adapter's tiles
   }
   const int j = 16 * jt + 4 * g;
   if (wave != 0 || !write || m0 + l16 >= a.rows.M || j >= width) return;
@@ -368,7 +387,7 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_t(StreamArgs a) {
 // every workgroup forms T itself, A's rows passing beside X's as E more tiles, which costs less
 // than a launch before this one.
 template <int MT, int E, int PD, bool WHOLE>
-__global__ __launch_bounds__(kStreamThreads, MT + E <= 3 ? 4 : 2) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
+__global__ __launch_bounds__(kStreamThreads, E == 0 && MT <= 3 ? 4 : 2) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
   static_assert(E == 0 || MT == 1, "T is formed for one tile of rows");
   constexpr int XT = MT + E;  // tiles that pass through LDS
   __shared__ uint4 smem[kStreamWaves * XT * 128];  // a block of them for each wavefront; then the sums
@@ -894,7 +913,7 @@ hipError_t launch_shrink_b(const AdapterRows& rows, const uint16_t* dY, int64_t 
 }
 
 // Tiles of 16 ranks in all up to which every workgroup of the stream forms T itself.
-constexpr int kSelfTiles = 4;
+constexpr int kSelfTiles = 1;
 constexpr int64_t kSelfBytes = int64_t(1) << 19;  // of A that each of them reads
 
 bool stream_forms_t(int64_t M, int64_t K, int32_t width) {
@@ -916,9 +935,8 @@ hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, co
   };
   if (stream_forms_t(rows.M, K, rows.width)) {
     const int64_t e = rows.M * ranks;
-    if (e <= 1) go(k_adapter_stream<1, 1, 2, true>, k_adapter_stream<1, 1, 2, false>);
-    else if (e <= 2) go(k_adapter_stream<1, 2, 1, true>, k_adapter_stream<1, 2, 1, false>);
-    else go(k_adapter_stream<1, 4, 1, true>, k_adapter_stream<1, 4, 1, false>);
+    if (e <= 1) go(k_adapter_stream<1, 1, 4, true>, k_adapter_stream<1, 1, 4, false>);
+    else go(k_adapter_stream<1, 2, 2, true>, k_adapter_stream<1, 2, 2, false>);
     return hipGetLastError();
   }
   const dim3 grid_t((unsigned)(tiles * ranks * a.lists));
