@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["api.cpp", "codebook.cpp", "quantize.hip", "dequant.hip", "lora.hip", "gemv.hip",
     "gemv_stream.hip", "gemm.hip", "gemm_nt.hip", "merge.hip", "adamw.hip", "mlp.hip", "noalloc.hip", "gemv_rows.hip",
-    "train_api.cpp", "norm.hip", "preference.hip", "gradients.hip", "adapters_api.cpp", "adapters.hip", "dropout.hip"]
+    "train_api.cpp", "norm.hip", "preference.hip", "gradients.hip", "adapters_api.cpp", "adapters.hip", "adapters_gemm.hip", "dropout.hip"]
 
 COMMON = [
     "-O3",

@@ -58,6 +58,8 @@ AdapterRows rows_of(const qlora_adapters_t* set, const int32_t* ids, int64_t M) 
 // Few rows read the weight's codes as they are; more (and formats that only the decode kernels
 // read) go through the decoded copy.
 bool stream_path(int64_t M, int dq) { return M <= kStreamMaxRows && dq == QLORA_DQ_E4M3; }
+// The product over the codes, for the rows between few and many.
+bool codes_path(int64_t M, int64_t F, int dq) { return dq == QLORA_DQ_E4M3 && adapter_gemm_fits(M, F); }
 
 // ---- workspaces: the counter head, then T and G, then what the steps need in turn
 struct Layout {
@@ -79,9 +81,10 @@ Layout layout(bool bwd, int64_t M, const qlora_adapters_t* set, int dq) {
   if (bwd || !stream_path(M, dq)) {
     const int32_t split = std::max(shrink_split(M, K), bwd ? shrink_split(M, N) : 1);
     w.spart = take(split > 1 ? t_bytes * split : 0);
-    w.wcopy = take(2 * (size_t)N * K);
-    w.gsplit = bwd ? gemm_nt_ksplit(K, M, N) : gemm_nt_ksplit(N, M, K);
-    w.gpart = take(w.gsplit > 1 ? sizeof(float) * (size_t)w.gsplit * M * (bwd ? K : N) : 0);
+    const int64_t F = bwd ? K : N, Kr = bwd ? N : K;
+    if (!codes_path(M, F, dq)) w.wcopy = take(2 * (size_t)N * K);
+    w.gsplit = codes_path(M, F, dq) ? adapter_gemm_split(M, F, Kr) : gemm_nt_ksplit(F, M, Kr);
+    w.gpart = take(w.gsplit > 1 ? sizeof(float) * (size_t)w.gsplit * M * F : 0);
   }
   if (bwd) w.grads = take(adapter_grad_plan(M, N, K, set->count, set->max_rank).part_bytes);
   w.total = off;
@@ -172,6 +175,13 @@ int qlora_adapters_fwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   if (stream_path(M, dq))
     return hip_status(launch_adapter_stream(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, X, rows, drop,
                                             stream_forms_t(M, K, rows.width) ? T_save : T, Y, tab, stream));
+  const AdapterHead head{rows, T, 0, 1.f, DropMask{}};
+  float* gpart = reinterpret_cast<float*>(base + L.gpart);
+  if (codes_path(M, N, dq)) {
+    if (launch_shrink_a(rows, X, K, drop, T, part, counters, nullptr, tab, stream) != hipSuccess) return QLORA_ERR_HIP;
+    return hip_status(launch_adapter_gemm(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, X, M, head, Y, gpart, L.gsplit, tab,
+                                          QLORA_K_GEMM_FWD, stream));
+  }
   uint16_t* wcopy = reinterpret_cast<uint16_t*>(base + L.wcopy);
   const ShrinkDecode dec = decode_args(Wq, wcopy);
   if (launch_shrink_a(rows, X, K, drop, T, part, counters, dq == QLORA_DQ_E4M3 ? &dec : nullptr, tab, stream) != hipSuccess)
@@ -179,9 +189,7 @@ int qlora_adapters_fwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   if (dq != QLORA_DQ_E4M3 &&
       launch_dequant(codes, Wq->code8, Wq->c2s, Wq->mu, wcopy, N * K / 8, tab, dq, stream) != hipSuccess)
     return QLORA_ERR_HIP;
-  const AdapterHead head{rows, T, 0, 1.f, DropMask{}};
-  return hip_status(launch_gemm_nt_adapters(wcopy, N, X, M, K, head, Y, QLORA_K_GEMM_FWD, stream,
-                                            reinterpret_cast<float*>(base + L.gpart), L.gsplit));
+  return hip_status(launch_gemm_nt_adapters(wcopy, N, X, M, K, head, Y, QLORA_K_GEMM_FWD, stream, gpart, L.gsplit));
 }
 
 int qlora_adapters_bwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, const uint16_t* X, const uint16_t* dY,
@@ -209,18 +217,23 @@ int qlora_adapters_bwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
     if (launch_shrink_a(rows, X, K, drop, t, part, counters, nullptr, tab, stream) != hipSuccess) return QLORA_ERR_HIP;
     T = t;
   }
+  const uint32_t* codes = reinterpret_cast<const uint32_t*>(Wq->codes);
   uint16_t* wcopy = reinterpret_cast<uint16_t*>(base + L.wcopy);
+  const bool copied = dX && !codes_path(M, K, dq);
   const ShrinkDecode dec = decode_args(Wq, wcopy);
-  if (launch_shrink_b(rows, dY, N, G, part, counters, dX && dq == QLORA_DQ_E4M3 ? &dec : nullptr, tab, stream) != hipSuccess)
+  if (launch_shrink_b(rows, dY, N, G, part, counters, copied && dq == QLORA_DQ_E4M3 ? &dec : nullptr, tab, stream) != hipSuccess)
     return QLORA_ERR_HIP;
   if (dX) {
-    if (dq != QLORA_DQ_E4M3 && launch_dequant_t(reinterpret_cast<const uint32_t*>(Wq->codes), Wq->code8, Wq->c2s, Wq->mu, N,
-                                                K, wcopy, tab, dq, stream) != hipSuccess)
+    if (copied && dq != QLORA_DQ_E4M3 &&
+        launch_dequant_t(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, wcopy, tab, dq, stream) != hipSuccess)
       return QLORA_ERR_HIP;
     const AdapterHead head{rows, G, 1, drop.scale, drop};
-    if (launch_gemm_nt_adapters(wcopy, K, dY, M, N, head, dX, QLORA_K_GEMM_DX, stream,
-                                reinterpret_cast<float*>(base + L.gpart), L.gsplit) != hipSuccess)
-      return QLORA_ERR_HIP;
+    float* gpart = reinterpret_cast<float*>(base + L.gpart);
+    const hipError_t e =
+        copied ? launch_gemm_nt_adapters(wcopy, K, dY, M, N, head, dX, QLORA_K_GEMM_DX, stream, gpart, L.gsplit)
+               : launch_adapter_gemm(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, dY, M, head, dX, gpart, L.gsplit, tab,
+                                     QLORA_K_GEMM_DX, stream);
+    if (e != hipSuccess) return QLORA_ERR_HIP;
   }
   return hip_status(launch_adapter_grads(rows, X, K, dY, N, T, G, drop, reinterpret_cast<float*>(base + L.grads), counters,
                                          stream));

@@ -1,0 +1,329 @@
+// Products with the stored weight for tens to about two thousand rows, each row with its own
+// adapter: the weight is decoded tile by tile on chip (exactly w_hat), so no decoded copy is written
+// and read back.
+//
+//   forward : Y[m][n]  = sum_k w_hat[n][k] X[m][k]    + adapters     features n, reduction k
+//   dX      : dX[m][k] = sum_n w_hat[n][k] dY[m][n]   + adapters     features k, reduction n
+//
+// Tile: 128 features x 32 TJ 2 tokens per workgroup of four wavefronts (2 x 2, each 64 features x
+// 32 TJ tokens of MFMA 32x32x16), reduction step 64, two workgroups to a compute unit, so that one's
+// decode (vector units) meets the other's products (matrix units).  A step decodes 128 blocks of 64
+// weights, two threads to a block and its level table.  Few tiles split the reduction over several
+// workgroups (FP32 partials, added in order by launch_sum_parts).
+//
+// Pipeline, as in gemm.hip: step kb issues the activations' direct loads to LDS for step kb + 2
+// (ring of three) and the codes' loads for it (registers), multiplies step kb, decodes step kb + 1
+// into the other weight buffer, waits for the activations of step kb + 1 and passes one barrier.
+// Every buffer is a __shared__ array of its own, known at compile time in a loop unrolled six
+// times, so that the compiler waits only for the loads an access needs.
+//
+// LDS.  Activations and the forward's weight: rows of 128 bytes, 16-byte chunk c of row r at c ^
+// (r / 2 % 8).  The transposed weight: rows n of 128 features in 64-byte units, unit u at u ^ (n % 4),
+// read with transposing reads (8 consecutive n of one feature); the four rows of a read then meet
+// all banks.
+#include "adapter_head.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int BF = 128;   // features per workgroup
+constexpr int BK = 64;    // reduction step
+constexpr int TI = 2;     // 32-feature tiles per wavefront
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <int N> __device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+// Own LDS accesses done, then the workgroup barrier (also a compiler memory barrier).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  asm volatile("s_barrier" ::: "memory");
+}
+
+__shared__ uint4 s_w0[1024], s_w1[1024];              // decoded weights, 16 KB each
+__shared__ uint4 s_x0[1024], s_x1[1024], s_x2[1024];  // activations
+template <int I> __device__ __forceinline__ uint4* wbuf() { return I == 0 ? s_w0 : s_w1; }
+template <int I> __device__ __forceinline__ uint4* xbuf() { return I == 0 ? s_x0 : (I == 1 ? s_x1 : s_x2); }
+
+struct MidArgs {
+  const uint8_t *codes, *code8;
+  const float *c2s, *mu;
+  int64_t N, K;
+  const uint16_t* X;  // [M, Kr]
+  int64_t M, F, Kr;   // features and reduction: (N, K), or (K, N) for dX
+  AdapterHead head;
+  uint16_t* C;
+  float* part;
+  uint32_t kb_per;
+};
+
+// Activation ring: 64 TJ rows from m0.  Wavefront w fills rows 16 TJ w .. +16 TJ of a slot, eight rows
+// of 128 bytes a load; lane p writes slot chunk p & 7 and fetches the chunk that belongs there.
+template <int TJ>
+struct Ring {
+  static constexpr int kLoads = 2 * TJ;
+  rsrc_t r;
+  uint32_t base[kLoads], col[kLoads], Kr;
+  int wave;
+  __device__ __forceinline__ void init(const MidArgs& a, int64_t m0, int w, int lane) {
+    const int64_t rows = a.M - m0 < 64 * TJ ? a.M - m0 : 64 * TJ;
+    r = make_rsrc(a.X + m0 * a.Kr, rows * a.Kr * 2);
+    Kr = (uint32_t)a.Kr;
+    wave = w;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int row = 8 * (kLoads * w + j) + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+      col[j] = 8 * chunk;
+      base[j] = row < rows ? (uint32_t)(row * a.Kr * 2 + 16 * chunk) : kOOB;
+    }
+  }
+  template <int SLOT> __device__ __forceinline__ void issue(uint32_t kb) const {
+    const uint32_t k0 = kb * BK;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const uint32_t off = (base[j] != kOOB && k0 + col[j] < Kr) ? base[j] + 2 * k0 : kOOB;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(xbuf<SLOT>() + (kLoads * wave + j) * 64), 16, off, 0, 0, 0);
+    }
+  }
+};
+
+// The weight of a step: thread t decodes half a block, 32 weights.  Forward: row f0 + t / 2, block kb,
+// half t % 2.  dX: row 64 kb + t / 4, block f0 / 64 + (t / 2) % 2, half t % 2.
+template <bool WT>
+struct Decoder {
+  static constexpr int kLoads = 3;
+  struct Regs {
+    uint4 c;
+    uint32_t c8, c2;
+  };
+  const uint8_t* codes;
+  rsrc_t rc, r8, r2;
+  int64_t codes_bytes;
+  uint32_t row_bytes, nb, off, blk;
+  float mu;
+  int t;
+  __device__ __forceinline__ void init(const MidArgs& a, int64_t f0, int tid) {
+    t = tid;
+    nb = (uint32_t)(a.K / 64);
+    row_bytes = (uint32_t)(a.K / 2);
+    codes = a.codes;
+    codes_bytes = a.N * (a.K / 2);
+    r8 = make_rsrc(a.code8, a.N * nb);
+    r2 = make_rsrc(a.c2s, ((a.N * nb + 255) / 256) * 4);
+    mu = a.mu[0];
+    if (!WT) {
+      const uint32_t row = (uint32_t)f0 + (t >> 1);
+      rc = make_rsrc(codes + f0 * row_bytes, (a.N - f0) * row_bytes);
+      off = row < a.N ? (t >> 1) * row_bytes + 16 * (t & 1) : kOOB;
+      blk = row * nb;
+    } else {
+      const uint32_t b = (uint32_t)(f0 / 64) + ((t >> 1) & 1);
+      off = b < nb ? (t >> 2) * row_bytes + 32 * b + 16 * (t & 1) : kOOB;
+      blk = (t >> 2) * nb + b;
+    }
+  }
+  __device__ __forceinline__ void load(Regs& R, uint32_t kb) const {
+    if (!WT) {
+      const bool ok = off != kOOB && kb < nb;
+      R.c = bload16(rc, ok ? off + 32 * kb : kOOB);
+      R.c8 = bload1(r8, ok ? blk + kb : kOOB);
+      R.c2 = bload4(r2, ok ? ((blk + kb) >> 8) * 4 : kOOB);
+    } else {
+      // a descriptor from the step's first row on (uniform); rows past the weight read as zero
+      const int64_t step = (int64_t)kb * BK * row_bytes;
+      R.c = bload16(make_rsrc(codes + step, codes_bytes - step), off);
+      const uint32_t at = blk + kb * BK * nb;
+      R.c8 = bload1(r8, off != kOOB ? at : kOOB);
+      R.c2 = bload4(r2, off != kOOB ? (at >> 8) * 4 : kOOB);
+    }
+  }
+  __device__ __forceinline__ void store(uint4* __restrict__ w, const Regs& R, const Nf4Tables& tab) const {
+    Lut L;
+    build_scaled_lut(tab, block_scale(R.c8, __uint_as_float(R.c2), mu), L);
+    const uint32_t words[4] = {R.c.x, R.c.y, R.c.z, R.c.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[4];
+      decode8(words[c], L, o);
+      if (!WT) {
+        const int row = t >> 1, chunk = 4 * (t & 1) + c;
+        w[8 * row + (chunk ^ ((row >> 1) & 7))] = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+        const int n = t >> 2, unit = t & 3;  // features 32 unit + 8 c ..
+        w[16 * n + 4 * (unit ^ (n & 3)) + c] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+};
+
+// Operand of features 32 u .. 32 u + 31, reduction indices 16 ks + 8 (lane >> 5) .. +7 of a step.
+template <bool WT>
+__device__ __forceinline__ bf16x8_t w_operand(const uint4* __restrict__ w, int u, int ks, int lane) {
+  const int l32 = lane & 31, h32 = lane >> 5;
+  if (!WT) {
+    const int row = 32 * u + l32;
+    return as_bf16x8(w[8 * row + ((2 * ks + h32) ^ ((row >> 1) & 7))]);
+  }
+  const int j = lane & 15, n = 16 * ks + 8 * h32 + (j >> 2);
+  const char* p = reinterpret_cast<const char*>(w) + 256 * n + 64 * (u ^ (n & 3)) + 32 * ((lane >> 4) & 1) + 8 * (j & 3);
+  const lds_i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p));
+  const lds_i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p + 4 * 256));
+  bf16x8_t r;
+  r[0] = lo[0]; r[1] = lo[1]; r[2] = lo[2]; r[3] = lo[3];
+  r[4] = hi[0]; r[5] = hi[1]; r[6] = hi[2]; r[7] = hi[3];
+  return r;
+}
+
+template <bool WT, int TJ, int XS, int WB>
+__device__ __forceinline__ void mid_step(const Decoder<WT>& dec, const Ring<TJ>& ring, const Nf4Tables& tab, uint32_t kb,
+                                         uint32_t last, typename Decoder<WT>::Regs& cur, typename Decoder<WT>::Regs& nxt,
+                                         int wf, int wm, int lane, f32x16_t (&acc)[TI][TJ]) {
+  // loads past the range read zeros or the next split's step, into buffers that nothing reads
+  const uint32_t k2 = kb + 2 < last ? kb + 2 : last;
+  dec.load(nxt, k2);
+  ring.template issue<(XS + 2) % 3>(k2);
+  const int l32 = lane & 31, h32 = lane >> 5;
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    bf16x8_t a[TI], b[TJ];
+#pragma unroll
+    for (int i = 0; i < TI; ++i) a[i] = w_operand<WT>(wbuf<WB>(), wf / 32 + i, ks, lane);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int row = wm + 32 * j + l32;
+      b[j] = as_bf16x8(xbuf<XS>()[8 * row + ((2 * ks + h32) ^ ((row >> 1) & 7))]);
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] = mfma32(a[i], b[j], acc[i][j]);
+  }
+  __builtin_amdgcn_sched_barrier(0);  // the other workgroup's products run beside the decode
+  dec.store(wbuf<WB ^ 1>(), cur, tab);
+  wait_vm<Ring<TJ>::kLoads + Decoder<WT>::kLoads>();  // the activations of step kb + 1 have landed
+  lds_barrier();
+}
+
+template <bool WT, int TJ>
+__global__ __launch_bounds__(kThreads, 2) void k_adapter_gemm(MidArgs a, Nf4Tables tab) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wf = (wave & 1) * 64, wm = (wave >> 1) * 32 * TJ;
+  const int64_t f0 = (int64_t)blockIdx.x * BF, m0 = (int64_t)blockIdx.y * 64 * TJ;
+  const uint32_t nk = (uint32_t)((a.Kr + BK - 1) / BK);
+  const uint32_t kb0 = blockIdx.z * a.kb_per, kb1 = kb0 + a.kb_per < nk ? kb0 + a.kb_per : nk;
+  Ring<TJ> ring;
+  ring.init(a, m0, wave, lane);
+  Decoder<WT> dec;
+  dec.init(a, f0, tid);
+  typename Decoder<WT>::Regs r0, r1;
+  // past the last step the offsets may not wrap: the step after the product reads zeros
+  ring.template issue<0>(kb0);
+  dec.load(r0, kb0);
+  ring.template issue<1>(kb0 + 1 < nk ? kb0 + 1 : nk);
+  dec.load(r1, kb0 + 1 < nk ? kb0 + 1 : nk);
+  f32x16_t acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x16_t{};
+  // (s_w1 is free until the barrier)
+  const bool any = adapter_rows<WT>(a.head, a.F, f0 + wf, m0 + wm, lane, reinterpret_cast<char*>(s_w1) + wave * 4096,
+                                    blockIdx.z, gridDim.z, acc);
+  if (WT && any && a.head.drop.threshold) drop_acc(a.head.drop, a.F, f0 + wf, m0 + wm, lane & 31, lane >> 5, acc);
+  dec.store(s_w0, r0, tab);
+  wait_vm<0>();
+  lds_barrier();
+  for (uint32_t kb = kb0; kb < kb1; kb += 6) {
+    mid_step<WT, TJ, 0, 0>(dec, ring, tab, kb + 0, nk, r1, r0, wf, wm, lane, acc);
+    if (kb + 1 >= kb1) break;
+    mid_step<WT, TJ, 1, 1>(dec, ring, tab, kb + 1, nk, r0, r1, wf, wm, lane, acc);
+    if (kb + 2 >= kb1) break;
+    mid_step<WT, TJ, 2, 0>(dec, ring, tab, kb + 2, nk, r1, r0, wf, wm, lane, acc);
+    if (kb + 3 >= kb1) break;
+    mid_step<WT, TJ, 0, 1>(dec, ring, tab, kb + 3, nk, r0, r1, wf, wm, lane, acc);
+    if (kb + 4 >= kb1) break;
+    mid_step<WT, TJ, 1, 0>(dec, ring, tab, kb + 4, nk, r1, r0, wf, wm, lane, acc);
+    if (kb + 5 >= kb1) break;
+    mid_step<WT, TJ, 2, 1>(dec, ring, tab, kb + 5, nk, r0, r1, wf, wm, lane, acc);
+  }
+  wait_vm<0>();   // the loads issued past the range have landed
+  lds_barrier();  // every wavefront is done with the buffers, which now stage the result
+  // 32 tokens x 64 features of FP32 at a time (8 KB of the wavefront's own): 16-byte unit u of row m at
+  // u ^ (m % 16); read back so that each row leaves in whole
+  uint4* stage = wave == 0 ? s_w0 : (wave == 1 ? s_w1 : (wave == 2 ? s_x0 : s_x1));
+  const int l32 = lane & 31, h32 = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int u = 8 * i + 2 * q + h32;
+        stage[16 * l32 + (u ^ (l32 & 15))] = make_uint4(__float_as_uint(acc[i][j][4 * q]), __float_as_uint(acc[i][j][4 * q + 1]),
+                                                        __float_as_uint(acc[i][j][4 * q + 2]), __float_as_uint(acc[i][j][4 * q + 3]));
+      }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // its own writes are done (it reads only its own region)
+    asm volatile("" ::: "memory");
+    if (a.part) {
+      float* part = a.part + (int64_t)blockIdx.z * a.M * a.F;
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const int m = 4 * it + (lane >> 4), c = lane & 15;
+        const uint4 v = stage[16 * m + (c ^ (m & 15))];
+        const int64_t gm = m0 + wm + 32 * j + m, gf = f0 + wf + 4 * c;
+        if (gm < a.M && gf < a.F) *reinterpret_cast<uint4*>(part + gm * a.F + gf) = v;
+      }
+    } else {
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int m = 8 * it + (lane >> 3), c = lane & 7;
+        const uint4 v = stage[16 * m + ((2 * c) ^ (m & 15))], w = stage[16 * m + ((2 * c + 1) ^ (m & 15))];
+        const int64_t gm = m0 + wm + 32 * j + m, gf = f0 + wf + 8 * c;
+        if (gm < a.M && gf < a.F)
+          *reinterpret_cast<uint4*>(a.C + gm * a.F + gf) =
+              make_uint4(pack_bf16x2(__uint_as_float(v.x), __uint_as_float(v.y)), pack_bf16x2(__uint_as_float(v.z), __uint_as_float(v.w)),
+                         pack_bf16x2(__uint_as_float(w.x), __uint_as_float(w.y)), pack_bf16x2(__uint_as_float(w.z), __uint_as_float(w.w)));
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // reads done before the next rows
+    asm volatile("" ::: "memory");
+  }
+}
+
+int64_t mid_tiles(int64_t M, int64_t F) { return ((F + BF - 1) / BF) * ((M + 127) / 128); }
+
+}  // namespace
+
+bool adapter_gemm_fits(int64_t M, int64_t F) { return mid_tiles(M, F) <= 512; }
+
+int32_t adapter_gemm_split(int64_t M, int64_t F, int64_t Kr) {
+  const int64_t nk = (Kr + BK - 1) / BK;
+  const int64_t split = std::min<int64_t>(512 / mid_tiles(M, F), nk / 4);
+  return (int32_t)std::max<int64_t>(1, split);
+}
+
+hipError_t launch_adapter_gemm(const uint32_t* codes, const uint8_t* code8, const float* c2s, const float* mu, int64_t N,
+                               int64_t K, const uint16_t* X, int64_t M, const AdapterHead& head, uint16_t* C, float* part,
+                               int32_t split, const Nf4Tables& tab, int kernel_id, hipStream_t st) {
+  const int64_t F = head.transposed ? K : N, Kr = head.transposed ? N : K;
+  if (split > 1 && !part) return hipErrorInvalidValue;
+  const uint32_t nk = (uint32_t)((Kr + BK - 1) / BK), kb_per = (nk + split - 1) / split;
+  const uint32_t splits = (nk + kb_per - 1) / kb_per;  // no split is empty
+  const MidArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, M, F, Kr, head, C, splits > 1 ? part : nullptr, kb_per};
+  const int rows = head.transposed && M <= 64 ? 64 : 128;
+  const dim3 grid((unsigned)((F + BF - 1) / BF), (unsigned)((M + rows - 1) / rows), splits);
+  {
+    LaunchTimer t(kernel_id, st);
+    const auto go = [&](auto kernel) { hipExtLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, t.start, t.stop, 0, a, tab); };
+    if (!head.transposed) go(k_adapter_gemm<false, 2>);
+    else if (M <= 64) go(k_adapter_gemm<true, 1>);
+    else go(k_adapter_gemm<true, 2>);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits <= 1) return e;
+  return launch_sum_parts(part, (int32_t)splits, M, F, C, st);
+}
+
+}  // namespace qlora

@@ -43,8 +43,7 @@ constexpr int BK = 32;                // reduction step
 constexpr int kChunks = BK / 8;       // 16-byte chunks per LDS row
 constexpr int kSlot = 256 * kChunks;  // 16-byte chunks per ring slot (16 KB)
 constexpr int TI = 4, TJ = 2;         // 32x32 MFMA tiles per wavefront
-static_assert(TI == kHeadTI && TJ == kHeadTJ, "adapter_head.h starts these accumulators");
-typedef HeadAcc Acc;
+typedef f32x16_t Acc[TI][TJ];
 typedef __attribute__((address_space(3))) void lds_void;
 
 // Two rings of five 16 KB slots (160 KB, all of a CU's LDS).
@@ -508,14 +507,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_nt_rows(const uint16_t* __
 
 }  // namespace
 
-namespace {
-hipError_t sum_parts(const float* part, int32_t ksplit, int64_t M, int64_t F, uint16_t* C, hipStream_t st) {
+hipError_t launch_sum_parts(const float* part, int32_t ksplit, int64_t M, int64_t F, uint16_t* C, hipStream_t st) {
   const int64_t n8 = M * F / 8;
   const int64_t blocks = std::min<int64_t>((n8 + 255) / 256, 2048);
   hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)blocks), dim3(256), 0, st, part, ksplit, M, F, C);
   return hipGetLastError();
 }
-}  // namespace
 
 int32_t gemm_nt_ksplit(int64_t F, int64_t M, int64_t Kr) {
   const int64_t tiles = ((F + BF - 1) / BF) * ((M + BMT - 1) / BMT);
@@ -547,7 +544,7 @@ hipError_t launch_gemm_nt(const uint16_t* A, int64_t F, const uint16_t* B, int64
 #undef GEMM_ARGS
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || ksplit <= 1) return e;
-  return sum_parts(part, ksplit, M, F, C, st);
+  return launch_sum_parts(part, ksplit, M, F, C, st);
 }
 
 hipError_t launch_gemm_nt_adapters(const uint16_t* A, int64_t F, const uint16_t* B, int64_t M, int64_t Kr,
@@ -571,7 +568,7 @@ hipError_t launch_gemm_nt_adapters(const uint16_t* A, int64_t F, const uint16_t*
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || ksplit <= 1) return e;
-  return sum_parts(part, ksplit, M, F, C, st);
+  return launch_sum_parts(part, ksplit, M, F, C, st);
 }
 
 }  // namespace qlora

@@ -196,6 +196,8 @@ int32_t gemm_nt_ksplit(int64_t F, int64_t M, int64_t Kr);
 hipError_t launch_gemm_nt(const uint16_t* A, int64_t F, const uint16_t* B, int64_t M, int64_t Kr,
                           const uint16_t* wl, int64_t wl_fs, int64_t wl_js, const uint16_t* L, int32_t r,
                           uint16_t* C, int kernel_id, hipStream_t st, float* part = nullptr, int32_t ksplit = 1);
+// C [M, F] BF16 = the sum of ksplit FP32 partials [M, F], in order; F % 16 == 0.
+hipError_t launch_sum_parts(const float* part, int32_t ksplit, int64_t M, int64_t F, uint16_t* C, hipStream_t st);
 
 // ---- element-wise steps of the MLP block (mlp.hip); n values, n % 8 == 0, 16-byte aligned
 hipError_t launch_swiglu_fwd(const uint16_t* G, const uint16_t* U, uint16_t* H, int64_t n, hipStream_t st);
