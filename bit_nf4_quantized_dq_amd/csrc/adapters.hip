@@ -519,7 +519,7 @@ __global__ __launch_bounds__(kStreamThreads, E == 0 && MT <= 3 ? 4 : 2) void k_a
     cur = next;
     next = load(group + 2 * kStreamWaves);
     Lut L;
-    build_scaled_lut(tab, block_scale(c.c8, __uint_as_float(c.c2), mu), L);
+    build_scaled_lut(tab, stored_scale(c.c8, __uint_as_float(c.c2), mu), L);
     const uint32_t words[8] = {c.c0.x, c.c0.y, c.c0.z, c.c0.w, c.c1.x, c.c1.y, c.c1.z, c.c1.w};
     uint32_t w[8][4];  // word i of this lane's block; then, of block i % 4, word 4 (i / 4) + g
 #pragma unroll

@@ -70,6 +70,12 @@ __device__ __forceinline__ void split_bf16(const float f[8], uint4& hi, uint4& l
 }
 
 // ---- operands
+// block_scale() by the chip's own conversion of OCP E4M3 (exact, and no branch): stored codes hold no
+// NaN.
+__device__ __forceinline__ float stored_scale(uint32_t code8, float c2s, float mu) {
+  return __fadd_rn(__fmul_rn(__builtin_amdgcn_cvt_f32_fp8((int)code8, 0), c2s), mu);
+}
+
 typedef short lds_i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) lds_i16x4 lds_i16x4_t;
 

@@ -5,8 +5,8 @@
 //   forward : Y[m][n]  = sum_k w_hat[n][k] X[m][k]    + adapters     features n, reduction k
 //   dX      : dX[m][k] = sum_n w_hat[n][k] dY[m][n]   + adapters     features k, reduction n
 //
-// Tile: 128 features x 32 TJ 2 tokens per workgroup of four wavefronts (2 x 2, each 64 features x
-// 32 TJ tokens of MFMA 32x32x16), reduction step 64, two workgroups to a compute unit, so that one's
+// Tile: 128 features x 128 tokens per workgroup of four wavefronts (2 x 2, each 64 features x 64
+// tokens of MFMA 32x32x16), reduction step 64, two workgroups to a compute unit, so that one's
 // decode (vector units) meets the other's products (matrix units).  A step decodes 128 blocks of 64
 // weights, two threads to a block and its level table.  Few tiles split the reduction over several
 // workgroups (FP32 partials, added in order by launch_sum_parts).
@@ -29,8 +29,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int BF = 128;   // features per workgroup
 constexpr int BK = 64;    // reduction step
-constexpr int TI = 2;     // 32-feature tiles per wavefront
+constexpr int BM = 128;   // tokens per workgroup
+constexpr int TI = 2, TJ = 2;  // 32 x 32 tiles per wavefront
 typedef __attribute__((address_space(3))) void lds_void;
+
+// An offset past every operand (tiles are below 2^31 bytes, the scalar offsets of steps below 2^24):
+// reads zeros however a step's offset adds to it.
+constexpr uint32_t kFar = 0xF0000000u;
 
 template <int N> __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
@@ -59,16 +64,15 @@ struct MidArgs {
   uint32_t kb_per;
 };
 
-// Activation ring: 64 TJ rows from m0.  Wavefront w fills rows 16 TJ w .. +16 TJ of a slot, eight rows
+// Activation ring: 128 rows from m0.  Wavefront w fills rows 32 w .. +32 of a slot, eight rows
 // of 128 bytes a load; lane p writes slot chunk p & 7 and fetches the chunk that belongs there.
-template <int TJ>
 struct Ring {
   static constexpr int kLoads = 2 * TJ;
   rsrc_t r;
   uint32_t base[kLoads], col[kLoads], Kr;
   int wave;
   __device__ __forceinline__ void init(const MidArgs& a, int64_t m0, int w, int lane) {
-    const int64_t rows = a.M - m0 < 64 * TJ ? a.M - m0 : 64 * TJ;
+    const int64_t rows = a.M - m0 < BM ? a.M - m0 : BM;
     r = make_rsrc(a.X + m0 * a.Kr, rows * a.Kr * 2);
     Kr = (uint32_t)a.Kr;
     wave = w;
@@ -76,15 +80,16 @@ struct Ring {
     for (int j = 0; j < kLoads; ++j) {
       const int row = 8 * (kLoads * w + j) + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
       col[j] = 8 * chunk;
-      base[j] = row < rows ? (uint32_t)(row * a.Kr * 2 + 16 * chunk) : kOOB;
+      base[j] = row < rows ? (uint32_t)(row * a.Kr * 2 + 16 * chunk) : kFar;
     }
   }
   template <int SLOT> __device__ __forceinline__ void issue(uint32_t kb) const {
     const uint32_t k0 = kb * BK;
+    const bool whole = k0 + BK <= Kr;  // uniform: else the step is the product's last, or past it
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const uint32_t off = (base[j] != kOOB && k0 + col[j] < Kr) ? base[j] + 2 * k0 : kOOB;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(xbuf<SLOT>() + (kLoads * wave + j) * 64), 16, off, 0, 0, 0);
+      const uint32_t off = whole || k0 + col[j] < Kr ? base[j] : kFar;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(xbuf<SLOT>() + (kLoads * wave + j) * 64), 16, off, 2 * k0, 0, 0);
     }
   }
 };
@@ -101,7 +106,7 @@ struct Decoder {
   const uint8_t* codes;
   rsrc_t rc, r8, r2;
   int64_t codes_bytes;
-  uint32_t row_bytes, nb, off, blk;
+  uint32_t row_bytes, nb, off, blk, to, chunk[4];
   float mu;
   int t;
   __device__ __forceinline__ void init(const MidArgs& a, int64_t f0, int tid) {
@@ -116,45 +121,51 @@ struct Decoder {
     if (!WT) {
       const uint32_t row = (uint32_t)f0 + (t >> 1);
       rc = make_rsrc(codes + f0 * row_bytes, (a.N - f0) * row_bytes);
-      off = row < a.N ? (t >> 1) * row_bytes + 16 * (t & 1) : kOOB;
-      blk = row * nb;
+      off = row < a.N ? (t >> 1) * row_bytes + 16 * (t & 1) : kFar;
+      blk = row < a.N ? row * nb : 0;
+      const int s = ((t >> 2) & 7) ^ (4 * (t & 1));
+      to = 8 * (t >> 1);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) chunk[c] = to + (s ^ c);
     } else {
       const uint32_t b = (uint32_t)(f0 / 64) + ((t >> 1) & 1);
-      off = b < nb ? (t >> 2) * row_bytes + 32 * b + 16 * (t & 1) : kOOB;
-      blk = (t >> 2) * nb + b;
+      off = b < nb ? (t >> 2) * row_bytes + 32 * b + 16 * (t & 1) : kFar;
+      blk = (t >> 2) * nb + (b < nb ? b : 0);
+      to = 16 * (t >> 2) + 4 * ((t & 3) ^ ((t >> 2) & 3));  // features 32 (t & 3) ..
+#pragma unroll
+      for (int c = 0; c < 4; ++c) chunk[c] = to + c;
     }
   }
+  // Steps past the product load its last one again (into registers that nothing uses); rows past the
+  // weight read as zero codes, whose products meet rows of the activations that are zero.
   __device__ __forceinline__ void load(Regs& R, uint32_t kb) const {
     if (!WT) {
-      const bool ok = off != kOOB && kb < nb;
-      R.c = bload16(rc, ok ? off + 32 * kb : kOOB);
-      R.c8 = bload1(r8, ok ? blk + kb : kOOB);
-      R.c2 = bload4(r2, ok ? ((blk + kb) >> 8) * 4 : kOOB);
+      const uint32_t k = kb < nb ? kb : nb - 1;
+      R.c = load16(rc, off, 32 * k);
+      const uint32_t at = blk + k;
+      R.c8 = bload1(r8, at);
+      R.c2 = bload4(r2, (at >> 8) * 4);
     } else {
-      // a descriptor from the step's first row on (uniform); rows past the weight read as zero
       const int64_t step = (int64_t)kb * BK * row_bytes;
-      R.c = bload16(make_rsrc(codes + step, codes_bytes - step), off);
+      R.c = load16(make_rsrc(codes + step, codes_bytes - step), off, 0);
       const uint32_t at = blk + kb * BK * nb;
-      R.c8 = bload1(r8, off != kOOB ? at : kOOB);
-      R.c2 = bload4(r2, off != kOOB ? (at >> 8) * 4 : kOOB);
+      R.c8 = bload1(r8, at);
+      R.c2 = bload4(r2, (at >> 8) * 4);
     }
   }
-  __device__ __forceinline__ void store(uint4* __restrict__ w, const Regs& R, const Nf4Tables& tab) const {
-    Lut L;
-    build_scaled_lut(tab, block_scale(R.c8, __uint_as_float(R.c2), mu), L);
+  static __device__ __forceinline__ uint4 load16(rsrc_t r, uint32_t off, uint32_t scalar) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, (int)scalar, 0);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  // The level table of the thread's block, then its words one by one.
+  __device__ __forceinline__ void table(const Regs& R, const Nf4Tables& tab, Lut& L) const {
+    build_scaled_lut(tab, stored_scale(R.c8, __uint_as_float(R.c2), mu), L);
+  }
+  __device__ __forceinline__ void store(uint4* __restrict__ w, const Regs& R, const Lut& L, int c) const {
     const uint32_t words[4] = {R.c.x, R.c.y, R.c.z, R.c.w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[4];
-      decode8(words[c], L, o);
-      if (!WT) {
-        const int row = t >> 1, chunk = 4 * (t & 1) + c;
-        w[8 * row + (chunk ^ ((row >> 1) & 7))] = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        const int n = t >> 2, unit = t & 3;  // features 32 unit + 8 c ..
-        w[16 * n + 4 * (unit ^ (n & 3)) + c] = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-    }
+    uint32_t o[4];
+    decode8(words[c], L, o);
+    w[chunk[c]] = make_uint4(o[0], o[1], o[2], o[3]);
   }
 };
 
@@ -176,49 +187,66 @@ __device__ __forceinline__ bf16x8_t w_operand(const uint4* __restrict__ w, int u
   return r;
 }
 
-template <bool WT, int TJ, int XS, int WB>
-__device__ __forceinline__ void mid_step(const Decoder<WT>& dec, const Ring<TJ>& ring, const Nf4Tables& tab, uint32_t kb,
+template <bool WT, int XS, int WB>
+__device__ __forceinline__ void mid_step(const Decoder<WT>& dec, const Ring& ring, const Nf4Tables& tab, uint32_t kb,
                                          uint32_t last, typename Decoder<WT>::Regs& cur, typename Decoder<WT>::Regs& nxt,
                                          int wf, int wm, int lane, f32x16_t (&acc)[TI][TJ]) {
-  // loads past the range read zeros or the next split's step, into buffers that nothing reads
+  // loads past the range go into buffers that nothing reads
   const uint32_t k2 = kb + 2 < last ? kb + 2 : last;
   dec.load(nxt, k2);
   ring.template issue<(XS + 2) % 3>(k2);
   const int l32 = lane & 31, h32 = lane >> 5;
+  Lut L;
+  dec.table(cur, tab, L);
+  bf16x8_t x[2][TI], y[2][TJ];
+  const auto read = [&](int ks) {
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    bf16x8_t a[TI], b[TJ];
-#pragma unroll
-    for (int i = 0; i < TI; ++i) a[i] = w_operand<WT>(wbuf<WB>(), wf / 32 + i, ks, lane);
+    for (int i = 0; i < TI; ++i) x[ks & 1][i] = w_operand<WT>(wbuf<WB>(), wf / 32 + i, ks, lane);
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const int row = wm + 32 * j + l32;
-      b[j] = as_bf16x8(xbuf<XS>()[8 * row + ((2 * ks + h32) ^ ((row >> 1) & 7))]);
+      y[ks & 1][j] = as_bf16x8(xbuf<XS>()[8 * row + ((2 * ks + h32) ^ ((row >> 1) & 7))]);
     }
+  };
+  read(0);
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    if (ks < 3) read(ks + 1);
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) acc[i][j] = mfma32(a[i], b[j], acc[i][j]);
+      for (int j = 0; j < TJ; ++j) acc[i][j] = mfma32(x[ks & 1][i], y[ks & 1][j], acc[i][j]);
+    dec.store(wbuf<WB ^ 1>(), cur, L, ks);
   }
-  __builtin_amdgcn_sched_barrier(0);  // the other workgroup's products run beside the decode
-  dec.store(wbuf<WB ^ 1>(), cur, tab);
-  wait_vm<Ring<TJ>::kLoads + Decoder<WT>::kLoads>();  // the activations of step kb + 1 have landed
+  // operands one 16-wide step ahead; the decode's vector instructions between the products, each of
+  // which holds the matrix unit for 32 clocks
+  constexpr int kReads = WT ? 2 * TI + TJ : TI + TJ;
+  __builtin_amdgcn_sched_group_barrier(0x100, 2 * kReads, 0);
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+#pragma unroll
+    for (int q = 0; q < TI * TJ; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 40 / (TI * TJ), 0);
+    }
+    if (ks < 2) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+  }
+  wait_vm<Ring::kLoads + Decoder<WT>::kLoads>();  // the activations of step kb + 1 have landed
   lds_barrier();
 }
 
-template <bool WT, int TJ>
+template <bool WT>
 __global__ __launch_bounds__(kThreads, 2) void k_adapter_gemm(MidArgs a, Nf4Tables tab) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wf = (wave & 1) * 64, wm = (wave >> 1) * 32 * TJ;
-  const int64_t f0 = (int64_t)blockIdx.x * BF, m0 = (int64_t)blockIdx.y * 64 * TJ;
+  const int64_t f0 = (int64_t)blockIdx.x * BF, m0 = (int64_t)blockIdx.y * BM;
   const uint32_t nk = (uint32_t)((a.Kr + BK - 1) / BK);
   const uint32_t kb0 = blockIdx.z * a.kb_per, kb1 = kb0 + a.kb_per < nk ? kb0 + a.kb_per : nk;
-  Ring<TJ> ring;
+  Ring ring;
   ring.init(a, m0, wave, lane);
   Decoder<WT> dec;
   dec.init(a, f0, tid);
   typename Decoder<WT>::Regs r0, r1;
-  // past the last step the offsets may not wrap: the step after the product reads zeros
   ring.template issue<0>(kb0);
   dec.load(r0, kb0);
   ring.template issue<1>(kb0 + 1 < nk ? kb0 + 1 : nk);
@@ -232,21 +260,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_adapter_gemm(MidArgs a, Nf4Tabl
   const bool any = adapter_rows<WT>(a.head, a.F, f0 + wf, m0 + wm, lane, reinterpret_cast<char*>(s_w1) + wave * 4096,
                                     blockIdx.z, gridDim.z, acc);
   if (WT && any && a.head.drop.threshold) drop_acc(a.head.drop, a.F, f0 + wf, m0 + wm, lane & 31, lane >> 5, acc);
-  dec.store(s_w0, r0, tab);
+  {
+    Lut L;
+    dec.table(r0, tab, L);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) dec.store(s_w0, r0, L, c);
+  }
   wait_vm<0>();
   lds_barrier();
   for (uint32_t kb = kb0; kb < kb1; kb += 6) {
-    mid_step<WT, TJ, 0, 0>(dec, ring, tab, kb + 0, nk, r1, r0, wf, wm, lane, acc);
+    mid_step<WT, 0, 0>(dec, ring, tab, kb + 0, nk, r1, r0, wf, wm, lane, acc);
     if (kb + 1 >= kb1) break;
-    mid_step<WT, TJ, 1, 1>(dec, ring, tab, kb + 1, nk, r0, r1, wf, wm, lane, acc);
+    mid_step<WT, 1, 1>(dec, ring, tab, kb + 1, nk, r0, r1, wf, wm, lane, acc);
     if (kb + 2 >= kb1) break;
-    mid_step<WT, TJ, 2, 0>(dec, ring, tab, kb + 2, nk, r1, r0, wf, wm, lane, acc);
+    mid_step<WT, 2, 0>(dec, ring, tab, kb + 2, nk, r1, r0, wf, wm, lane, acc);
     if (kb + 3 >= kb1) break;
-    mid_step<WT, TJ, 0, 1>(dec, ring, tab, kb + 3, nk, r0, r1, wf, wm, lane, acc);
+    mid_step<WT, 0, 1>(dec, ring, tab, kb + 3, nk, r0, r1, wf, wm, lane, acc);
     if (kb + 4 >= kb1) break;
-    mid_step<WT, TJ, 1, 0>(dec, ring, tab, kb + 4, nk, r1, r0, wf, wm, lane, acc);
+    mid_step<WT, 1, 0>(dec, ring, tab, kb + 4, nk, r1, r0, wf, wm, lane, acc);
     if (kb + 5 >= kb1) break;
-    mid_step<WT, TJ, 2, 1>(dec, ring, tab, kb + 5, nk, r0, r1, wf, wm, lane, acc);
+    mid_step<WT, 2, 1>(dec, ring, tab, kb + 5, nk, r0, r1, wf, wm, lane, acc);
   }
   wait_vm<0>();   // the loads issued past the range have landed
   lds_barrier();  // every wavefront is done with the buffers, which now stage the result
@@ -292,7 +325,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_adapter_gemm(MidArgs a, Nf4Tabl
   }
 }
 
-int64_t mid_tiles(int64_t M, int64_t F) { return ((F + BF - 1) / BF) * ((M + 127) / 128); }
+int64_t mid_tiles(int64_t M, int64_t F) { return ((F + BF - 1) / BF) * ((M + BM - 1) / BM); }
 
 }  // namespace
 
@@ -312,14 +345,11 @@ hipError_t launch_adapter_gemm(const uint32_t* codes, const uint8_t* code8, cons
   const uint32_t nk = (uint32_t)((Kr + BK - 1) / BK), kb_per = (nk + split - 1) / split;
   const uint32_t splits = (nk + kb_per - 1) / kb_per;  // no split is empty
   const MidArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, M, F, Kr, head, C, splits > 1 ? part : nullptr, kb_per};
-  const int rows = head.transposed && M <= 64 ? 64 : 128;
-  const dim3 grid((unsigned)((F + BF - 1) / BF), (unsigned)((M + rows - 1) / rows), splits);
+  const dim3 grid((unsigned)((F + BF - 1) / BF), (unsigned)((M + BM - 1) / BM), splits);
   {
     LaunchTimer t(kernel_id, st);
     const auto go = [&](auto kernel) { hipExtLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, t.start, t.stop, 0, a, tab); };
-    if (!head.transposed) go(k_adapter_gemm<false, 2>);
-    else if (M <= 64) go(k_adapter_gemm<true, 1>);
-    else go(k_adapter_gemm<true, 2>);
+    head.transposed ? go(k_adapter_gemm<true>) : go(k_adapter_gemm<false>);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits <= 1) return e;
