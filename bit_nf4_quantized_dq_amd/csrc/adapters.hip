@@ -43,26 +43,17 @@ struct ShrinkArgs {
 // One workgroup per 16 rows and slice of the reduction.  An item is a 32-wide slab of the slice
 // and one of the rows' adapters; the wavefronts take the items in turn, D in flight each.  JT:
 // 16-rank tiles.  QT: the operand is B_a [Kd, r] (transposed through LDS), else A_a [r, Kd].
+template <int JT>
+struct ShrinkLds {
+  __attribute__((aligned(16))) char tiles[kShrinkWaves * JT * 1024];
+  bool last;
+};
 template <int JT, bool QT, bool DROP, bool VEC, int D>
-__global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a, ShrinkDecode dec, uint32_t n_shrink,
-                                                                   Nf4Tables tab) {
-  __shared__ __attribute__((aligned(16))) char smem[kShrinkWaves * JT * 1024];
-  __shared__ bool s_last;
-  if (blockIdx.x >= n_shrink) {  // the weight's decode, beside the products
-    if (!QT) {
-      decode_words<kDqE4M3, kShrinkThreads>(dec.codes, dec.code8, dec.c2s, dec.mu, reinterpret_cast<uint4*>(dec.out),
-                                            (int64_t)(blockIdx.x - n_shrink), threadIdx.x, dec.N * dec.K / 8, tab);
-    } else {
-      const uint32_t groups_k = (uint32_t)((dec.K / 64 + kShrinkWaves - 1) / kShrinkWaves);
-      const uint32_t grp = blockIdx.x - n_shrink, gn = grp / groups_k;
-      decode_pairs_t<kDqE4M3, kShrinkThreads>(dec.codes, dec.code8, dec.c2s, dec.mu, dec.out, dec.N, dec.K, tab,
-                                              (int64_t)gn, (int64_t)(grp - gn * groups_k), threadIdx.x);
-    }
-    return;
-  }
+__device__ __forceinline__ void shrink_body(const ShrinkArgs& a, uint32_t wg, ShrinkLds<JT>& lds) {
+  char* smem = lds.tiles;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const uint32_t split = (uint32_t)a.split, tile = blockIdx.x / split, slice = blockIdx.x - tile * split;
+  const uint32_t split = (uint32_t)a.split, tile = wg / split, slice = wg - tile * split;
   const int64_t m0 = (int64_t)tile * kRowTile, M = a.rows.M, Kd = a.Kd, width = a.rows.width;
   // each lane its row's adapter; the four groups of 16 lanes hold the same rows
   const int id = adapter_of(a.rows, m0 + l16);
@@ -180,9 +171,7 @@ __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a,
       for (int v = 0; v < 4; ++v) sum[v] = j + v < rank ? sum[v] * keep : 0.f;
       *reinterpret_cast<f32x4_t*>(a.out + m * width + j) = sum;
     } else {
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        __hip_atomic_store(a.part + ((int64_t)slice * M + m) * width + j + v, sum[v], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+      store_partial(a.part + ((int64_t)slice * M + m) * width + j, sum);
     }
   }
   if (split == 1) return;
@@ -191,26 +180,22 @@ __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a,
   __syncthreads();
   if (threadIdx.x == 0) {
     const unsigned int old = __hip_atomic_fetch_add(&a.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s_last = old + 1u == split;
-    if (s_last) __hip_atomic_store(&a.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    lds.last = old + 1u == split;
+    if (lds.last) __hip_atomic_store(&a.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
-  if (!s_last) return;
+  if (!lds.last) return;
   for (int t = wave; t < JT; t += kShrinkWaves) {
     const int j = 16 * t + 4 * g;
     if (m >= M || j >= width) continue;
     f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t s0 = 0; s0 < split; s0 += 4) {
-      float v[4][4];
+    for (uint32_t s0 = 0; s0 < split; s0 += 8) {
+      f32x4_t v[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 8; ++u)
+        v[u] = s0 + u < split ? load_partial(a.part + ((int64_t)(s0 + u) * M + m) * width + j) : f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[u][i] = s0 + u < split ? __hip_atomic_load(a.part + ((int64_t)(s0 + u) * M + m) * width + j + i, __ATOMIC_RELAXED,
-                                                       __HIP_MEMORY_SCOPE_SYSTEM)
-                                   : 0.f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 8; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] += v[u][i];
     }
@@ -218,6 +203,31 @@ __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a,
     for (int v = 0; v < 4; ++v) sum[v] = j + v < rank ? sum[v] * keep : 0.f;
     *reinterpret_cast<f32x4_t*>(a.out + m * width + j) = sum;
   }
+}
+
+// T or G; workgroups from n_shrink on decode the weight beside it (w_hat, or w_hat^T beside G).
+template <int JT, bool QT, bool DROP, bool VEC, int D>
+__global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a, ShrinkDecode dec, uint32_t n_shrink,
+                                                                   Nf4Tables tab) {
+  __shared__ ShrinkLds<JT> lds;
+  if (blockIdx.x < n_shrink) {
+    shrink_body<JT, QT, DROP, VEC, D>(a, blockIdx.x, lds);
+  } else if (!QT) {
+    decode_words<kDqE4M3, kShrinkThreads>(dec.codes, dec.code8, dec.c2s, dec.mu, reinterpret_cast<uint4*>(dec.out),
+                                          (int64_t)(blockIdx.x - n_shrink), threadIdx.x, dec.N * dec.K / 8, tab);
+  } else {
+    const uint32_t groups_k = (uint32_t)((dec.K / 64 + kShrinkWaves - 1) / kShrinkWaves);
+    const uint32_t grp = blockIdx.x - n_shrink, gn = grp / groups_k;
+    decode_pairs_t<kDqE4M3, kShrinkThreads>(dec.codes, dec.code8, dec.c2s, dec.mu, dec.out, dec.N, dec.K, tab, (int64_t)gn,
+                                            (int64_t)(grp - gn * groups_k), threadIdx.x);
+  }
+}
+// T and G in one launch: they are independent, and a launch alone takes 6 to 8 us for few rows.
+template <int JT, bool DROP, bool VEC, int D>
+__global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink2(ShrinkArgs t, ShrinkArgs g, uint32_t n_t) {
+  __shared__ ShrinkLds<JT> lds;
+  if (blockIdx.x < n_t) shrink_body<JT, false, DROP, true, D>(t, blockIdx.x, lds);
+  else shrink_body<JT, true, false, VEC, D>(g, blockIdx.x - n_t, lds);
 }
 
 template <int JT, bool QT, bool DROP, bool VEC>
@@ -233,6 +243,21 @@ hipError_t shrink_as(const ShrinkArgs& a, const ShrinkDecode* dec, const Nf4Tabl
   hipLaunchKernelGGL((k_adapter_shrink<JT, QT, DROP, VEC, kMost>), dim3((unsigned)(n + n_dec)), dim3(kShrinkThreads), 0, st, a,
                      d, (uint32_t)n, tab);
   return hipGetLastError();
+}
+template <int JT, bool DROP, bool VEC>
+hipError_t shrink2_as(const ShrinkArgs& t, const ShrinkArgs& g, hipStream_t st) {
+  constexpr int kMost = JT == 1 ? 8 : (JT == 2 ? 4 : 2);
+  const int64_t tiles = (t.rows.M + kRowTile - 1) / kRowTile, n_t = tiles * t.split;
+  hipLaunchKernelGGL((k_adapter_shrink2<JT, DROP, VEC, kMost>), dim3((unsigned)(n_t + tiles * g.split)), dim3(kShrinkThreads), 0,
+                     st, t, g, (uint32_t)n_t);
+  return hipGetLastError();
+}
+template <bool DROP, bool VEC>
+hipError_t shrink2_by_rank(const ShrinkArgs& t, const ShrinkArgs& g, hipStream_t st) {
+  if (t.rows.max_rank <= 16) return shrink2_as<1, DROP, VEC>(t, g, st);
+  if (t.rows.max_rank <= 32) return shrink2_as<2, DROP, VEC>(t, g, st);
+  if (t.rows.max_rank <= 64) return shrink2_as<4, DROP, VEC>(t, g, st);
+  return shrink2_as<8, DROP, VEC>(t, g, st);
 }
 template <bool QT, bool DROP, bool VEC>
 hipError_t shrink_by_rank(const ShrinkArgs& a, const ShrinkDecode* dec, const Nf4Tables& tab, hipStream_t st) {
@@ -672,7 +697,7 @@ constexpr int kGradCols = 64;         // columns per workgroup
 constexpr int kGradRanks = 64;        // ranks per workgroup
 constexpr int kSpan = 256;            // rows that a wavefront looks through at once
 constexpr int kVTile = 32 * 32 + 64;  // bytes of a staged [32][16] BF16 tile, padded (bank offset)
-constexpr int kSumU = 16;             // partials loaded together before they are added
+constexpr int kSumU = 4;              // partials loaded together before they are added
 
 struct GradsArgs {
   AdapterRows rows;
@@ -773,7 +798,6 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
           if (DROP) {
             const int m = row(i0 + 32 * d + in);
             v = drop8(v, key, (uint64_t)((first + (m < 0 ? 0 : m)) * (C / 8) + c0 / 8 + (lane & 7)), t2);
-            __builtin_amdgcn_sched_barrier(0);  // one vector's words at a time
           }
           *reinterpret_cast<uint4*>(vt + ct * kVTile + in * 32 + 16 * half) = v;
         }
@@ -811,30 +835,34 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
   __syncthreads();
   const float scale = DROP ? e.s * a.drop.scale : e.s;
   const int32_t split = a.split;
-  const int64_t CT = a.K + a.N;
-  float* part = a.part + ((int64_t)blockIdx.z * split * kGradRanks) * CT + (IS_B ? a.K : 0);
+  constexpr int kItems = JT * 4 * 64;  // of four ranks each
+  float* part = a.part + ((int64_t)(blockIdx.z * gridDim.x + blockIdx.x) * split) * kItems * 4;
   uint16_t* out = IS_B ? e.dB : e.dA;
-  const auto store = [&](int j, int64_t c, float v) {
-    const uint16_t h = (uint16_t)(pack_bf16x2(v * scale, 0.f) & 0xFFFFu);
-    if (IS_B) out[c * e.r + j] = h;
-    else out[(int64_t)j * C + c] = h;
+  // item i: ranks j_first + 16 (i / 256) + 4 (i % 64 / 16) .. +3 of column c0 + 16 (i / 64 % 4) + i % 16
+  const auto store = [&](int i, const f32x4_t& sum) {
+    const int l = i & 63;
+    const int64_t c = c0 + 16 * ((i >> 6) & 3) + (l & 15);
+    const int j = j_first + 16 * (i >> 8) + 4 * (l >> 4);
+    if (c >= C) return;
+    const uint32_t lo = pack_bf16x2(sum[0] * scale, sum[1] * scale), hi = pack_bf16x2(sum[2] * scale, sum[3] * scale);
+    const uint32_t h[4] = {lo & 0xFFFFu, lo >> 16, hi & 0xFFFFu, hi >> 16};
+    if (IS_B && (e.r & 3) == 0 && (reinterpret_cast<uintptr_t>(out) & 7u) == 0) {
+      if (j < e.r) *reinterpret_cast<uint2*>(out + c * e.r + j) = make_uint2(lo, hi);
+      return;
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (j + v < e.r) out[IS_B ? c * e.r + j + v : (int64_t)(j + v) * C + c] = (uint16_t)h[v];
   };
-  for (int i = threadIdx.x; i < JT * 4 * 64; i += kGradThreads) {
+  for (int i = threadIdx.x; i < kItems; i += kGradThreads) {
     const int l = i & 63, q = (i >> 6) & 3, t = i >> 8;
     f32x4_t sum = red[(t * 4 + q) * 64 + l];
     for (int w = 1; w < kGradWaves; ++w) {
       const f32x4_t v = red[((w * JT + t) * 4 + q) * 64 + l];
       sum[0] += v[0]; sum[1] += v[1]; sum[2] += v[2]; sum[3] += v[3];
     }
-    const int64_t c = c0 + 16 * q + (l & 15);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int j = 16 * t + 4 * (l >> 4) + v;
-      if (j_first + j >= e.r || c >= C) continue;
-      if (split == 1) store(j_first + j, c, sum[v]);
-      else
-        __hip_atomic_store(part + ((int64_t)blockIdx.y * kGradRanks + j) * CT + c, sum[v], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-    }
+    if (split == 1) store(i, sum);
+    else if (j_first + 16 * t < e.r) store_partial(part + ((int64_t)blockIdx.y * kItems + i) * 4, sum);
   }
   if (split == 1) return;
   // every partial store of this workgroup has completed before its counter increment
@@ -848,23 +876,19 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
   }
   __syncthreads();
   if (!lds.last) return;
-  const int ranks = e.r - j_first < 16 * JT ? e.r - j_first : 16 * JT;
-  for (int i = threadIdx.x; i < ranks * kGradCols; i += kGradThreads) {
-    const int j = i >> 6;
-    const int64_t c = c0 + (i & 63);
-    if (c >= C) continue;
-    const float* p = part + (int64_t)j * CT + c;
-    float s = 0.f;
+  for (int i = threadIdx.x; i < kItems && j_first + 16 * (i >> 8) < e.r; i += kGradThreads) {
+    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
     for (int32_t k0 = 0; k0 < split; k0 += kSumU) {
-      float v[kSumU];
+      f32x4_t v[kSumU];
 #pragma unroll
       for (int u = 0; u < kSumU; ++u)
-        v[u] = (k0 + u < split) ? __hip_atomic_load(p + (int64_t)(k0 + u) * kGradRanks * CT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM)
-                                : 0.f;
+        v[u] = k0 + u < split ? load_partial(part + ((int64_t)(k0 + u) * kItems + i) * 4) : f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < kSumU; ++u) s += v[u];
+      for (int u = 0; u < kSumU; ++u)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) sum[n] += v[u][n];
     }
-    store(j_first + j, c, s);
+    store(i, sum);
   }
 }
 
@@ -921,6 +945,16 @@ bool stream_forms_t(int64_t M, int64_t K, int32_t width) {
   return tiles <= kSelfTiles && tiles * 16 * K * 2 <= kSelfBytes;
 }
 
+hipError_t launch_shrink_both(const AdapterRows& rows, const uint16_t* X, int64_t K, const DropMask& drop, float* T,
+                              const uint16_t* dY, int64_t N, float* G, float* part_t, float* part_g,
+                              unsigned int* counters, hipStream_t st) {
+  const int64_t tiles = (rows.M + kRowTile - 1) / kRowTile;
+  const ShrinkArgs t{rows, X, K, drop, T, part_t, counters, shrink_split(rows.M, K)};
+  const ShrinkArgs g{rows, dY, N, DropMask{}, G, part_g, counters + tiles, shrink_split(rows.M, N)};
+  if (drop.threshold) return rows.whole ? shrink2_by_rank<true, true>(t, g, st) : shrink2_by_rank<true, false>(t, g, st);
+  return rows.whole ? shrink2_by_rank<false, true>(t, g, st) : shrink2_by_rank<false, false>(t, g, st);
+}
+
 hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, const float* c2s, const float* mu,
                                  int64_t N, int64_t K, const uint16_t* X, const AdapterRows& rows, const DropMask& drop,
                                  float* T, uint16_t* Y, const Nf4Tables& tab, hipStream_t st) {
@@ -960,8 +994,8 @@ GradPlan adapter_grad_plan(int64_t M, int64_t N, int64_t K, int32_t count, int32
   p.blocks = (max_rank + kGradRanks - 1) / kGradRanks;
   p.split = 1;
   const int64_t groups = (p.tiles_a + p.tiles_b) * count * p.blocks;
-  while (groups * p.split < 512 && (int64_t)p.split * 2 * 128 <= M && p.split < 64) p.split *= 2;
-  if (p.split > 1) p.part_bytes = sizeof(float) * (size_t)count * p.blocks * p.split * kGradRanks * (size_t)(K + N);
+  while (groups * p.split < 512 && (int64_t)p.split * 2 * 512 <= M && p.split < 64) p.split *= 2;
+  if (p.split > 1) p.part_bytes = sizeof(float) * (size_t)groups * p.split * kGradRanks * kGradCols;
   return p;
 }
 

@@ -63,7 +63,7 @@ bool codes_path(int64_t M, int64_t F, int dq) { return dq == QLORA_DQ_E4M3 && ad
 
 // ---- workspaces: the counter head, then T and G, then what the steps need in turn
 struct Layout {
-  size_t t, g, spart, wcopy, gpart, grads, total;
+  size_t t, g, spart, gspart, wcopy, gpart, grads, total;
   int32_t gsplit;
 };
 Layout layout(bool bwd, int64_t M, const qlora_adapters_t* set, int dq) {
@@ -79,8 +79,9 @@ Layout layout(bool bwd, int64_t M, const qlora_adapters_t* set, int dq) {
   w.t = take(t_bytes);
   if (bwd) w.g = take(t_bytes);
   if (bwd || !stream_path(M, dq)) {
-    const int32_t split = std::max(shrink_split(M, K), bwd ? shrink_split(M, N) : 1);
-    w.spart = take(split > 1 ? t_bytes * split : 0);
+    const int32_t t_split = shrink_split(M, K), g_split = shrink_split(M, N);
+    w.spart = take(t_split > 1 ? t_bytes * t_split : 0);
+    if (bwd) w.gspart = take(g_split > 1 ? t_bytes * g_split : 0);
     const int64_t F = bwd ? K : N, Kr = bwd ? N : K;
     if (!codes_path(M, F, dq)) w.wcopy = take(2 * (size_t)N * K);
     w.gsplit = codes_path(M, F, dq) ? adapter_gemm_split(M, F, Kr) : gemm_nt_ksplit(F, M, Kr);
@@ -211,26 +212,34 @@ int qlora_adapters_bwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   float* G = reinterpret_cast<float*>(base + L.g);
   float* part = reinterpret_cast<float*>(base + L.spart);
   unsigned int* counters = static_cast<unsigned int*>(ws);
-  const float* T = T_saved;
-  if (!T) {
-    float* t = reinterpret_cast<float*>(base + L.t);
-    if (launch_shrink_a(rows, X, K, drop, t, part, counters, nullptr, tab, stream) != hipSuccess) return QLORA_ERR_HIP;
-    T = t;
-  }
+  float* g_part = reinterpret_cast<float*>(base + L.gspart);
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(Wq->codes);
   uint16_t* wcopy = reinterpret_cast<uint16_t*>(base + L.wcopy);
   const bool copied = dX && !codes_path(M, K, dq);
+  const bool beside = copied && dq == QLORA_DQ_E4M3;  // the decode joins G's launch
   const ShrinkDecode dec = decode_args(Wq, wcopy);
-  if (launch_shrink_b(rows, dY, N, G, part, counters, copied && dq == QLORA_DQ_E4M3 ? &dec : nullptr, tab, stream) != hipSuccess)
-    return QLORA_ERR_HIP;
+  const float* T = T_saved;
+  hipError_t e;
+  if (!T && !beside) {
+    float* t = reinterpret_cast<float*>(base + L.t);
+    e = launch_shrink_both(rows, X, K, drop, t, dY, N, G, part, g_part, counters, stream);
+    T = t;
+  } else {
+    if (!T) {
+      float* t = reinterpret_cast<float*>(base + L.t);
+      if (launch_shrink_a(rows, X, K, drop, t, part, counters, nullptr, tab, stream) != hipSuccess) return QLORA_ERR_HIP;
+      T = t;
+    }
+    e = launch_shrink_b(rows, dY, N, G, g_part, counters, beside ? &dec : nullptr, tab, stream);
+  }
+  if (e != hipSuccess) return QLORA_ERR_HIP;
   if (dX) {
     if (copied && dq != QLORA_DQ_E4M3 &&
         launch_dequant_t(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, wcopy, tab, dq, stream) != hipSuccess)
       return QLORA_ERR_HIP;
     const AdapterHead head{rows, G, 1, drop.scale, drop};
     float* gpart = reinterpret_cast<float*>(base + L.gpart);
-    const hipError_t e =
-        copied ? launch_gemm_nt_adapters(wcopy, K, dY, M, N, head, dX, QLORA_K_GEMM_DX, stream, gpart, L.gsplit)
+    e = copied ? launch_gemm_nt_adapters(wcopy, K, dY, M, N, head, dX, QLORA_K_GEMM_DX, stream, gpart, L.gsplit)
                : launch_adapter_gemm(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, dY, M, head, dX, gpart, L.gsplit, tab,
                                      QLORA_K_GEMM_DX, stream);
     if (e != hipSuccess) return QLORA_ERR_HIP;

@@ -118,6 +118,22 @@ __device__ __forceinline__ uint4 load_row8(const uint16_t* __restrict__ p, int64
   return make_uint4(v.x & keep(0), v.y & keep(1), v.z & keep(2), v.w & keep(3));
 }
 
+// ---- partial sums between workgroups: stores and loads that pass the caches, 8 bytes each
+__device__ __forceinline__ void store_partial(float* to, const f32x4_t& v) {
+  uint64_t* p = reinterpret_cast<uint64_t*>(to);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    __hip_atomic_store(p + i, ((uint64_t)__float_as_uint(v[2 * i + 1]) << 32) | __float_as_uint(v[2 * i]), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_SYSTEM);
+}
+__device__ __forceinline__ f32x4_t load_partial(const float* from) {
+  const uint64_t* p = reinterpret_cast<const uint64_t*>(from);
+  const uint64_t a = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+  const uint64_t b = __hip_atomic_load(p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+  return f32x4_t{__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32)), __uint_as_float((uint32_t)b),
+                 __uint_as_float((uint32_t)(b >> 32))};
+}
+
 // Row m's adapter, -1 for none (also past the rows).
 __device__ __forceinline__ int adapter_of(const AdapterRows& rows, int64_t m) {
   if (m >= rows.M) return -1;

@@ -59,6 +59,10 @@ hipError_t launch_shrink_a(const AdapterRows& rows, const uint16_t* X, int64_t K
                            hipStream_t st);
 hipError_t launch_shrink_b(const AdapterRows& rows, const uint16_t* dY, int64_t N, float* G, float* part,
                            unsigned int* counters, const ShrinkDecode* decode, const Nf4Tables& tab, hipStream_t st);
+// T and G in one launch (no decode); counters: two per 16 rows.
+hipError_t launch_shrink_both(const AdapterRows& rows, const uint16_t* X, int64_t K, const DropMask& drop, float* T,
+                              const uint16_t* dY, int64_t N, float* G, float* part_t, float* part_g,
+                              unsigned int* counters, hipStream_t st);
 
 // ---- few rows: Y by a launch that streams the weight once (E4M3 constants).  T (FP32 [M, width]) is
 // written by a launch before it, or, where stream_forms_t(), by the same one (T may then be NULL).
@@ -91,7 +95,7 @@ hipError_t launch_adapter_gemm(const uint32_t* codes, const uint8_t* code8, cons
                                int32_t split, const Nf4Tables& tab, int kernel_id, hipStream_t st);
 
 // ---- dA_a and dB_a of every adapter in one launch.  Rows in `split` slices; with more than one,
-// FP32 partials [adapter][rank block][split][64][columns of dA and dB] and one counter per
+// FP32 partials [adapter][rank block][column tile][split][64 x 64] and one counter per
 // (adapter, rank block, column tile).
 struct GradPlan {
   int64_t tiles_a, tiles_b;  // 64-column tiles of dA and dB
