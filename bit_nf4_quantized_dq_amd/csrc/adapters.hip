@@ -40,17 +40,19 @@ struct ShrinkArgs {
   int32_t split;
 };
 
-// One workgroup per 16 rows and slice of the reduction.  An item is a 32-wide slab of the slice
-// and one of the rows' adapters; the wavefronts take the items in turn, D in flight each.  JT:
-// 16-rank tiles.  QT: the operand is B_a [Kd, r] (transposed through LDS), else A_a [r, Kd].
+// One workgroup per 16 rows and slice of the reduction.  An item is 64 columns (or rows of B) of the
+// slice for one of the rows' adapters; the wavefronts take the items in turn, D in flight each.
+// JT: 16-rank tiles.  QT: the operand is B_a [Kd, r], else A_a [r, Kd].  Rows of X (dY) and A come in
+// whole cache lines and pass through the wavefront's own LDS into operand order, chunks laid as in
+// the stream below (straight into operand order, where neighbouring lanes are in 16 rows, the
+// address unit bounds the loads: 256 rows of 48 adapters over 14336 columns 21 us).
 template <int JT>
 struct ShrinkLds {
-  __attribute__((aligned(16))) char tiles[kShrinkWaves * JT * 1024];
+  uint4 tiles[kShrinkWaves][(1 + JT) * 128];
   bool last;
 };
 template <int JT, bool QT, bool DROP, bool VEC, int D>
 __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, uint32_t wg, ShrinkLds<JT>& lds) {
-  char* smem = lds.tiles;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const uint32_t split = (uint32_t)a.split, tile = wg / split, slice = wg - tile * split;
@@ -70,15 +72,16 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, uint32_t wg, Sh
   const rsrc_t rp = make_rsrc(a.P + m0 * Kd, (M - m0) * Kd * 2);
   const uint64_t block0 = (uint64_t)(m0 + l16) * (uint64_t)(Kd / 8);
 
-  const int nslab = (int)((Kd + 31) / 32), per = (nslab + (int)split - 1) / (int)split;
-  const int sbeg = (int)slice * per, send = sbeg + per < nslab ? sbeg + per : nslab, len = send - sbeg;
+  const int nblk = (int)((Kd + 63) / 64), per = (nblk + (int)split - 1) / (int)split;
+  const int sbeg = (int)slice * per, send = sbeg + per < nblk ? sbeg + per : nblk, len = send - sbeg;
   f32x4_t acc[JT];
 #pragma unroll
   for (int t = 0; t < JT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  char* qs = smem + wave * JT * 1024;
+  uint4* xs = lds.tiles[wave];
+  uint4* qs = xs + 128;
 
   uint64_t pending = __ballot(id >= 0);
-  int cur = -1, from = 0, at = wave;  // the adapter's lane (`from`: the last one's), the slab within the slice
+  int cur = -1, from = 0, at = wave;  // the adapter's lane (`from`: the last one's), the block within the slice
   if (len > 0 && pending) {
     cur = lowest(pending);
     const auto step = [&](int by) {  // to the item `by` further on
@@ -91,34 +94,39 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, uint32_t wg, Sh
     };
     step(0);
     while (cur >= 0) {
-      uint4 pv[D], qv[D][JT];
-      int which[D], slab[D];
+      uint4 pv[D][2], qv[D][JT][2];
+      int which[D], blk[D];
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         const bool live = cur >= 0;
         from = live ? cur : from;
         which[d] = live ? __builtin_amdgcn_readlane(id, from) : -2;
-        slab[d] = sbeg + at;
+        blk[d] = sbeg + at;
         const int r = __builtin_amdgcn_readlane(rank, from);
+        const uint64_t rows_mine = __ballot(id == which[d]);  // bit m: row m of the tile
         const rsrc_t rq = make_rsrc(reinterpret_cast<const void*>(readlane64(base, from)), live ? (int64_t)r * Kd * 2 : 0);
-        const int64_t k = 32 * (int64_t)slab[d] + 8 * g;
-        pv[d] = bload16(rp, (id == which[d] && k < Kd) ? (uint32_t)((l16 * Kd + k) * 2) : kOOB);
-        if (!QT) {
 #pragma unroll
-          for (int t = 0; t < JT; ++t) {
-            const int j = 16 * t + l16;
-            qv[d][t] = bload16(rq, (k < Kd && j < r) ? (uint32_t)(((int64_t)j * Kd + k) * 2) : kOOB);
-          }
-        } else {
-          // rows 32 slab + (lane >> 1), columns 8 (lane & 1) .. +7 of every tile
-          const int64_t kr = 32 * (int64_t)slab[d] + (lane >> 1);
+        for (int i = 0; i < 2; ++i) {
+          const int row = 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((4 * i + (lane >> 4)) & 7);
+          const int64_t k = 64 * (int64_t)blk[d] + 8 * chunk;
+          pv[d][i] = bload16(rp, (k < Kd && ((rows_mine >> row) & 1)) ? (uint32_t)((row * Kd + k) * 2) : kOOB);
+          if (!QT) {
 #pragma unroll
-          for (int t = 0; t < JT; ++t) {
-            const int j = 16 * t + 8 * (lane & 1);
-            if (VEC)
-              qv[d][t] = bload16(rq, (kr < Kd && j < r) ? (uint32_t)((kr * r + j) * 2) : kOOB);
-            else  // past the rows (or without an item) the last row again, whose product with zeros is not taken
-              qv[d][t] = load_row8(reinterpret_cast<const uint16_t*>(readlane64(base, from)), Kd * r, (kr < Kd ? kr : Kd - 1) * r, j, r);
+            for (int t = 0; t < JT; ++t) {
+              const int j = 16 * t + row;
+              qv[d][t][i] = bload16(rq, (k < Kd && j < r) ? (uint32_t)((j * Kd + k) * 2) : kOOB);
+            }
+          } else {
+            // rows 64 blk + 32 i + (lane >> 1), columns 8 (lane & 1) .. +7 of every tile
+            const int64_t kr = 64 * (int64_t)blk[d] + 32 * i + (lane >> 1);
+#pragma unroll
+            for (int t = 0; t < JT; ++t) {
+              const int j = 16 * t + 8 * (lane & 1);
+              if (VEC)
+                qv[d][t][i] = bload16(rq, (kr < Kd && j < r) ? (uint32_t)((kr * r + j) * 2) : kOOB);
+              else  // past the rows (or without an item) the last row again, whose product with zeros is not taken
+                qv[d][t][i] = load_row8(reinterpret_cast<const uint16_t*>(readlane64(base, from)), Kd * r, (kr < Kd ? kr : Kd - 1) * r, j, r);
+            }
           }
         }
         if (live) step(kShrinkWaves);
@@ -126,33 +134,40 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, uint32_t wg, Sh
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         const bool mine = id == which[d];
-        bf16x8_t qa[JT];
-        if (!QT) {
+        // the wavefront's LDS tiles are reused item after item; its LDS accesses run in order
+        asm volatile("" ::: "memory");
 #pragma unroll
-          for (int t = 0; t < JT; ++t) qa[t] = as_bf16x8(qv[d][t]);
-        } else {
-          // the wavefront's LDS tiles are reused item after item; its LDS accesses run in order
-          asm volatile("" ::: "memory");
+        for (int i = 0; i < 2; ++i) {
+          xs[64 * i + lane] = pv[d][i];
 #pragma unroll
-          for (int t = 0; t < JT; ++t) *reinterpret_cast<uint4*>(qs + t * 1024 + (lane >> 1) * 32 + 16 * (lane & 1)) = qv[d][t];
-          asm volatile("" ::: "memory");
-#pragma unroll
-          for (int t = 0; t < JT; ++t) qa[t] = tr_operand(qs + t * 1024, l16, 8 * g);
-          asm volatile("" ::: "memory");
+          for (int t = 0; t < JT; ++t) qs[128 * t + 64 * i + lane] = qv[d][t][i];
         }
-        const uint4 p = DROP ? drop8(pv[d], key, block0 + (uint64_t)(4 * slab[d] + g), t2) : pv[d];
+        asm volatile("" ::: "memory");
+        f32x4_t v[JT];
 #pragma unroll
-        for (int t = 0; t < JT; ++t) {
-          const f32x4_t v = mfma16x16x32(qa[t], as_bf16x8(p), f32x4_t{0.f, 0.f, 0.f, 0.f});
+        for (int t = 0; t < JT; ++t) v[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][i] += mine ? v[i] : 0.f;
+        for (int h = 0; h < 2; ++h) {
+          const int chunk = 8 * l16 + ((4 * h + g) ^ (l16 >> 1));
+          uint4 p = xs[chunk];
+          if (DROP) p = drop8(p, key, block0 + (uint64_t)(8 * blk[d] + 4 * h + g), t2);
+#pragma unroll
+          for (int t = 0; t < JT; ++t)
+            v[t] = mfma16x16x32(QT ? tr_operand(reinterpret_cast<const char*>(qs + 128 * t + 64 * h), l16, 8 * g)
+                                   : as_bf16x8(qs[128 * t + chunk]),
+                                as_bf16x8(p), v[t]);
         }
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int t = 0; t < JT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][i] += mine ? v[t][i] : 0.f;
       }
     }
   }
   // fixed-order sum over the wavefronts; D[j][m]: lane l holds ranks 4 (l >> 4) + v of row l & 15
   __syncthreads();
-  f32x4_t* red = reinterpret_cast<f32x4_t*>(smem);
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(&lds.tiles[0][0]);
 #pragma unroll
   for (int t = 0; t < JT; ++t) red[(wave * JT + t) * 64 + lane] = acc[t];
   __syncthreads();
@@ -232,7 +247,7 @@ __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink2(ShrinkArgs t
 
 template <int JT, bool QT, bool DROP, bool VEC>
 hipError_t shrink_as(const ShrinkArgs& a, const ShrinkDecode* dec, const Nf4Tables& tab, hipStream_t st) {
-  constexpr int kMost = JT == 1 ? 8 : (JT == 2 ? 4 : 2);
+  constexpr int kMost = JT == 1 ? 4 : (JT <= 4 ? 2 : 1);
   const int64_t tiles = (a.rows.M + kRowTile - 1) / kRowTile;
   const int64_t n = tiles * a.split;
   int64_t n_dec = 0;
@@ -246,7 +261,7 @@ hipError_t shrink_as(const ShrinkArgs& a, const ShrinkDecode* dec, const Nf4Tabl
 }
 template <int JT, bool DROP, bool VEC>
 hipError_t shrink2_as(const ShrinkArgs& t, const ShrinkArgs& g, hipStream_t st) {
-  constexpr int kMost = JT == 1 ? 8 : (JT == 2 ? 4 : 2);
+  constexpr int kMost = JT == 1 ? 4 : (JT <= 4 ? 2 : 1);
   const int64_t tiles = (t.rows.M + kRowTile - 1) / kRowTile, n_t = tiles * t.split;
   hipLaunchKernelGGL((k_adapter_shrink2<JT, DROP, VEC, kMost>), dim3((unsigned)(n_t + tiles * g.split)), dim3(kShrinkThreads), 0,
                      st, t, g, (uint32_t)n_t);
@@ -916,8 +931,8 @@ hipError_t launch_adapter_table(const AdapterBatch& batch, int count, AdapterEnt
 }
 
 int32_t shrink_split(int64_t M, int64_t Kd) {
-  const int64_t tiles = (M + kRowTile - 1) / kRowTile, slabs = (Kd + 31) / 32;
-  const int64_t split = std::min<int64_t>({int64_t(16), 256 / tiles, slabs / kShrinkWaves});
+  const int64_t tiles = (M + kRowTile - 1) / kRowTile, blocks = (Kd + 63) / 64;
+  const int64_t split = std::min<int64_t>({int64_t(16), 256 / tiles, blocks / kShrinkWaves});
   return (int32_t)std::max<int64_t>(split, 1);
 }
 
