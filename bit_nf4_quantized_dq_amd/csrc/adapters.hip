@@ -423,14 +423,15 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_t(StreamArgs a) {
 //
 // The adapters' term is more of the same sum.  E == 0: T is there; the wavefronts deal the distinct
 // adapters of all rows among themselves, and each multiplies its ones' 16 rows of B with T (hi and
-// lo BF16 parts) into its accumulators.  E > 0 (a row or a few, up to E tiles of 16 ranks in all):
-// every workgroup forms T itself, A's rows passing beside X's as E more tiles, which costs less
-// than a launch before this one.
-template <int MT, int E, int PD, bool WHOLE>
-__global__ __launch_bounds__(kStreamThreads, E == 0 && MT <= 3 ? 4 : 2) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
+// lo BF16 parts) into its accumulators.  E > 0 (a row or two, up to E tiles of 16 ranks in all):
+// every workgroup forms T itself, A's rows passing beside X's as E more tiles.  W: wavefronts; four
+// where there are more than two workgroups of eight to a compute unit (longer runs of blocks for
+// each: 37 rows at 14336 x 4096 41 -> 39 us, 64 rows 42 -> 36).
+template <int W, int MT, int E, int PD, bool WHOLE>
+__global__ __launch_bounds__(64 * W, E == 0 && MT <= 3 ? 4 : 2) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
   static_assert(E == 0 || MT == 1, "T is formed for one tile of rows");
   constexpr int XT = MT + E;  // tiles that pass through LDS
-  __shared__ uint4 smem[kStreamWaves * XT * 128];  // a block of them for each wavefront; then the sums
+  __shared__ uint4 smem[W * XT * 128];  // a block of them for each wavefront; then the sums
   f32x4_t(*red)[XT][64] = reinterpret_cast<f32x4_t(*)[XT][64]>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -461,7 +462,7 @@ __global__ __launch_bounds__(kStreamThreads, E == 0 && MT <= 3 ? 4 : 2) void k_a
   int id[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) id[t] = adapter_of(a.rows, 16 * t + l16);
-  Codes cur = load(wave), next = load(wave + kStreamWaves);
+  Codes cur = load(wave), next = load(wave + W);
   const float mu = a.mu[0];
   f32x4_t acc[XT];
 #pragma unroll
@@ -500,7 +501,7 @@ __global__ __launch_bounds__(kStreamThreads, E == 0 && MT <= 3 ? 4 : 2) void k_a
         } else {
           mine = lane == count ? one : mine;
           ++count;
-          skip = kStreamWaves - 1;
+          skip = W - 1;
         }
       }
   } else {
@@ -554,10 +555,10 @@ __global__ __launch_bounds__(kStreamThreads, E == 0 && MT <= 3 ? 4 : 2) void k_a
   const uint32_t t2 = threshold_halves(a.drop.threshold);
 
   // ---- the base product, and T beside it
-  for (uint32_t group = wave; group < ng; group += kStreamWaves) {
+  for (uint32_t group = wave; group < ng; group += W) {
     const Codes c = cur;
     cur = next;
-    next = load(group + 2 * kStreamWaves);
+    next = load(group + 2 * W);
     Lut L;
     build_scaled_lut(tab, stored_scale(c.c8, __uint_as_float(c.c2), mu), L);
     const uint32_t words[8] = {c.c0.x, c.c0.y, c.c0.z, c.c0.w, c.c1.x, c.c1.y, c.c1.z, c.c1.w};
@@ -582,7 +583,7 @@ __global__ __launch_bounds__(kStreamThreads, E == 0 && MT <= 3 ? 4 : 2) void k_a
 #pragma unroll
         for (int i = 0; i < 2; ++i) xs[128 * t + 64 * i + lane] = xr[b % PD][t][i];
       asm volatile("" ::: "memory");
-      const uint32_t ahead = 4 * (group + kStreamWaves * ((b + PD) / 4)) + (b + PD) % 4;
+      const uint32_t ahead = 4 * (group + W * ((b + PD) / 4)) + (b + PD) % 4;
       load_x(xr[b % PD], ahead);
       if (E > 0) load_a(xr[b % PD], ahead);
 #pragma unroll
@@ -642,14 +643,14 @@ __global__ __launch_bounds__(kStreamThreads, E == 0 && MT <= 3 ? 4 : 2) void k_a
   const auto summed = [&](int t) {
     f32x4_t y = red[0][t][lane];
 #pragma unroll
-    for (int w = 1; w < kStreamWaves; ++w) {
+    for (int w = 1; w < W; ++w) {
       const f32x4_t v = red[w][t][lane];
       y[0] += v[0]; y[1] += v[1]; y[2] += v[2]; y[3] += v[3];
     }
     return y;
   };
   if (E == 0) {
-    for (int t = wave; t < MT; t += kStreamWaves) {
+    for (int t = wave; t < MT; t += W) {
       const int m = 16 * t + l16;
       if (m >= M) continue;
       const f32x4_t y = summed(t);
@@ -914,6 +915,23 @@ __global__ __launch_bounds__(kGradThreads) void k_adapter_grads(GradsArgs a) {
   else grads_body<JT, D, false, true>(a, lds);
 }
 
+template <int W, int MT, int E, int PD>
+hipError_t stream_go(const StreamArgs& a, const Nf4Tables& tab, hipStream_t st) {
+  const dim3 grid((unsigned)(a.N / kStreamRows));
+  if (a.rows.whole) hipLaunchKernelGGL((k_adapter_stream<W, MT, E, PD, true>), grid, dim3(64 * W), 0, st, a, tab);
+  else hipLaunchKernelGGL((k_adapter_stream<W, MT, E, PD, false>), grid, dim3(64 * W), 0, st, a, tab);
+  return hipGetLastError();
+}
+template <int W>
+hipError_t stream_as(const StreamArgs& a, const Nf4Tables& tab, hipStream_t st) {
+  if (a.rows.M <= 16) return stream_go<W, 1, 0, 4>(a, tab, st);
+  if (a.rows.M <= 32) return stream_go<W, 2, 0, 2>(a, tab, st);
+  if (a.rows.M <= 48) return stream_go<W, 3, 0, 1>(a, tab, st);
+  if (a.rows.M <= 64) return stream_go<W, 4, 0, 1>(a, tab, st);
+  if (a.rows.M <= 96) return stream_go<W, 6, 0, 1>(a, tab, st);
+  return stream_go<W, 8, 0, 1>(a, tab, st);
+}
+
 template <int JT>
 hipError_t grads_as(const GradsArgs& a, const GradPlan& plan, hipStream_t st) {
   constexpr int D = JT <= 2 ? 4 : 2;
@@ -932,7 +950,7 @@ hipError_t launch_adapter_table(const AdapterBatch& batch, int count, AdapterEnt
 
 int32_t shrink_split(int64_t M, int64_t Kd) {
   const int64_t tiles = (M + kRowTile - 1) / kRowTile, blocks = (Kd + 63) / 64;
-  const int64_t split = std::min<int64_t>({int64_t(16), 256 / tiles, blocks / kShrinkWaves});
+  const int64_t split = std::min<int64_t>({int64_t(32), 512 / tiles, blocks / kShrinkWaves});
   return (int32_t)std::max<int64_t>(split, 1);
 }
 
@@ -951,15 +969,6 @@ hipError_t launch_shrink_b(const AdapterRows& rows, const uint16_t* dY, int64_t 
                     : shrink_by_rank<true, false, false>(a, decode, tab, st);
 }
 
-// Tiles of 16 ranks in all up to which every workgroup of the stream forms T itself.
-constexpr int kSelfTiles = 1;
-constexpr int64_t kSelfBytes = int64_t(1) << 19;  // of A that each of them reads
-
-bool stream_forms_t(int64_t M, int64_t K, int32_t width) {
-  const int64_t tiles = M * ((width + 15) / 16);
-  return tiles <= kSelfTiles && tiles * 16 * K * 2 <= kSelfBytes;
-}
-
 hipError_t launch_shrink_both(const AdapterRows& rows, const uint16_t* X, int64_t K, const DropMask& drop, float* T,
                               const uint16_t* dY, int64_t N, float* G, float* part_t, float* part_g,
                               unsigned int* counters, hipStream_t st) {
@@ -970,6 +979,15 @@ hipError_t launch_shrink_both(const AdapterRows& rows, const uint16_t* X, int64_
   return rows.whole ? shrink2_by_rank<false, true>(t, g, st) : shrink2_by_rank<false, false>(t, g, st);
 }
 
+// Where every workgroup of the stream forms T itself: up to two tiles of 16 ranks in all, while
+// reading them in every workgroup costs less than the launch that it saves (4096 x 4096: one tile
+// 9.8 us and 12.2 in two launches, two tiles 11.0 and 12.3, four 15.6 and 12.5; one tile at 14336 x
+// 4096 31.8 and 24.0).  That launch is slower over long rows (4096 x 14336 22.0 and 27.4).
+bool stream_forms_t(int64_t M, int64_t N, int64_t K, int32_t width) {
+  const int64_t tiles = M * ((width + 15) / 16);
+  return tiles <= 2 && (2 * tiles * N * K <= (int64_t(1) << 26) || (tiles == 1 && N <= 4096));
+}
+
 hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, const float* c2s, const float* mu,
                                  int64_t N, int64_t K, const uint16_t* X, const AdapterRows& rows, const DropMask& drop,
                                  float* T, uint16_t* Y, const Nf4Tables& tab, hipStream_t st) {
@@ -977,29 +995,15 @@ hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, co
   const int tiles = (int)((rows.M + kRowTile - 1) / kRowTile), ranks = (rows.width + 15) / 16;
   const StreamArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, rows, drop, T, Y,
                      std::min((int)rows.count, kRowTile)};
-  const dim3 grid((unsigned)(N / kStreamRows));
-  const auto go = [&](auto whole, auto not_whole) {
-    if (rows.whole) hipLaunchKernelGGL(whole, grid, dim3(kStreamThreads), 0, st, a, tab);
-    else hipLaunchKernelGGL(not_whole, grid, dim3(kStreamThreads), 0, st, a, tab);
-  };
-  if (stream_forms_t(rows.M, K, rows.width)) {
-    const int64_t e = rows.M * ranks;
-    if (e <= 1) go(k_adapter_stream<1, 1, 4, true>, k_adapter_stream<1, 1, 4, false>);
-    else go(k_adapter_stream<1, 2, 2, true>, k_adapter_stream<1, 2, 2, false>);
-    return hipGetLastError();
+  if (stream_forms_t(rows.M, N, K, rows.width)) {
+    return rows.M * ranks <= 1 ? stream_go<8, 1, 1, 4>(a, tab, st) : stream_go<8, 1, 2, 2>(a, tab, st);
   }
   const dim3 grid_t((unsigned)(tiles * ranks * a.lists));
   if (drop.threshold) hipLaunchKernelGGL(k_adapter_t<true>, grid_t, dim3(kStreamThreads), 0, st, a);
   else hipLaunchKernelGGL(k_adapter_t<false>, grid_t, dim3(kStreamThreads), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (rows.M <= 16) go(k_adapter_stream<1, 0, 4, true>, k_adapter_stream<1, 0, 4, false>);
-  else if (rows.M <= 32) go(k_adapter_stream<2, 0, 2, true>, k_adapter_stream<2, 0, 2, false>);
-  else if (rows.M <= 48) go(k_adapter_stream<3, 0, 1, true>, k_adapter_stream<3, 0, 1, false>);
-  else if (rows.M <= 64) go(k_adapter_stream<4, 0, 1, true>, k_adapter_stream<4, 0, 1, false>);
-  else if (rows.M <= 96) go(k_adapter_stream<6, 0, 1, true>, k_adapter_stream<6, 0, 1, false>);
-  else go(k_adapter_stream<8, 0, 1, true>, k_adapter_stream<8, 0, 1, false>);
-  return hipGetLastError();
+  return N / kStreamRows > 512 ? stream_as<4>(a, tab, st) : stream_as<8>(a, tab, st);
 }
 
 GradPlan adapter_grad_plan(int64_t M, int64_t N, int64_t K, int32_t count, int32_t max_rank) {
