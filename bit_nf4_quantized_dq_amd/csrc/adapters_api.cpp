@@ -16,6 +16,11 @@ constexpr int64_t kMaxDropout = int64_t(1) << 40;
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+// Two ranges of memory that share no byte.
+inline bool apart(const void* p, size_t bytes, const void* q, size_t other) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a + bytes <= b || b + other <= a;
+}
 int hip_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP; }
 inline bool type_ok(int type) { return type == QLORA_BF16 || type == QLORA_F32; }
 inline size_t type_bytes(int type) { return type == QLORA_F32 ? 4 : 2; }
@@ -162,6 +167,7 @@ int qlora_adapters_fwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   int st = check_call(Wq, set, M, ids, dropout, rng, &drop);
   if (st) return st;
   if (!X || !Y || !aligned(X, 16) || !aligned(Y, 16) || !aligned(T_save, 16)) return QLORA_ERR_INVALID_ARG;
+  if (!apart(X, 2 * (size_t)M * Wq->d_in, Y, 2 * (size_t)M * Wq->d_out)) return QLORA_ERR_INVALID_ARG;
   const int dq = Wq->dq_format;
   const Layout L = layout(false, M, set, dq);
   if ((st = check_ws(ws, ws_bytes, L.total))) return st;
@@ -201,6 +207,9 @@ int qlora_adapters_bwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   if (st) return st;
   if (!set->grads) return QLORA_ERR_INVALID_ARG;
   if (!X || !dY || !aligned(X, 16) || !aligned(dY, 16) || !aligned(dX, 16) || !aligned(T_saved, 16))
+    return QLORA_ERR_INVALID_ARG;
+  const size_t x_bytes = 2 * (size_t)M * Wq->d_in;
+  if (dX && (!apart(dX, x_bytes, X, x_bytes) || !apart(dX, x_bytes, dY, 2 * (size_t)M * Wq->d_out)))
     return QLORA_ERR_INVALID_ARG;
   const int dq = Wq->dq_format;
   const Layout L = layout(true, M, set, dq);
@@ -258,12 +267,11 @@ int qlora_dropout(const void* x, int x_type, int64_t n, float dropout, const uin
   if (n == 0) return QLORA_OK;
   const size_t xb = type_bytes(x_type), ob = type_bytes(out_type);
   if (!x || !out || !aligned(x, xb) || !aligned(out, ob) || !aligned(residual, ob)) return QLORA_ERR_INVALID_ARG;
-  // out's bytes against those of an operand: none shared, or the very same elements
-  const auto apart = [&](const void* p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), o = reinterpret_cast<uintptr_t>(out);
-    return (a == o && bytes == ob) || a + (uintptr_t)n * bytes <= o || o + (uintptr_t)n * ob <= a;
+  // an operand is out itself, element for element, or shares no byte with it
+  const auto separate = [&](const void* p, size_t bytes) {
+    return (p == out && bytes == ob) || apart(p, (size_t)n * bytes, out, (size_t)n * ob);
   };
-  if (!apart(x, xb) || (residual && !apart(residual, ob))) return QLORA_ERR_INVALID_ARG;
+  if (!separate(x, xb) || (residual && !separate(residual, ob))) return QLORA_ERR_INVALID_ARG;
   return hip_status(launch_dropout(x, x_type == QLORA_F32, n, drop, residual, out, out_type == QLORA_F32, stream));
 }
 

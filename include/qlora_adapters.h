@@ -6,9 +6,10 @@
  * uint16_t bit patterns, a status per call, arguments checked before any launch, work enqueued
  * on `stream` without synchronization, no device memory allocated, and workspaces whose first
  * QLORA_WS_COUNTER_BYTES bytes are zero before their first use and left zero by every call (one
- * workspace serves calls of any kind; calls that share one must not overlap in time).  Every
- * call may be captured in a HIP graph.  Sums are taken in a fixed order: the same inputs give
- * the same bits.
+ * workspace serves calls of any kind; calls that share one must not overlap in time, and graphs
+ * captured with one must not run at once).  Outputs overlap no input unless stated otherwise.
+ * Every call may be captured in a HIP graph.  Sums are taken in a fixed order: the same inputs
+ * give the same bits.
  *
  * Dropout masks come from a counter-based generator and are never stored: Philox4x32 with ten
  * rounds ("Parallel random numbers: as easy as 1, 2, 3", Salmon et al. 2011).  `rng` is device
@@ -83,8 +84,8 @@ int qlora_adapters_workspace_size(int op, int64_t M, const qlora_adapters_t *set
  * A row's result depends on its own adapter only: values of others that are not finite stay
  * with the rows that name them.
  * ws: qlora_adapters_workspace_size(QLORA_OP_FWD) bytes.
- * Errors: INVALID_ARG (null or misaligned pointer, M outside [1, 2^23], dropout outside [0, 1)
- * or so near 1 that t would be 65536), BAD_SHAPE (also where the weight's shape is not the
+ * Errors: INVALID_ARG (null or misaligned pointer, Y overlapping X, M outside [1, 2^23], dropout
+ * outside [0, 1) or so near 1 that t would be 65536), BAD_SHAPE (also where the weight's shape is not the
  * set's), UNSUPPORTED, WORKSPACE, HIP. */
 int qlora_adapters_fwd(const qlora_nf4dq_t *Wq, const qlora_adapters_t *set, const uint16_t *X, int64_t M,
                        const int32_t *ids, float dropout, const uint64_t *rng, uint16_t *Y, float *T_save, void *ws,
@@ -99,7 +100,8 @@ int qlora_adapters_fwd(const qlora_nf4dq_t *Wq, const qlora_adapters_t *set, con
  * adapter).  dY [M, d_out], X [M, d_in], dX: device BF16, 16-byte aligned.  T_saved: the
  * forward's, or NULL to recompute it.  dropout and rng as in the forward.
  * ws: qlora_adapters_workspace_size(QLORA_OP_BWD) bytes.
- * Errors: as the forward, INVALID_ARG also for a set without gradients. */
+ * Errors: as the forward, INVALID_ARG also for a set without gradients and for dX overlapping X
+ * or dY. */
 int qlora_adapters_bwd(const qlora_nf4dq_t *Wq, const qlora_adapters_t *set, const uint16_t *X, const uint16_t *dY,
                        int64_t M, const int32_t *ids, float dropout, const uint64_t *rng, const float *T_saved,
                        uint16_t *dX, void *ws, size_t ws_bytes, hipStream_t stream);

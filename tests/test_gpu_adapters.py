@@ -123,6 +123,29 @@ SHAPES = [  # M, d_out, d_in, ranks, ids
     (1100, 336, 448, [16, 16, 4], "runs"),
     (777, 2064, 128, [8, 8], "base"),
     (40, 96, 128, [8, 16], "base"),
+    # one launch for T and the stream: one and two tiles of 16 ranks
+    (1, 48, 4160, [16, 3], "tokens"),
+    (1, 272, 192, [32], "none"),
+    (1, 4096, 1088, [19, 7], "tokens"),
+    (2, 528, 1088, [3, 16], "tokens"),
+    (2, 8208, 128, [8], "none"),
+    # wide weights: four wavefronts to a workgroup, for each number of row tiles
+    (1, 8208, 192, [128, 40], "tokens"),
+    (16, 8208, 576, [16, 5], "tokens"),
+    (32, 8224, 192, [8] * 20, "tokens"),
+    (47, 8208, 320, [16, 24], "tokens"),
+    (50, 8208, 192, [7, 16], "tokens"),
+    (95, 8208, 128, [16, 8], "runs"),
+    (127, 8240, 192, [48, 9, 16], "tokens"),
+    # several row tiles of a narrow weight
+    (96, 112, 1344, [16, 16], "tokens"),
+    (113, 64, 4160, [24, 128], "tokens"),
+    # products by the decoded copy, forward and backward
+    (520, 6672, 128, [16, 20], "tokens"),
+    (513, 128, 6720, [8, 64], "runs"),
+    # the gradients' rows in two and four parts
+    (2100, 80, 128, [16, 40], "runs"),
+    (4111, 48, 64, [128], "none"),
 ]
 
 
@@ -292,6 +315,37 @@ def test_two_streams_at_once(gpu_lib):
         for o in outs[k]:
             assert torch.equal(o[0], want[k][0]) and torch.equal(o[1], want[k][1])
         assert all(map(torch.equal, want[k][2:], c["set"].dA + c["set"].dB))
+
+
+def test_two_graphs_on_one_workspace(gpu_lib):
+    """Two captured calls of different shapes that share a workspace, replayed in turn on one stream."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    cases = [make(i, *SHAPES[i]) for i in (13, 6)]
+    ws = Q.new_workspace(max(c["set"].workspace_size(op, c["X"].shape[0]) for c in cases for op in (Q.OP_FWD, Q.OP_BWD)))
+
+    def step(c):
+        Y = Q.linear_adapters_fwd(c["q"], c["set"], c["X"], c["ids"], ws=ws)
+        return [Y, Q.linear_adapters_bwd(c["q"], c["set"], c["X"], c["dY"], c["ids"], ws=ws), *c["set"].dA, *c["set"].dB]
+
+    want = [[t.clone() for t in step(c)] for c in cases]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    with torch.cuda.stream(side):
+        for c in cases:
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=side):
+                outs.append(step(c))
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert all(map(torch.equal, o, w))
 
 
 def test_set_of_more_adapters_than_one_launch_describes(gpu_lib):
