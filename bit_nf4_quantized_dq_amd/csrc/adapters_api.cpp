@@ -64,7 +64,7 @@ AdapterRows rows_of(const qlora_adapters_t* set, const int32_t* ids, int64_t M) 
 // read) go through the decoded copy.
 bool stream_path(int64_t M, int dq) { return M <= kStreamMaxRows && dq == QLORA_DQ_E4M3; }
 // The product over the codes, for the rows between few and many.
-bool codes_path(int64_t M, int64_t F, int dq) { return dq == QLORA_DQ_E4M3 && adapter_gemm_fits(M, F); }
+bool codes_path(int64_t M, int64_t F, int64_t Kr, int dq) { return dq == QLORA_DQ_E4M3 && adapter_gemm_fits(M, F, Kr); }
 
 // ---- workspaces: the counter head, then T and G, then what the steps need in turn
 struct Layout {
@@ -88,8 +88,8 @@ Layout layout(bool bwd, int64_t M, const qlora_adapters_t* set, int dq) {
     w.spart = take(t_split > 1 ? t_bytes * t_split : 0);
     if (bwd) w.gspart = take(g_split > 1 ? t_bytes * g_split : 0);
     const int64_t F = bwd ? K : N, Kr = bwd ? N : K;
-    if (!codes_path(M, F, dq)) w.wcopy = take(2 * (size_t)N * K);
-    w.gsplit = codes_path(M, F, dq) ? adapter_gemm_split(M, F, Kr) : gemm_nt_ksplit(F, M, Kr);
+    if (!codes_path(M, F, Kr, dq)) w.wcopy = take(2 * (size_t)N * K);
+    w.gsplit = codes_path(M, F, Kr, dq) ? adapter_gemm_split(M, F, Kr) : gemm_nt_ksplit(F, M, Kr);
     w.gpart = take(w.gsplit > 1 ? sizeof(float) * (size_t)w.gsplit * M * F : 0);
   }
   if (bwd) w.grads = take(adapter_grad_plan(M, N, K, set->count, set->max_rank).part_bytes);
@@ -184,7 +184,7 @@ int qlora_adapters_fwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
                                             stream_forms_t(M, N, K, rows.width) ? T_save : T, Y, tab, stream));
   const AdapterHead head{rows, T, 0, 1.f, DropMask{}};
   float* gpart = reinterpret_cast<float*>(base + L.gpart);
-  if (codes_path(M, N, dq)) {
+  if (codes_path(M, N, K, dq)) {
     if (launch_shrink_a(rows, X, K, drop, T, part, counters, nullptr, tab, stream) != hipSuccess) return QLORA_ERR_HIP;
     return hip_status(launch_adapter_gemm(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, X, M, head, Y, gpart, L.gsplit, tab,
                                           QLORA_K_GEMM_FWD, stream));
@@ -224,7 +224,7 @@ int qlora_adapters_bwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   float* g_part = reinterpret_cast<float*>(base + L.gspart);
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(Wq->codes);
   uint16_t* wcopy = reinterpret_cast<uint16_t*>(base + L.wcopy);
-  const bool copied = dX && !codes_path(M, K, dq);
+  const bool copied = dX && !codes_path(M, K, N, dq);
   const bool beside = copied && dq == QLORA_DQ_E4M3;  // the decode joins G's launch
   const ShrinkDecode dec = decode_args(Wq, wcopy);
   const float* T = T_saved;

@@ -5,17 +5,22 @@
 //   forward : Y[m][n]  = sum_k w_hat[n][k] X[m][k]    + adapters     features n, reduction k
 //   dX      : dX[m][k] = sum_n w_hat[n][k] dY[m][n]   + adapters     features k, reduction n
 //
-// Tile: 128 features x 128 tokens per workgroup of four wavefronts (2 x 2, each 64 features x 64
-// tokens of MFMA 32x32x16), reduction step 64, two workgroups to a compute unit, so that one's
-// decode (vector units) meets the other's products (matrix units).  A step decodes 128 blocks of 64
-// weights, two threads to a block and its level table.  Few tiles split the reduction over several
-// workgroups (FP32 partials, added in order by launch_sum_parts).
+// Tile: 128 features x 128 TJ tokens per workgroup of eight wavefronts (2 x 4, each 64 features x
+// 32 TJ tokens of MFMA 32x32x16), reduction step 64.  A step decodes 128 blocks of 64 weights, two
+// threads to a block and its level table, so four wavefronts decode in one step and the other
+// four in the next: each SIMD holds one of either kind, and one's decode (vector units) meets the
+// other's products (matrix units).  A step of 128 x 256 takes 0.95 us, as long as the GEMM over a
+// decoded copy takes for its share: both read 32 KB of activations a step through the L2.  (Four
+// wavefronts that all decode, two workgroups to a compute unit: 1.1 us for 128 x 128; 1024 rows of
+// 4096 x 4096 backward 96 us, here 76.)  Few tiles split the reduction over several workgroups (FP32
+// partials, added in order by launch_sum_parts).
 //
-// Pipeline, as in gemm.hip: step kb issues the activations' direct loads to LDS for step kb + 2
-// (ring of three) and the codes' loads for it (registers), multiplies step kb, decodes step kb + 1
-// into the other weight buffer, waits for the activations of step kb + 1 and passes one barrier.
-// Every buffer is a __shared__ array of its own, known at compile time in a loop unrolled six
-// times, so that the compiler waits only for the loads an access needs.
+// Pipeline: step kb issues the activations' direct loads to LDS for step kb + 2 (ring of three); half
+// of the wavefronts load their codes for it (registers) and the other half decodes step kb + 1
+// into the other weight buffer while both multiply step kb; then the activations of step kb + 1 are
+// waited for and one barrier passed.  Every buffer is a __shared__ array of its own, known at
+// compile time in a loop unrolled six times, so that the compiler waits only for the loads an
+// access needs.
 //
 // LDS.  Activations and the forward's weight: rows of 128 bytes, 16-byte chunk c of row r at c ^
 // (r / 2 % 8).  The transposed weight: rows n of 128 features in 64-byte units, unit u at u ^ (n % 4),
@@ -26,11 +31,11 @@
 namespace qlora {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int BF = 128;   // features per workgroup
 constexpr int BK = 64;    // reduction step
-constexpr int BM = 128;   // tokens per workgroup
-constexpr int TI = 2, TJ = 2;  // 32 x 32 tiles per wavefront
+constexpr int TI = 2;     // 32 x 32 tiles per wavefront: TI of features, TJ of tokens
+template <int TJ> constexpr int kTokens = 128 * TJ;  // tokens per workgroup
 typedef __attribute__((address_space(3))) void lds_void;
 
 // An offset past every operand (tiles are below 2^31 bytes, the scalar offsets of steps below 2^24):
@@ -48,7 +53,7 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 __shared__ uint4 s_w0[1024], s_w1[1024];              // decoded weights, 16 KB each
-__shared__ uint4 s_x0[1024], s_x1[1024], s_x2[1024];  // activations
+__shared__ uint4 s_x0[2048], s_x1[2048], s_x2[2048];  // activations, 32 KB each
 template <int I> __device__ __forceinline__ uint4* wbuf() { return I == 0 ? s_w0 : s_w1; }
 template <int I> __device__ __forceinline__ uint4* xbuf() { return I == 0 ? s_x0 : (I == 1 ? s_x1 : s_x2); }
 
@@ -64,15 +69,16 @@ struct MidArgs {
   uint32_t kb_per;
 };
 
-// Activation ring: 128 rows from m0.  Wavefront w fills rows 32 w .. +32 of a slot, eight rows
+// Activation ring: 128 TJ rows from m0.  Wavefront w fills rows 16 TJ w .. of a slot, eight rows
 // of 128 bytes a load; lane p writes slot chunk p & 7 and fetches the chunk that belongs there.
+template <int TJ>
 struct Ring {
   static constexpr int kLoads = 2 * TJ;
   rsrc_t r;
   uint32_t base[kLoads], col[kLoads], Kr;
   int wave;
   __device__ __forceinline__ void init(const MidArgs& a, int64_t m0, int w, int lane) {
-    const int64_t rows = a.M - m0 < BM ? a.M - m0 : BM;
+    const int64_t rows = a.M - m0 < kTokens<TJ> ? a.M - m0 : kTokens<TJ>;
     r = make_rsrc(a.X + m0 * a.Kr, rows * a.Kr * 2);
     Kr = (uint32_t)a.Kr;
     wave = w;
@@ -187,105 +193,124 @@ __device__ __forceinline__ bf16x8_t w_operand(const uint4* __restrict__ w, int u
   return r;
 }
 
-template <bool WT, int XS, int WB>
-__device__ __forceinline__ void mid_step(const Decoder<WT>& dec, const Ring& ring, const Nf4Tables& tab, uint32_t kb,
-                                         uint32_t last, typename Decoder<WT>::Regs& cur, typename Decoder<WT>::Regs& nxt,
-                                         int wf, int wm, int lane, f32x16_t (&acc)[TI][TJ]) {
+// Step kb of a wavefront.  The group whose turn it is (DEC) decodes step kb + 1 from R; the other
+// loads R for step kb + 2.  `live`: the wavefront has tokens (uniform).
+template <bool WT, int TJ, bool DEC, int XS, int WB>
+__device__ __forceinline__ void mid_step(const Decoder<WT>& dec, const Ring<TJ>& ring, const Nf4Tables& tab, uint32_t kb,
+                                         uint32_t last, typename Decoder<WT>::Regs& R, int wf, int wm, int lane, bool live,
+                                         f32x16_t (&acc)[TI][TJ]) {
   // loads past the range go into buffers that nothing reads
   const uint32_t k2 = kb + 2 < last ? kb + 2 : last;
-  dec.load(nxt, k2);
+  if (!DEC) dec.load(R, k2);
   ring.template issue<(XS + 2) % 3>(k2);
   const int l32 = lane & 31, h32 = lane >> 5;
   Lut L;
-  dec.table(cur, tab, L);
-  bf16x8_t x[2][TI], y[2][TJ];
-  const auto read = [&](int ks) {
+  if (DEC) dec.table(R, tab, L);
+  if (live) {
+    bf16x8_t x[2][TI], y[2][TJ];
+    const auto read = [&](int ks) {
 #pragma unroll
-    for (int i = 0; i < TI; ++i) x[ks & 1][i] = w_operand<WT>(wbuf<WB>(), wf / 32 + i, ks, lane);
+      for (int i = 0; i < TI; ++i) x[ks & 1][i] = w_operand<WT>(wbuf<WB>(), wf / 32 + i, ks, lane);
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      const int row = wm + 32 * j + l32;
-      y[ks & 1][j] = as_bf16x8(xbuf<XS>()[8 * row + ((2 * ks + h32) ^ ((row >> 1) & 7))]);
+      for (int j = 0; j < TJ; ++j) {
+        const int row = wm + 32 * j + l32;
+        y[ks & 1][j] = as_bf16x8(xbuf<XS>()[8 * row + ((2 * ks + h32) ^ ((row >> 1) & 7))]);
+      }
+    };
+    read(0);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      if (ks < 3) read(ks + 1);
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = mfma32(x[ks & 1][i], y[ks & 1][j], acc[i][j]);
+      if (DEC) dec.store(wbuf<WB ^ 1>(), R, L, ks);
     }
-  };
-  read(0);
+    // operands one 16-wide step ahead; the decode's vector instructions between the products, each of
+    // which holds the matrix unit for 32 clocks
+    constexpr int kReads = WT ? 2 * TI + TJ : TI + TJ;
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * kReads, 0);
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    if (ks < 3) read(ks + 1);
+    for (int ks = 0; ks < 4; ++ks) {
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) acc[i][j] = mfma32(x[ks & 1][i], y[ks & 1][j], acc[i][j]);
-    dec.store(wbuf<WB ^ 1>(), cur, L, ks);
-  }
-  // operands one 16-wide step ahead; the decode's vector instructions between the products, each of
-  // which holds the matrix unit for 32 clocks
-  constexpr int kReads = WT ? 2 * TI + TJ : TI + TJ;
-  __builtin_amdgcn_sched_group_barrier(0x100, 2 * kReads, 0);
-#pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-#pragma unroll
-    for (int q = 0; q < TI * TJ; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, 40 / (TI * TJ), 0);
+      for (int q = 0; q < TI * TJ; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (DEC) __builtin_amdgcn_sched_group_barrier(0x002, 40 / (TI * TJ), 0);
+      }
+      if (ks < 2) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
     }
-    if (ks < 2) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+  } else if (DEC) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) dec.store(wbuf<WB ^ 1>(), R, L, c);
   }
-  wait_vm<Ring::kLoads + Decoder<WT>::kLoads>();  // the activations of step kb + 1 have landed
+  // the activations of step kb + 1 have landed
+  wait_vm<DEC ? Ring<TJ>::kLoads : Ring<TJ>::kLoads + Decoder<WT>::kLoads>();
   lds_barrier();
 }
 
-template <bool WT>
+// The steps of the wavefronts of group G: those with kb - kb0 of G's parity load, the others decode.
+template <bool WT, int TJ, int G>
+__device__ __forceinline__ void mid_loop(const Decoder<WT>& dec, const Ring<TJ>& ring, const Nf4Tables& tab, uint32_t kb0,
+                                         uint32_t kb1, uint32_t nk, typename Decoder<WT>::Regs& R, int wf, int wm, int lane,
+                                         bool live, f32x16_t (&acc)[TI][TJ]) {
+  for (uint32_t kb = kb0; kb < kb1; kb += 6) {
+    mid_step<WT, TJ, G == 1, 0, 0>(dec, ring, tab, kb + 0, nk, R, wf, wm, lane, live, acc);
+    if (kb + 1 >= kb1) break;
+    mid_step<WT, TJ, G == 0, 1, 1>(dec, ring, tab, kb + 1, nk, R, wf, wm, lane, live, acc);
+    if (kb + 2 >= kb1) break;
+    mid_step<WT, TJ, G == 1, 2, 0>(dec, ring, tab, kb + 2, nk, R, wf, wm, lane, live, acc);
+    if (kb + 3 >= kb1) break;
+    mid_step<WT, TJ, G == 0, 0, 1>(dec, ring, tab, kb + 3, nk, R, wf, wm, lane, live, acc);
+    if (kb + 4 >= kb1) break;
+    mid_step<WT, TJ, G == 1, 1, 0>(dec, ring, tab, kb + 4, nk, R, wf, wm, lane, live, acc);
+    if (kb + 5 >= kb1) break;
+    mid_step<WT, TJ, G == 0, 2, 1>(dec, ring, tab, kb + 5, nk, R, wf, wm, lane, live, acc);
+  }
+}
+
+template <bool WT, int TJ>
 __global__ __launch_bounds__(kThreads, 2) void k_adapter_gemm(MidArgs a, Nf4Tables tab) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wf = (wave & 1) * 64, wm = (wave >> 1) * 32 * TJ;
-  const int64_t f0 = (int64_t)blockIdx.x * BF, m0 = (int64_t)blockIdx.y * BM;
+  const int64_t f0 = (int64_t)blockIdx.x * BF, m0 = (int64_t)blockIdx.y * kTokens<TJ>;
   const uint32_t nk = (uint32_t)((a.Kr + BK - 1) / BK);
   const uint32_t kb0 = blockIdx.z * a.kb_per, kb1 = kb0 + a.kb_per < nk ? kb0 + a.kb_per : nk;
-  Ring ring;
+  Ring<TJ> ring;
   ring.init(a, m0, wave, lane);
   Decoder<WT> dec;
-  dec.init(a, f0, tid);
-  typename Decoder<WT>::Regs r0, r1;
+  dec.init(a, f0, tid & 255);
+  // group 0 decodes the first step here, group 1 the second in the loop
+  const int group = wave >> 2;
+  const bool live = m0 + wm < a.M;
+  typename Decoder<WT>::Regs R;
   ring.template issue<0>(kb0);
-  dec.load(r0, kb0);
+  dec.load(R, kb0 + group < nk ? kb0 + group : nk);
   ring.template issue<1>(kb0 + 1 < nk ? kb0 + 1 : nk);
-  dec.load(r1, kb0 + 1 < nk ? kb0 + 1 : nk);
   f32x16_t acc[TI][TJ];
 #pragma unroll
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x16_t{};
-  // (s_w1 is free until the barrier)
-  const bool any = adapter_rows<WT>(a.head, a.F, f0 + wf, m0 + wm, lane, reinterpret_cast<char*>(s_w1) + wave * 4096,
-                                    blockIdx.z, gridDim.z, acc);
+  // (s_x2 is free until the barrier)
+  const bool any = live && adapter_rows<WT>(a.head, a.F, f0 + wf, m0 + wm, lane, reinterpret_cast<char*>(s_x2) + wave * 4096,
+                                            blockIdx.z, gridDim.z, acc);
   if (WT && any && a.head.drop.threshold) drop_acc(a.head.drop, a.F, f0 + wf, m0 + wm, lane & 31, lane >> 5, acc);
-  {
+  if (group == 0) {
     Lut L;
-    dec.table(r0, tab, L);
+    dec.table(R, tab, L);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) dec.store(s_w0, r0, L, c);
+    for (int c = 0; c < 4; ++c) dec.store(s_w0, R, L, c);
   }
   wait_vm<0>();
   lds_barrier();
-  for (uint32_t kb = kb0; kb < kb1; kb += 6) {
-    mid_step<WT, 0, 0>(dec, ring, tab, kb + 0, nk, r1, r0, wf, wm, lane, acc);
-    if (kb + 1 >= kb1) break;
-    mid_step<WT, 1, 1>(dec, ring, tab, kb + 1, nk, r0, r1, wf, wm, lane, acc);
-    if (kb + 2 >= kb1) break;
-    mid_step<WT, 2, 0>(dec, ring, tab, kb + 2, nk, r1, r0, wf, wm, lane, acc);
-    if (kb + 3 >= kb1) break;
-    mid_step<WT, 0, 1>(dec, ring, tab, kb + 3, nk, r0, r1, wf, wm, lane, acc);
-    if (kb + 4 >= kb1) break;
-    mid_step<WT, 1, 0>(dec, ring, tab, kb + 4, nk, r1, r0, wf, wm, lane, acc);
-    if (kb + 5 >= kb1) break;
-    mid_step<WT, 2, 1>(dec, ring, tab, kb + 5, nk, r0, r1, wf, wm, lane, acc);
-  }
+  if (group == 0) mid_loop<WT, TJ, 0>(dec, ring, tab, kb0, kb1, nk, R, wf, wm, lane, live, acc);
+  else mid_loop<WT, TJ, 1>(dec, ring, tab, kb0, kb1, nk, R, wf, wm, lane, live, acc);
   wait_vm<0>();   // the loads issued past the range have landed
   lds_barrier();  // every wavefront is done with the buffers, which now stage the result
   // 32 tokens x 64 features of FP32 at a time (8 KB of the wavefront's own): 16-byte unit u of row m at
   // u ^ (m % 16); read back so that each row leaves in whole
-  uint4* stage = wave == 0 ? s_w0 : (wave == 1 ? s_w1 : (wave == 2 ? s_x0 : s_x1));
+  uint4* stage = (wave < 4 ? s_x0 : s_x1) + (wave & 3) * 512;
   const int l32 = lane & 31, h32 = lane >> 5;
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
@@ -325,21 +350,25 @@ __global__ __launch_bounds__(kThreads, 2) void k_adapter_gemm(MidArgs a, Nf4Tabl
   }
 }
 
-int64_t mid_tiles(int64_t M, int64_t F) { return ((F + BF - 1) / BF) * ((M + BM - 1) / BM); }
+int64_t mid_tiles(int64_t M, int64_t F, int tj) { return ((F + BF - 1) / BF) * ((M + 128 * tj - 1) / (128 * tj)); }
+
+// Tiles of 256 tokens (TJ = 2) read the weight and the activations less often; of 128 where there are no
+// more rows, and for short reductions, whose time goes into the tiles' start and end (555 rows over
+// 1040 to 4096: 53 us in tiles of 128 and 58 in tiles of 256; 1024 rows over 4096 to 4096: 87 and 76).
+int mid_tj(int64_t M, int64_t F, int64_t Kr) { return M <= 128 || (Kr < 32 * BK && mid_tiles(M, F, 1) <= 256) ? 1 : 2; }
 
 }  // namespace
 
-// Beyond two rounds of workgroups, the weight decoded once and the larger tiles of the GEMM over
-// the copy are faster (4096 x 4096: 1024 rows 72 us here and 74 there, 2048 rows 118 and 103).
-bool adapter_gemm_fits(int64_t M, int64_t F) { return mid_tiles(M, F) <= 256; }
+// From about one tile for each compute unit on, the weight decoded once and the larger tiles of the
+// GEMM over the copy are faster (400 rows of 14336 x 4096, 224 tiles: 85 us here and 103 there;
+// 8192 rows of 1024 x 4096, 256 tiles: 101 and 95; 1024 rows of 14336 x 4096, 448: 157 and 136).
+bool adapter_gemm_fits(int64_t M, int64_t F, int64_t Kr) { return M <= 128 || mid_tj(M, F, Kr) == 1 || mid_tiles(M, F, 2) <= 224; }
 
 int32_t adapter_gemm_split(int64_t M, int64_t F, int64_t Kr) {
-  // two workgroups to a compute unit; not for more than 128 tiles, which gain less than adding the
-  // partials costs (160 tiles of 17 steps 33 us in three splits, 31 whole; 128 tiles of 64 steps 41
-  // us in four, 45 in two)
-  const int64_t nk = (Kr + BK - 1) / BK, tiles = mid_tiles(M, F);
-  const int64_t split = tiles > 128 ? 1 : std::min<int64_t>(512 / tiles, nk / 4);
-  return (int32_t)std::max<int64_t>(1, split);
+  // a workgroup to a compute unit, and four steps at least to a split (1999 rows of 1024 x 4096: 80 us
+  // whole, 58 in two, 50 in four, 62 in eight)
+  const int64_t nk = (Kr + BK - 1) / BK, tiles = mid_tiles(M, F, mid_tj(M, F, Kr));
+  return (int32_t)std::max<int64_t>(1, std::min<int64_t>(256 / tiles, nk / 4));
 }
 
 hipError_t launch_adapter_gemm(const uint32_t* codes, const uint8_t* code8, const float* c2s, const float* mu, int64_t N,
@@ -350,11 +379,13 @@ hipError_t launch_adapter_gemm(const uint32_t* codes, const uint8_t* code8, cons
   const uint32_t nk = (uint32_t)((Kr + BK - 1) / BK), kb_per = (nk + split - 1) / split;
   const uint32_t splits = (nk + kb_per - 1) / kb_per;  // no split is empty
   const MidArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, M, F, Kr, head, C, splits > 1 ? part : nullptr, kb_per};
-  const dim3 grid((unsigned)((F + BF - 1) / BF), (unsigned)((M + BM - 1) / BM), splits);
+  const int tj = mid_tj(M, F, Kr);
+  const dim3 grid((unsigned)((F + BF - 1) / BF), (unsigned)((M + 128 * tj - 1) / (128 * tj)), splits);
   {
     LaunchTimer t(kernel_id, st);
     const auto go = [&](auto kernel) { hipExtLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, t.start, t.stop, 0, a, tab); };
-    head.transposed ? go(k_adapter_gemm<true>) : go(k_adapter_gemm<false>);
+    if (tj == 1) head.transposed ? go(k_adapter_gemm<true, 1>) : go(k_adapter_gemm<false, 1>);
+    else head.transposed ? go(k_adapter_gemm<true, 2>) : go(k_adapter_gemm<false, 2>);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits <= 1) return e;

@@ -88,7 +88,7 @@ hipError_t launch_gemm_nt_adapters(const uint16_t* A, int64_t F, const uint16_t*
 
 // ---- a moderate number of rows: the same product over the codes, decoded on chip (adapters_gemm.hip,
 // E4M3 constants), where adapter_gemm_fits(); part: FP32 [split][M][F] when split > 1.
-bool adapter_gemm_fits(int64_t M, int64_t F);
+bool adapter_gemm_fits(int64_t M, int64_t F, int64_t Kr);
 int32_t adapter_gemm_split(int64_t M, int64_t F, int64_t Kr);
 hipError_t launch_adapter_gemm(const uint32_t* codes, const uint8_t* code8, const float* c2s, const float* mu, int64_t N,
                                int64_t K, const uint16_t* X, int64_t M, const AdapterHead& head, uint16_t* C, float* part,

@@ -140,9 +140,13 @@ SHAPES = [  # M, d_out, d_in, ranks, ids
     # several row tiles of a narrow weight
     (96, 112, 1344, [16, 16], "tokens"),
     (113, 64, 4160, [24, 128], "tokens"),
-    # products by the decoded copy, forward and backward
+    # products over the codes in tiles of 256 rows, forward and backward, and by the decoded copy
     (520, 6672, 128, [16, 20], "tokens"),
     (513, 128, 6720, [8, 64], "runs"),
+    (300, 2064, 192, [16, 24, 7], "tokens"),
+    (447, 208, 2112, [9, 40], "runs"),
+    (1030, 5776, 64, [16, 20], "tokens"),
+    (1030, 64, 5824, [8, 64], "runs"),
     # the gradients' rows in two and four parts
     (2100, 80, 128, [16, 40], "runs"),
     (4111, 48, 64, [128], "none"),
