@@ -305,9 +305,10 @@ struct StreamArgs {
   const uint16_t* X;
   AdapterRows rows;
   DropMask drop;
-  float* T;  // read; where a workgroup forms T itself, written (null: not wanted)
+  float* T;  // read; where the stream forms T itself, written (null: not wanted)
   uint16_t* Y;
   int32_t lists;
+  uint64_t* words;  // [workgroup][row][width], zero before and after
 };
 
 // T for the stream: 16 rows, 16 ranks and every `lists`-th of the rows' distinct adapters, over the
@@ -411,6 +412,74 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_t(StreamArgs a) {
   *reinterpret_cast<f32x4_t*>(a.T + (int64_t)(m0 + l16) * width + j) = out;
 }
 
+// ---- T of a row or a few, formed by the stream's own workgroups.  Workgroup j takes element j of T
+// [M][width] (and every gridDim.x-th from there), a dot product of two rows of K, and posts it, with a
+// bit that marks it as there, to a word of its own in each workgroup's block, in the workspace's
+// head.  A workgroup reads its words after its share of the weight, waits for those that are still
+// on their way, and clears them, so the head is zero after every call.  A workgroup posts before
+// it waits, and those that post start first, so each wait ends.  (A launch for T before the stream
+// costs 2 to 4 us; T formed anew by every workgroup, which reads all of A from the L2 in each, took
+// 12.2 us for one row of 64 ranks at 4096 x 4096, here 9.8.)
+constexpr uint64_t kPosted = uint64_t(1) << 32;  // beside the value's 32 bits
+constexpr int kMostPolls = 1 << 20;
+constexpr int64_t kPostedWords = 32768;
+
+template <int W>
+__device__ __forceinline__ void post_t(const StreamArgs& a, int tid) {
+  __shared__ float dots[W];
+  const uint32_t width = (uint32_t)a.rows.width, slots = (uint32_t)a.rows.M * width, groups = gridDim.x;
+  if (blockIdx.x >= slots) return;
+  const uint32_t chunks = (uint32_t)(a.K / 8), t2 = threshold_halves(a.drop.threshold);
+  const bool drop = a.drop.threshold != 0;
+  RngKey key{};
+  if (drop) key = load_rng(a.drop.rng);
+  for (uint32_t slot = blockIdx.x; slot < slots; slot += groups) {
+    const uint32_t m = slot / width, j = slot - m * width;
+    const int one = adapter_of(a.rows, m);
+    const bool has = one >= 0 && (int)j < a.rows.table[one].r;
+    float t = 0.f;
+    if (has) {
+      const uint4* p = reinterpret_cast<const uint4*>(a.rows.table[one].A + (int64_t)j * a.K);
+      const uint4* x = reinterpret_cast<const uint4*>(a.X + (int64_t)m * a.K);
+      float sum = 0.f;
+      for (uint32_t c = (uint32_t)tid; c < chunks; c += 64 * W) {
+        const uint4 u = p[c];
+        uint4 v = x[c];
+        if (drop) v = drop8(v, key, (uint64_t)m * chunks + c, t2);
+        const uint32_t pu[4] = {u.x, u.y, u.z, u.w}, pv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum = fmaf(bf16lo_to_f32(pu[i]), bf16lo_to_f32(pv[i]), sum);
+          sum = fmaf(bf16hi_to_f32(pu[i]), bf16hi_to_f32(pv[i]), sum);
+        }
+      }
+#pragma unroll
+      for (int by = 32; by; by >>= 1) sum += __shfl_xor(sum, by);
+      if ((tid & 63) == 0) dots[tid >> 6] = sum;
+      __syncthreads();
+      t = dots[0];
+#pragma unroll
+      for (int w = 1; w < W; ++w) t += dots[w];
+      t *= a.drop.scale;
+      const uint64_t word = kPosted | __float_as_uint(t);
+      for (uint32_t to = (uint32_t)tid; to < groups; to += 64 * W)
+        __hip_atomic_store(a.words + (uint64_t)to * slots + slot, word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+      __syncthreads();  // dots is free again
+    }
+    if (a.T && tid == 0) a.T[slot] = t;
+  }
+}
+
+// acc += B's 16 rows times v (eight ranks for each lane's row of X, as hi and lo BF16 parts), where
+// `has`: the products of other rows are not taken.
+__device__ __forceinline__ void add_term(f32x4_t& acc, const uint4& w, const float (&v)[8], bool has) {
+  uint4 hi, lo;
+  split_bf16(v, hi, lo);
+  const f32x4_t p = mfma16x16x32(as_bf16x8(w), as_bf16x8(lo), mfma16x16x32(as_bf16x8(w), as_bf16x8(hi), f32x4_t{0.f, 0.f, 0.f, 0.f}));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] += has ? p[i] : 0.f;
+}
+
 // 16 weight rows over the whole reduction.  A wavefront takes groups of four 64-weight blocks;
 // lane (l16, g) decodes block 4 group + g of row l16 (32 bytes of codes, one level table scaled by
 // the block's constant: exactly w_hat).  The four lanes of a row then exchange their words (a 4 x 4
@@ -421,18 +490,17 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_t(StreamArgs a) {
 // have neighbouring lanes in 16 rows: 37 rows at 14336 x 4096 91 us in the blocks' order, 56 in
 // 64-byte pieces.)
 //
-// The adapters' term is more of the same sum.  E == 0: T is there; the wavefronts deal the distinct
-// adapters of all rows among themselves, and each multiplies its ones' 16 rows of B with T (hi and
-// lo BF16 parts) into its accumulators.  E > 0 (a row or two, up to E tiles of 16 ranks in all):
-// every workgroup forms T itself, A's rows passing beside X's as E more tiles.  W: wavefronts; four
-// where there are more than two workgroups of eight to a compute unit (longer runs of blocks for
-// each: 37 rows at 14336 x 4096 41 -> 39 us, 64 rows 42 -> 36).
-template <int W, int MT, int E, int PD, bool WHOLE>
-__global__ __launch_bounds__(64 * W, E == 0 && MT <= 3 ? 4 : 2) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
-  static_assert(E == 0 || MT == 1, "T is formed for one tile of rows");
-  constexpr int XT = MT + E;  // tiles that pass through LDS
-  __shared__ uint4 smem[W * XT * 128];  // a block of them for each wavefront; then the sums
-  f32x4_t(*red)[XT][64] = reinterpret_cast<f32x4_t(*)[XT][64]>(smem);
+// The adapters' term is more of the same sum.  Without POST, T is there; the wavefronts deal the
+// distinct adapters of all rows among themselves, and each multiplies its ones' 16 rows of B with T
+// (hi and lo BF16 parts) into its accumulators.  With POST (a row or a few), workgroups form T while
+// they stream, one element each, and post it to every workgroup (below); the wavefronts deal the rows
+// among themselves.  W: wavefronts; four where there are more than two workgroups of eight to a
+// compute unit (longer runs of blocks for each: 37 rows at 14336 x 4096 41 -> 39 us, 64 rows 42 -> 36).
+template <int W, int MT, bool POST, int PD, bool WHOLE>
+__global__ __launch_bounds__(64 * W, !POST && MT <= 3 ? 4 : 2) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
+  static_assert(!POST || MT == 1, "few rows");
+  __shared__ uint4 smem[W * MT * 128];  // a wavefront's tiles of X; then the sums
+  f32x4_t(*red)[MT][64] = reinterpret_cast<f32x4_t(*)[MT][64]>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int64_t K = a.K, N = a.N, row0 = (int64_t)blockIdx.x * kStreamRows;
@@ -464,12 +532,12 @@ __global__ __launch_bounds__(64 * W, E == 0 && MT <= 3 ? 4 : 2) void k_adapter_s
   for (int t = 0; t < MT; ++t) id[t] = adapter_of(a.rows, 16 * t + l16);
   Codes cur = load(wave), next = load(wave + W);
   const float mu = a.mu[0];
-  f32x4_t acc[XT];
+  f32x4_t acc[MT];
 #pragma unroll
-  for (int t = 0; t < XT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  uint4* xs = smem + wave * XT * 128;
-  uint4 xr[PD][XT][2];
-  const auto load_x = [&](uint4 (&x)[XT][2], uint32_t blk) {
+  for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  uint4* xs = smem + wave * MT * 128;
+  uint4 xr[PD][MT][2];
+  const auto load_x = [&](uint4 (&x)[MT][2], uint32_t blk) {
     // lane p takes chunk (p & 7) ^ (row / 2 % 8) of rows p >> 3 and 8 + (p >> 3) of a tile
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -482,10 +550,11 @@ __global__ __launch_bounds__(64 * W, E == 0 && MT <= 3 ? 4 : 2) void k_adapter_s
 #pragma unroll
   for (int d = 0; d < PD; ++d) load_x(xr[d], 4 * wave + d);
 
-  // E == 0: this wavefront's adapters, every eighth distinct one, lane k holding the k-th.  E > 0: lane
-  // m holds row m's, and tile MT + e is ranks 16 (e % ranks) .. of row e / ranks.
+  if (POST) post_t<W>(a, tid);
+  // this wavefront's adapters, every W-th distinct one, lane k holding the k-th; with POST, lane m
+  // holds row m's
   int mine = 0, count = 0;
-  if (E == 0) {
+  if (!POST) {
     uint64_t pending[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) pending[t] = __ballot(id[t] >= 0);
@@ -508,53 +577,26 @@ __global__ __launch_bounds__(64 * W, E == 0 && MT <= 3 ? 4 : 2) void k_adapter_s
     mine = id[0] < 0 ? 0 : id[0];
     count = M;
   }
-  uint64_t base_a = 0, base_b = 0;
+  uint64_t base_b = 0;
   int rank_l = 0;
   float scale_l = 0.f;
   if (count) {
     const AdapterEntry* e = a.rows.table + mine;
     base_b = reinterpret_cast<uint64_t>(e->B);
-    rank_l = e->r;
+    rank_l = POST && id[0] < 0 ? 0 : e->r;
     scale_l = e->s;
-    if (E > 0) {
-      base_a = reinterpret_cast<uint64_t>(e->A);
-      if (id[0] < 0) rank_l = 0;  // no tile of its has a rank
-    }
   }
-  const int ranks = (width + 15) / 16;
-  uint64_t tile_a[E ? E : 1];  // A of tile MT + e, and the ranks that it has from the tile's first on
-  int tile_r[E ? E : 1];
-  if (E > 0) {
-    int m = 0, jt = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      tile_a[e] = readlane64(base_a, m) + (uint64_t)(16 * jt) * (uint64_t)K * 2;
-      tile_r[e] = m < M ? __builtin_amdgcn_readlane(rank_l, m) - 16 * jt : 0;
-      if (++jt == ranks) jt = 0, ++m;
-    }
-  }
-  const auto load_a = [&](uint4 (&x)[XT][2], uint32_t blk) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int have = tile_r[e] < 0 ? 0 : tile_r[e];
-      const rsrc_t ra = make_rsrc(reinterpret_cast<const void*>(tile_a[e]), have * K * 2);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((4 * i + (lane >> 4)) & 7);
-        x[MT + e][i] = bload16(ra, (j < have && blk < nb) ? (uint32_t)((j * K + 64 * (int64_t)blk + 8 * chunk) * 2) : kOOB);
-      }
-    }
+  // ranks r0 + 8 g .. +7 of B's row row0 + l16, for the adapter that lane k holds
+  const auto load_b = [&](int k, int r0) {
+    const int r = __builtin_amdgcn_readlane(rank_l, k), at = r0 + 8 * g;
+    const uint16_t* B = reinterpret_cast<const uint16_t*>(readlane64(base_b, k));
+    return WHOLE ? bload16(make_rsrc(B + row0 * r, (int64_t)kStreamRows * r * 2), at < r ? (uint32_t)((l16 * r + at) * 2) : kOOB)
+                 : load_row8(B, N * (r ? r : 1), (row0 + l16) * r, at, r);
   };
-  if (E > 0) {
-#pragma unroll
-    for (int d = 0; d < PD; ++d) load_a(xr[d], 4 * wave + d);
-  }
-  const bool drop = E > 0 && a.drop.threshold != 0;
-  RngKey key{};
-  if (drop) key = load_rng(a.drop.rng);
-  const uint32_t t2 = threshold_halves(a.drop.threshold);
+  uint4 ahead_b = make_uint4(0, 0, 0, 0);
+  if (POST && wave < M) ahead_b = load_b(wave, 0);
 
-  // ---- the base product, and T beside it
+  // ---- the base product
   for (uint32_t group = wave; group < ng; group += W) {
     const Codes c = cur;
     cur = next;
@@ -579,43 +621,33 @@ __global__ __launch_bounds__(64 * W, E == 0 && MT <= 3 ? 4 : 2) void k_adapter_s
       // the wavefront's LDS accesses run in order
       asm volatile("" ::: "memory");
 #pragma unroll
-      for (int t = 0; t < XT; ++t)
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int i = 0; i < 2; ++i) xs[128 * t + 64 * i + lane] = xr[b % PD][t][i];
       asm volatile("" ::: "memory");
       const uint32_t ahead = 4 * (group + W * ((b + PD) / 4)) + (b + PD) % 4;
       load_x(xr[b % PD], ahead);
-      if (E > 0) load_a(xr[b % PD], ahead);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int at = 8 * l16 + ((4 * h + g) ^ (l16 >> 1));
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          uint4 x = xs[128 * t + at];
-          acc[t] = mfma16x16x32(as_bf16x8(w[b + 4 * h]), as_bf16x8(x), acc[t]);
-          if (E > 0) {
-            if (drop) x = drop8(x, key, (uint64_t)l16 * (uint64_t)(K / 8) + (uint64_t)(8 * (4 * group + b) + 4 * h + g), t2);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[MT + e] = mfma16x16x32(as_bf16x8(xs[128 * (MT + e) + at]), as_bf16x8(x), acc[MT + e]);
-          }
+          acc[t] = mfma16x16x32(as_bf16x8(w[b + 4 * h]), as_bf16x8(xs[128 * t + at]), acc[t]);
         }
       }
       asm volatile("" ::: "memory");
     }
   }
 
-  if (E == 0) {
+  if (!POST) {
     // ---- this wavefront's adapters
     const rsrc_t rt = make_rsrc(a.T, (int64_t)M * width * 4);
     for (int k = 0; k < count; ++k) {
       const int one = __builtin_amdgcn_readlane(mine, k), r = __builtin_amdgcn_readlane(rank_l, k);
-      const uint16_t* B = reinterpret_cast<const uint16_t*>(readlane64(base_b, k));
       const float s = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_l), k));
-      const rsrc_t rb = make_rsrc(B + row0 * r, (int64_t)kStreamRows * r * 2);
       for (int r0 = 0; r0 < r; r0 += 32) {
         const int at = r0 + 8 * g;
-        const uint4 w = WHOLE ? bload16(rb, at < r ? (uint32_t)((l16 * r + at) * 2) : kOOB)
-                              : load_row8(B, N * r, (row0 + l16) * r, at, r);
+        const uint4 w = load_b(k, r0);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           const bool has = id[t] == one;
@@ -625,85 +657,57 @@ __global__ __launch_bounds__(64 * W, E == 0 && MT <= 3 ? 4 : 2) void k_adapter_s
           const float v[8] = {__uint_as_float(x.x) * s, __uint_as_float(x.y) * s, __uint_as_float(x.z) * s,
                               __uint_as_float(x.w) * s, __uint_as_float(y.x) * s, __uint_as_float(y.y) * s,
                               __uint_as_float(y.z) * s, __uint_as_float(y.w) * s};
-          uint4 hi, lo;
-          split_bf16(v, hi, lo);
-          const f32x4_t p = mfma16x16x32(as_bf16x8(w), as_bf16x8(lo),
-                                         mfma16x16x32(as_bf16x8(w), as_bf16x8(hi), f32x4_t{0.f, 0.f, 0.f, 0.f}));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][i] += has ? p[i] : 0.f;
+          add_term(acc[t], w, v, has);
         }
+      }
+    }
+  } else {
+    // ---- this wavefront's rows: their words of T, taken as they arrive and cleared
+    uint64_t* mine_t = a.words + (int64_t)blockIdx.x * M * width;
+    for (int k = wave; k < M; k += W) {
+      const int r = __builtin_amdgcn_readlane(rank_l, k);
+      const float s = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_l), k));
+      for (int r0 = 0; r0 < r; r0 += 32) {
+        const int at = r0 + 8 * g, have = l16 == k && at < r ? r - at : 0;
+        const uint4 w = k == wave && r0 == 0 ? ahead_b : load_b(k, r0);
+        uint64_t t[8];
+        bool ready = false;
+        for (int it = 0; !ready && it < kMostPolls; ++it) {
+          if (it) __builtin_amdgcn_s_sleep(1);
+          ready = true;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            t[i] = i < have ? __hip_atomic_load(mine_t + k * width + at + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM) : kPosted;
+            ready = ready && (t[i] & kPosted);
+          }
+        }
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // (never in practice: a word that did not arrive makes its row NaN instead of waiting for good)
+          v[i] = __uint_as_float((t[i] & kPosted) ? (uint32_t)t[i] : 0x7FC00000u) * s;
+          if (i < have) __hip_atomic_store(mine_t + k * width + at + i, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+        }
+        add_term(acc[0], w, v, l16 == k);
       }
     }
   }
   __syncthreads();  // the sums take the place of every wavefront's tiles
 #pragma unroll
-  for (int t = 0; t < XT; ++t) red[wave][t][lane] = acc[t];
+  for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
   __syncthreads();
   // the wavefronts' sums in order; lane l of tile t: row 16 t + (l & 15) of X, weight rows 4 (l >> 4) + v
-  const auto summed = [&](int t) {
+  for (int t = wave; t < MT; t += W) {
+    const int m = 16 * t + l16;
+    if (m >= M) continue;
     f32x4_t y = red[0][t][lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) {
       const f32x4_t v = red[w][t][lane];
       y[0] += v[0]; y[1] += v[1]; y[2] += v[2]; y[3] += v[3];
     }
-    return y;
-  };
-  if (E == 0) {
-    for (int t = wave; t < MT; t += W) {
-      const int m = 16 * t + l16;
-      if (m >= M) continue;
-      const f32x4_t y = summed(t);
-      *reinterpret_cast<uint2*>(a.Y + (int64_t)m * N + row0 + 4 * g) =
-          make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-    }
-    return;
+    *reinterpret_cast<uint2*>(a.Y + (int64_t)m * N + row0 + 4 * g) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
   }
-  if (wave != 0) return;
-  // ---- E > 0: T's tiles, each one column m of its sum, then their products with B's 16 rows
-  __shared__ float ts[E ? E * 16 : 1];  // [row][ranks * 16]
-  f32x4_t y = summed(0);
-  int m = 0, jt = 0;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if (m < M) {
-      f32x4_t t = summed(MT + e);
-      if (l16 == m) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) t[v] = 4 * g + v < tile_r[e] ? t[v] * a.drop.scale : 0.f;
-        *reinterpret_cast<f32x4_t*>(ts + 16 * e + 4 * g) = t;
-        if (a.T && blockIdx.x == 0 && 16 * jt + 4 * g < width)
-          *reinterpret_cast<f32x4_t*>(a.T + (int64_t)m * width + 16 * jt + 4 * g) = t;
-      }
-    }
-    if (++jt == ranks) jt = 0, ++m;
-  }
-  asm volatile("" ::: "memory");
-  for (int k = 0; k < M; ++k) {
-    const int r = __builtin_amdgcn_readlane(rank_l, k);
-    const uint16_t* B = reinterpret_cast<const uint16_t*>(readlane64(base_b, k));
-    const float s = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_l), k));
-    const rsrc_t rb = make_rsrc(B + row0 * r, (int64_t)kStreamRows * r * 2);
-    for (int r0 = 0; r0 < r; r0 += 32) {
-      const int at = r0 + 8 * g;
-      const uint4 w = WHOLE ? bload16(rb, at < r ? (uint32_t)((l16 * r + at) * 2) : kOOB)
-                            : load_row8(B, N * r, (row0 + l16) * r, at, r);
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (l16 == k && at < r) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = ts[16 * ranks * k + at + i] * s;
-      }
-      uint4 hi, lo;
-      split_bf16(v, hi, lo);
-      const f32x4_t p = mfma16x16x32(as_bf16x8(w), as_bf16x8(lo),
-                                     mfma16x16x32(as_bf16x8(w), as_bf16x8(hi), f32x4_t{0.f, 0.f, 0.f, 0.f}));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] += l16 == k ? p[i] : 0.f;
-    }
-  }
-  if (l16 < M)
-    *reinterpret_cast<uint2*>(a.Y + (int64_t)l16 * N + row0 + 4 * g) =
-        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
 }
 
 // ---------------------------------------------------------------- dA and dB
@@ -711,7 +715,7 @@ constexpr int kGradThreads = 256;
 constexpr int kGradWaves = kGradThreads / 64;
 constexpr int kGradCols = 64;         // columns per workgroup
 constexpr int kGradRanks = 64;        // ranks per workgroup
-constexpr int kSpan = 256;            // rows that a wavefront looks through at once
+constexpr int kSpan = 256;            // rows that a wavefront looks through at once, at most
 constexpr int kVTile = 32 * 32 + 64;  // bytes of a staged [32][16] BF16 tile, padded (bank offset)
 constexpr int kSumU = 4;              // partials loaded together before they are added
 
@@ -729,15 +733,17 @@ struct GradsArgs {
 };
 
 // Workgroup (x, y, z): 64 columns of dA (or of dB), a slice of the rows, an adapter and up to 64 of
-// its ranks.  A wavefront takes every fourth run of 256 rows, lists those of its adapter (ballots
-// over ids) and multiplies them 32 at a time: U [32 rows][ranks] as hi and lo
-// BF16 parts and V [32 rows][64 columns], both transposed through LDS.
+// its ranks.  The workgroup looks through 1024 rows at a time, lists those of its adapter (ballots
+// over ids) and deals them to its wavefronts 32 by 32, so that runs of one adapter's rows are
+// shared like rows that lie apart: U [32 rows][ranks] as hi and lo BF16 parts and V [32 rows][64
+// columns], both transposed through LDS.
 template <int JT>
 struct GradsLds {
   static constexpr int kWaveBytes = (4 + 2 * JT) * kVTile;
   static constexpr int kRedBytes = kGradWaves * JT * 4 * 64 * 16;
   __attribute__((aligned(16))) char tiles[kGradWaves * kWaveBytes > kRedBytes ? kGradWaves * kWaveBytes : kRedBytes];
-  uint16_t lists[kGradWaves][kSpan];
+  uint16_t list[kGradWaves * kSpan];
+  int counts[kGradWaves];
   bool last;
 };
 template <int JT, int D, bool DROP, bool IS_B>
@@ -759,7 +765,8 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
   if (DROP) key = load_rng(a.drop.rng), t2 = threshold_halves(a.drop.threshold);
   char* vt = smem + wave * kWaveBytes;  // 4 V tiles, JT hi tiles, JT lo tiles
   char* ut = vt + 4 * kVTile;
-  uint16_t* list = lds.lists[wave];
+  uint16_t* list = lds.list;
+  const int span = C <= (int64_t(1) << 20) ? kSpan : 64;  // the rows looked through stay below 2^31 bytes
   const int32_t* __restrict__ ids = a.rows.ids;
   const uint64_t below = lane ? ~0ull >> (64 - lane) : 0ull;
   f32x4_t acc[JT][4];
@@ -767,34 +774,48 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
   for (int t = 0; t < JT; ++t)
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int64_t first = mbeg + kSpan * wave; first < mend; first += (int64_t)kSpan * kGradWaves) {
-    const int n = (int)(mend - first < kSpan ? mend - first : kSpan);
-    int count = 0, id[kSpan / 64];
-#pragma unroll
-    for (int q = 0; q < kSpan / 64; ++q) id[q] = 64 * q + lane < n ? (ids ? ids[first + 64 * q + lane] : 0) : -1;
-    asm volatile("" ::: "memory");
+  for (int64_t first = mbeg; first < mend; first += (int64_t)span * kGradWaves) {
+    const int n = (int)(mend - first < span * kGradWaves ? mend - first : span * kGradWaves);
+    int own = 0, id[kSpan / 64];
+    uint64_t hits[kSpan / 64];
 #pragma unroll
     for (int q = 0; q < kSpan / 64; ++q) {
-      const bool hit = id[q] == adapter;
-      const uint64_t mask = __ballot(hit);
-      if (hit) list[count + __popcll(mask & below)] = (uint16_t)(64 * q + lane);
-      count += __popcll(mask);
+      const int at = span * wave + 64 * q + lane;
+      id[q] = 64 * q < span && at < n ? (ids ? ids[first + at] : 0) : -1;
     }
-    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int q = 0; q < kSpan / 64; ++q) hits[q] = __ballot(id[q] == adapter), own += __popcll(hits[q]);
+    __syncthreads();  // the last rows' list is read
+    if (lane == 0) lds.counts[wave] = own;
+    __syncthreads();
+    int to = 0, count = 0;
+#pragma unroll
+    for (int w = 0; w < kGradWaves; ++w) {
+      const int c = __builtin_amdgcn_readfirstlane(lds.counts[w]);
+      to += w < wave ? c : 0;
+      count += c;
+    }
+#pragma unroll
+    for (int q = 0; q < kSpan / 64; ++q) {
+      if (id[q] == adapter) list[to + __popcll(hits[q] & below)] = (uint16_t)(span * wave + 64 * q + lane);
+      to += __popcll(hits[q]);
+    }
+    __syncthreads();
     const rsrc_t rv = make_rsrc(V + first * C, n * C * 2);
     const rsrc_t ru = make_rsrc(U + first * width, n * width * 4);
     const auto row = [&](int i) { return i < count ? (int)list[i] : -1; };
-    for (int i0 = 0; i0 < count; i0 += 32 * D) {
+    constexpr int kStep = 32 * kGradWaves;  // from one of a wavefront's groups to its next
+    for (int i0 = 32 * wave; i0 < count; i0 += kStep * D) {
       uint4 vv[D][4], uw[D][JT][2];
 #pragma unroll
       for (int d = 0; d < D; ++d) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int m = row(i0 + 32 * d + 8 * i + (lane >> 3));
+          const int m = row(i0 + kStep * d + 8 * i + (lane >> 3));
           const int64_t c = c0 + 8 * (lane & 7);
           vv[d][i] = bload16(rv, (m >= 0 && c < C) ? (uint32_t)((m * C + c) * 2) : kOOB);
         }
-        const int m = row(i0 + 32 * d + (lane >> 1));
+        const int m = row(i0 + kStep * d + (lane >> 1));
 #pragma unroll
         for (int t = 0; t < JT; ++t) {
           const int j = j_first + 16 * t + 8 * (lane & 1);
@@ -812,7 +833,7 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
           const int in = 8 * i + (lane >> 3), ct = (lane & 7) >> 1, half = lane & 1;
           uint4 v = vv[d][i];
           if (DROP) {
-            const int m = row(i0 + 32 * d + in);
+            const int m = row(i0 + kStep * d + in);
             v = drop8(v, key, (uint64_t)((first + (m < 0 ? 0 : m)) * (C / 8) + c0 / 8 + (lane & 7)), t2);
           }
           *reinterpret_cast<uint4*>(vt + ct * kVTile + in * 32 + 16 * half) = v;
@@ -915,21 +936,21 @@ __global__ __launch_bounds__(kGradThreads) void k_adapter_grads(GradsArgs a) {
   else grads_body<JT, D, false, true>(a, lds);
 }
 
-template <int W, int MT, int E, int PD>
+template <int W, int MT, bool POST, int PD>
 hipError_t stream_go(const StreamArgs& a, const Nf4Tables& tab, hipStream_t st) {
   const dim3 grid((unsigned)(a.N / kStreamRows));
-  if (a.rows.whole) hipLaunchKernelGGL((k_adapter_stream<W, MT, E, PD, true>), grid, dim3(64 * W), 0, st, a, tab);
-  else hipLaunchKernelGGL((k_adapter_stream<W, MT, E, PD, false>), grid, dim3(64 * W), 0, st, a, tab);
+  if (a.rows.whole) hipLaunchKernelGGL((k_adapter_stream<W, MT, POST, PD, true>), grid, dim3(64 * W), 0, st, a, tab);
+  else hipLaunchKernelGGL((k_adapter_stream<W, MT, POST, PD, false>), grid, dim3(64 * W), 0, st, a, tab);
   return hipGetLastError();
 }
 template <int W>
 hipError_t stream_as(const StreamArgs& a, const Nf4Tables& tab, hipStream_t st) {
-  if (a.rows.M <= 16) return stream_go<W, 1, 0, 4>(a, tab, st);
-  if (a.rows.M <= 32) return stream_go<W, 2, 0, 2>(a, tab, st);
-  if (a.rows.M <= 48) return stream_go<W, 3, 0, 1>(a, tab, st);
-  if (a.rows.M <= 64) return stream_go<W, 4, 0, 1>(a, tab, st);
-  if (a.rows.M <= 96) return stream_go<W, 6, 0, 1>(a, tab, st);
-  return stream_go<W, 8, 0, 1>(a, tab, st);
+  if (a.rows.M <= 16) return stream_go<W, 1, false, 4>(a, tab, st);
+  if (a.rows.M <= 32) return stream_go<W, 2, false, 2>(a, tab, st);
+  if (a.rows.M <= 48) return stream_go<W, 3, false, 1>(a, tab, st);
+  if (a.rows.M <= 64) return stream_go<W, 4, false, 1>(a, tab, st);
+  if (a.rows.M <= 96) return stream_go<W, 6, false, 1>(a, tab, st);
+  return stream_go<W, 8, false, 1>(a, tab, st);
 }
 
 template <int JT>
@@ -979,31 +1000,33 @@ hipError_t launch_shrink_both(const AdapterRows& rows, const uint16_t* X, int64_
   return rows.whole ? shrink2_by_rank<false, true>(t, g, st) : shrink2_by_rank<false, false>(t, g, st);
 }
 
-// Where every workgroup of the stream forms T itself: up to two tiles of 16 ranks in all, while
-// reading them in every workgroup costs less than the launch that it saves (4096 x 4096: one tile
-// 9.8 us and 12.2 in two launches, two tiles 11.0 and 12.3, four 15.6 and 12.5; one tile at 14336 x
-// 4096 31.8 and 24.0).  That launch is slower over long rows (4096 x 14336 22.0 and 27.4).
-bool stream_forms_t(int64_t M, int64_t N, int64_t K, int32_t width) {
-  const int64_t tiles = M * ((width + 15) / 16);
-  return tiles <= 2 && (2 * tiles * N * K <= (int64_t(1) << 26) || (tiles == 1 && N <= 4096));
+// Where the stream's workgroups form T and post it: one tile of rows, few enough elements that no
+// workgroup forms more than two and that the posted words (elements times workgroups) cost less
+// than the launch that they save (4096 x 4096: one row of 16 ranks 9.4 us and 12.3 in two launches,
+// of 64 ranks 9.8 and 12.2, 8 rows 10.7 and 12.3, 16 rows 12.6 and 12.5; 14336 x 4096: one row 20 and
+// 24, 8 rows of 8 ranks, 57000 words, 33 and 24; 64 x 64, four elements each: 8.6 and 7.0).
+bool stream_forms_t(int64_t M, int64_t N, int32_t width) {
+  const int64_t slots = M * width, groups = N / kStreamRows;
+  static_assert(kPostedWords * sizeof(uint64_t) <= QLORA_WS_COUNTER_BYTES, "in the workspace's head");
+  return M <= 16 && slots <= 2 * groups && slots * groups <= kPostedWords;
 }
 
 hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, const float* c2s, const float* mu,
                                  int64_t N, int64_t K, const uint16_t* X, const AdapterRows& rows, const DropMask& drop,
-                                 float* T, uint16_t* Y, const Nf4Tables& tab, hipStream_t st) {
+                                 float* T, uint16_t* Y, void* head, const Nf4Tables& tab, hipStream_t st) {
   if (rows.M > kStreamMaxRows) return hipErrorInvalidValue;
   const int tiles = (int)((rows.M + kRowTile - 1) / kRowTile), ranks = (rows.width + 15) / 16;
   const StreamArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, rows, drop, T, Y,
-                     std::min((int)rows.count, kRowTile)};
-  if (stream_forms_t(rows.M, N, K, rows.width)) {
-    return rows.M * ranks <= 1 ? stream_go<8, 1, 1, 4>(a, tab, st) : stream_go<8, 1, 2, 2>(a, tab, st);
-  }
+                     std::min((int)rows.count, kRowTile), static_cast<uint64_t*>(head)};
+  const bool wide = N / kStreamRows > 512;
+  if (stream_forms_t(rows.M, N, rows.width))
+    return wide ? stream_go<4, 1, true, 4>(a, tab, st) : stream_go<8, 1, true, 4>(a, tab, st);
   const dim3 grid_t((unsigned)(tiles * ranks * a.lists));
   if (drop.threshold) hipLaunchKernelGGL(k_adapter_t<true>, grid_t, dim3(kStreamThreads), 0, st, a);
   else hipLaunchKernelGGL(k_adapter_t<false>, grid_t, dim3(kStreamThreads), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return N / kStreamRows > 512 ? stream_as<4>(a, tab, st) : stream_as<8>(a, tab, st);
+  return wide ? stream_as<4>(a, tab, st) : stream_as<8>(a, tab, st);
 }
 
 GradPlan adapter_grad_plan(int64_t M, int64_t N, int64_t K, int32_t count, int32_t max_rank) {

@@ -181,7 +181,7 @@ int qlora_adapters_fwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(Wq->codes);
   if (stream_path(M, dq))
     return hip_status(launch_adapter_stream(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, X, rows, drop,
-                                            stream_forms_t(M, N, K, rows.width) ? T_save : T, Y, tab, stream));
+                                            stream_forms_t(M, N, rows.width) ? T_save : T, Y, ws, tab, stream));
   const AdapterHead head{rows, T, 0, 1.f, DropMask{}};
   float* gpart = reinterpret_cast<float*>(base + L.gpart);
   if (codes_path(M, N, K, dq)) {
