@@ -296,7 +296,8 @@ __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
 
 constexpr int kStreamThreads = 512;
 constexpr int kStreamWaves = kStreamThreads / 64;
-constexpr int kStreamRows = 16;  // weight rows per workgroup
+constexpr int kStreamRows = 16;  // weight rows of a tile
+constexpr int kStreamMaxRows = 128;
 
 struct StreamArgs {
   const uint8_t *codes, *code8;
@@ -470,17 +471,15 @@ __device__ __forceinline__ void post_t(const StreamArgs& a, int tid) {
   }
 }
 
-// acc += B's 16 rows times v (eight ranks for each lane's row of X, as hi and lo BF16 parts), where
-// `has`: the products of other rows are not taken.
-__device__ __forceinline__ void add_term(f32x4_t& acc, const uint4& w, const float (&v)[8], bool has) {
-  uint4 hi, lo;
-  split_bf16(v, hi, lo);
+// acc += B's 16 rows times hi + lo (eight ranks for each lane's row of X) where `has`: the products of
+// other rows are not taken.
+__device__ __forceinline__ void add_term(f32x4_t& acc, const uint4& w, const uint4& hi, const uint4& lo, bool has) {
   const f32x4_t p = mfma16x16x32(as_bf16x8(w), as_bf16x8(lo), mfma16x16x32(as_bf16x8(w), as_bf16x8(hi), f32x4_t{0.f, 0.f, 0.f, 0.f}));
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i] += has ? p[i] : 0.f;
 }
 
-// 16 weight rows over the whole reduction.  A wavefront takes groups of four 64-weight blocks;
+// 16 RT weight rows over the whole reduction.  A wavefront takes groups of four 64-weight blocks;
 // lane (l16, g) decodes block 4 group + g of row l16 (32 bytes of codes, one level table scaled by
 // the block's constant: exactly w_hat).  The four lanes of a row then exchange their words (a 4 x 4
 // transpose by lane swaps), so that an MFMA 16x16x32 operand holds 32 consecutive columns.  X comes
@@ -494,36 +493,46 @@ __device__ __forceinline__ void add_term(f32x4_t& acc, const uint4& w, const flo
 // distinct adapters of all rows among themselves, and each multiplies its ones' 16 rows of B with T
 // (hi and lo BF16 parts) into its accumulators.  With POST (a row or a few), workgroups form T while
 // they stream, one element each, and post it to every workgroup (below); the wavefronts deal the rows
-// among themselves.  W: wavefronts; four where there are more than two workgroups of eight to a
-// compute unit (longer runs of blocks for each: 37 rows at 14336 x 4096 41 -> 39 us, 64 rows 42 -> 36).
-template <int W, int MT, bool POST, int PD, bool WHOLE>
-__global__ __launch_bounds__(64 * W, !POST && MT <= 3 ? 4 : 2) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
-  static_assert(!POST || MT == 1, "few rows");
+// among themselves.
+//
+// Every workgroup reads all of X, by way of the L2 (at 14336 x 4096 and RT = 1, 940 MB for 64 rows), so
+// wide weights are taken two tiles of rows at a time, RT = 2 (64 rows there 44 us with RT = 1, 35 with 2;
+// 4096 x 4096, where that leaves half of the compute units without work, 16 and 20).  W: wavefronts;
+// four where more workgroups of eight are started than fit at once (longer runs of blocks for each:
+// 64 rows at 14336 x 4096 35 -> 32 us; at 4096 x 4096 16 -> 19).
+template <int W, int RT, int MT, bool POST, int PD, bool WHOLE>
+__global__ __launch_bounds__(64 * W, !POST && RT == 1 && MT <= 3 ? 4 : 2) void k_adapter_stream(StreamArgs a, Nf4Tables tab) {
+  static_assert(!POST || RT * MT == 1, "few rows");
+  static_assert(RT <= 2, "the sums take the place of the tiles");
   __shared__ uint4 smem[W * MT * 128];  // a wavefront's tiles of X; then the sums
-  f32x4_t(*red)[MT][64] = reinterpret_cast<f32x4_t(*)[MT][64]>(smem);
+  f32x4_t(*red)[RT * MT][64] = reinterpret_cast<f32x4_t(*)[RT * MT][64]>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int64_t K = a.K, N = a.N, row0 = (int64_t)blockIdx.x * kStreamRows;
+  const int64_t K = a.K, N = a.N, row0 = (int64_t)blockIdx.x * (kStreamRows * RT);
   const int M = (int)a.rows.M, width = a.rows.width;
   const uint32_t nb = (uint32_t)(K / 64), ng = (nb + 3) / 4;
   const rsrc_t rx = make_rsrc(a.X, (int64_t)M * K * 2);
-  const rsrc_t rc = make_rsrc(a.codes + row0 * (K / 2), kStreamRows * (K / 2));
-  const rsrc_t r8 = make_rsrc(a.code8 + row0 * nb, (int64_t)kStreamRows * nb);
+  const int64_t rows_here = N - row0 < kStreamRows * RT ? N - row0 : kStreamRows * RT;
+  const rsrc_t rc = make_rsrc(a.codes + row0 * (K / 2), rows_here * (K / 2));
+  const rsrc_t r8 = make_rsrc(a.code8 + row0 * nb, rows_here * nb);
   const rsrc_t r2 = make_rsrc(a.c2s, ((N * nb + 255) / 256) * 4);
   const uint32_t blk_row = (uint32_t)(row0 + l16) * nb;
   struct Codes {
-    uint4 c0, c1;
-    uint32_t c8, c2;
+    uint4 c0[RT], c1[RT];
+    uint32_t c8[RT], c2[RT];
   };
   const auto load = [&](uint32_t group) {
     const uint32_t b = 4 * group + g;
     const bool ok = group < ng && b < nb;
     Codes c;
-    const uint32_t off = (uint32_t)(l16 * (K / 2)) + 32 * b;
-    c.c0 = bload16(rc, ok ? off : kOOB);
-    c.c1 = bload16(rc, ok ? off + 16 : kOOB);
-    c.c8 = bload1(r8, ok ? l16 * nb + b : kOOB);
-    c.c2 = bload4(r2, ok ? ((blk_row + b) >> 8) * 4 : kOOB);
+#pragma unroll
+    for (int u = 0; u < RT; ++u) {
+      const uint32_t off = (uint32_t)((16 * u + l16) * (K / 2)) + 32 * b;
+      c.c0[u] = bload16(rc, ok ? off : kOOB);
+      c.c1[u] = bload16(rc, ok ? off + 16 : kOOB);
+      c.c8[u] = bload1(r8, ok ? (16 * u + l16) * nb + b : kOOB);
+      c.c2[u] = bload4(r2, ok ? ((blk_row + 16 * u * nb + b) >> 8) * 4 : kOOB);
+    }
     return c;
   };
   // each lane its rows' adapters (asked for first: what follows depends on them)
@@ -532,9 +541,11 @@ __global__ __launch_bounds__(64 * W, !POST && MT <= 3 ? 4 : 2) void k_adapter_st
   for (int t = 0; t < MT; ++t) id[t] = adapter_of(a.rows, 16 * t + l16);
   Codes cur = load(wave), next = load(wave + W);
   const float mu = a.mu[0];
-  f32x4_t acc[MT];
+  f32x4_t acc[RT][MT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int u = 0; u < RT; ++u)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[u][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   uint4* xs = smem + wave * MT * 128;
   uint4 xr[PD][MT][2];
   const auto load_x = [&](uint4 (&x)[MT][2], uint32_t blk) {
@@ -586,36 +597,41 @@ __global__ __launch_bounds__(64 * W, !POST && MT <= 3 ? 4 : 2) void k_adapter_st
     rank_l = POST && id[0] < 0 ? 0 : e->r;
     scale_l = e->s;
   }
-  // ranks r0 + 8 g .. +7 of B's row row0 + l16, for the adapter that lane k holds
-  const auto load_b = [&](int k, int r0) {
+  // ranks r0 + 8 g .. +7 of B's row row0 + 16 u + l16, for the adapter that lane k holds
+  const auto load_b = [&](int k, int r0, int u) {
     const int r = __builtin_amdgcn_readlane(rank_l, k), at = r0 + 8 * g;
     const uint16_t* B = reinterpret_cast<const uint16_t*>(readlane64(base_b, k));
-    return WHOLE ? bload16(make_rsrc(B + row0 * r, (int64_t)kStreamRows * r * 2), at < r ? (uint32_t)((l16 * r + at) * 2) : kOOB)
-                 : load_row8(B, N * (r ? r : 1), (row0 + l16) * r, at, r);
+    if (WHOLE)
+      return bload16(make_rsrc(B + row0 * r, rows_here * r * 2), at < r ? (uint32_t)(((16 * u + l16) * r + at) * 2) : kOOB);
+    const int64_t row = row0 + 16 * u + l16;
+    return load_row8(B, N * (r ? r : 1), (row < N ? row : N - 1) * r, at, r);
   };
   uint4 ahead_b = make_uint4(0, 0, 0, 0);
-  if (POST && wave < M) ahead_b = load_b(wave, 0);
+  if (POST && wave < M) ahead_b = load_b(wave, 0, 0);
 
   // ---- the base product
   for (uint32_t group = wave; group < ng; group += W) {
     const Codes c = cur;
     cur = next;
     next = load(group + 2 * W);
-    Lut L;
-    build_scaled_lut(tab, stored_scale(c.c8, __uint_as_float(c.c2), mu), L);
-    const uint32_t words[8] = {c.c0.x, c.c0.y, c.c0.z, c.c0.w, c.c1.x, c.c1.y, c.c1.z, c.c1.w};
-    uint32_t w[8][4];  // word i of this lane's block; then, of block i % 4, word 4 (i / 4) + g
+    uint32_t w[RT][8][4];  // word i of this lane's block; then, of block i % 4, word 4 (i / 4) + g
 #pragma unroll
-    for (int i = 0; i < 8; ++i) decode8(words[i], L, w[i]);
+    for (int u = 0; u < RT; ++u) {
+      Lut L;
+      build_scaled_lut(tab, stored_scale(c.c8[u], __uint_as_float(c.c2[u]), mu), L);
+      const uint32_t words[8] = {c.c0[u].x, c.c0[u].y, c.c0[u].z, c.c0[u].w, c.c1[u].x, c.c1[u].y, c.c1[u].z, c.c1[u].w};
 #pragma unroll
-    for (int h = 0; h < 8; h += 4)
+      for (int i = 0; i < 8; ++i) decode8(words[i], L, w[u][i]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        swap16(w[h][q], w[h + 1][q]);
-        swap16(w[h + 2][q], w[h + 3][q]);
-        swap32(w[h][q], w[h + 2][q]);
-        swap32(w[h + 1][q], w[h + 3][q]);
-      }
+      for (int h = 0; h < 8; h += 4)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          swap16(w[u][h][q], w[u][h + 1][q]);
+          swap16(w[u][h + 2][q], w[u][h + 3][q]);
+          swap32(w[u][h][q], w[u][h + 2][q]);
+          swap32(w[u][h + 1][q], w[u][h + 3][q]);
+        }
+    }
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       // the wavefront's LDS accesses run in order
@@ -632,7 +648,9 @@ __global__ __launch_bounds__(64 * W, !POST && MT <= 3 ? 4 : 2) void k_adapter_st
         const int at = 8 * l16 + ((4 * h + g) ^ (l16 >> 1));
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          acc[t] = mfma16x16x32(as_bf16x8(w[b + 4 * h]), as_bf16x8(xs[128 * t + at]), acc[t]);
+          const bf16x8_t x = as_bf16x8(xs[128 * t + at]);
+#pragma unroll
+          for (int u = 0; u < RT; ++u) acc[u][t] = mfma16x16x32(as_bf16x8(w[u][b + 4 * h]), x, acc[u][t]);
         }
       }
       asm volatile("" ::: "memory");
@@ -647,7 +665,9 @@ __global__ __launch_bounds__(64 * W, !POST && MT <= 3 ? 4 : 2) void k_adapter_st
       const float s = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_l), k));
       for (int r0 = 0; r0 < r; r0 += 32) {
         const int at = r0 + 8 * g;
-        const uint4 w = load_b(k, r0);
+        uint4 w[RT];
+#pragma unroll
+        for (int u = 0; u < RT; ++u) w[u] = load_b(k, r0, u);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           const bool has = id[t] == one;
@@ -657,7 +677,10 @@ __global__ __launch_bounds__(64 * W, !POST && MT <= 3 ? 4 : 2) void k_adapter_st
           const float v[8] = {__uint_as_float(x.x) * s, __uint_as_float(x.y) * s, __uint_as_float(x.z) * s,
                               __uint_as_float(x.w) * s, __uint_as_float(y.x) * s, __uint_as_float(y.y) * s,
                               __uint_as_float(y.z) * s, __uint_as_float(y.w) * s};
-          add_term(acc[t], w, v, has);
+          uint4 hi, lo;
+          split_bf16(v, hi, lo);
+#pragma unroll
+          for (int u = 0; u < RT; ++u) add_term(acc[u][t], w[u], hi, lo, has);
         }
       }
     }
@@ -669,7 +692,7 @@ __global__ __launch_bounds__(64 * W, !POST && MT <= 3 ? 4 : 2) void k_adapter_st
       const float s = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_l), k));
       for (int r0 = 0; r0 < r; r0 += 32) {
         const int at = r0 + 8 * g, have = l16 == k && at < r ? r - at : 0;
-        const uint4 w = k == wave && r0 == 0 ? ahead_b : load_b(k, r0);
+        const uint4 w = k == wave && r0 == 0 ? ahead_b : load_b(k, r0, 0);
         uint64_t t[8];
         bool ready = false;
         for (int it = 0; !ready && it < kMostPolls; ++it) {
@@ -688,25 +711,31 @@ __global__ __launch_bounds__(64 * W, !POST && MT <= 3 ? 4 : 2) void k_adapter_st
           v[i] = __uint_as_float((t[i] & kPosted) ? (uint32_t)t[i] : 0x7FC00000u) * s;
           if (i < have) __hip_atomic_store(mine_t + k * width + at + i, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
         }
-        add_term(acc[0], w, v, l16 == k);
+        uint4 hi, lo;
+        split_bf16(v, hi, lo);
+        add_term(acc[0][0], w, hi, lo, l16 == k);
       }
     }
   }
   __syncthreads();  // the sums take the place of every wavefront's tiles
 #pragma unroll
-  for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
+  for (int u = 0; u < RT; ++u)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) red[wave][RT * t + u][lane] = acc[u][t];
   __syncthreads();
-  // the wavefronts' sums in order; lane l of tile t: row 16 t + (l & 15) of X, weight rows 4 (l >> 4) + v
-  for (int t = wave; t < MT; t += W) {
-    const int m = 16 * t + l16;
-    if (m >= M) continue;
-    f32x4_t y = red[0][t][lane];
+  // the wavefronts' sums in order; lane l of tile RT t + u: row 16 t + (l & 15) of X, weight rows
+  // 16 u + 4 (l >> 4) + v
+  for (int i = wave; i < RT * MT; i += W) {
+    const int m = 16 * (i / RT) + l16;
+    const int64_t n = row0 + 16 * (i % RT) + 4 * g;
+    if (m >= M || n >= N) continue;
+    f32x4_t y = red[0][i][lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) {
-      const f32x4_t v = red[w][t][lane];
+      const f32x4_t v = red[w][i][lane];
       y[0] += v[0]; y[1] += v[1]; y[2] += v[2]; y[3] += v[3];
     }
-    *reinterpret_cast<uint2*>(a.Y + (int64_t)m * N + row0 + 4 * g) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    *reinterpret_cast<uint2*>(a.Y + (int64_t)m * N + n) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
   }
 }
 
@@ -936,21 +965,20 @@ __global__ __launch_bounds__(kGradThreads) void k_adapter_grads(GradsArgs a) {
   else grads_body<JT, D, false, true>(a, lds);
 }
 
-template <int W, int MT, bool POST, int PD>
+template <int W, int RT, int MT, bool POST, int PD>
 hipError_t stream_go(const StreamArgs& a, const Nf4Tables& tab, hipStream_t st) {
-  const dim3 grid((unsigned)(a.N / kStreamRows));
-  if (a.rows.whole) hipLaunchKernelGGL((k_adapter_stream<W, MT, POST, PD, true>), grid, dim3(64 * W), 0, st, a, tab);
-  else hipLaunchKernelGGL((k_adapter_stream<W, MT, POST, PD, false>), grid, dim3(64 * W), 0, st, a, tab);
+  const dim3 grid((unsigned)((a.N + kStreamRows * RT - 1) / (kStreamRows * RT)));
+  if (a.rows.whole) hipLaunchKernelGGL((k_adapter_stream<W, RT, MT, POST, PD, true>), grid, dim3(64 * W), 0, st, a, tab);
+  else hipLaunchKernelGGL((k_adapter_stream<W, RT, MT, POST, PD, false>), grid, dim3(64 * W), 0, st, a, tab);
   return hipGetLastError();
 }
-template <int W>
+// 17 to 96 rows
+template <int W, int RT>
 hipError_t stream_as(const StreamArgs& a, const Nf4Tables& tab, hipStream_t st) {
-  if (a.rows.M <= 16) return stream_go<W, 1, false, 4>(a, tab, st);
-  if (a.rows.M <= 32) return stream_go<W, 2, false, 2>(a, tab, st);
-  if (a.rows.M <= 48) return stream_go<W, 3, false, 1>(a, tab, st);
-  if (a.rows.M <= 64) return stream_go<W, 4, false, 1>(a, tab, st);
-  if (a.rows.M <= 96) return stream_go<W, 6, false, 1>(a, tab, st);
-  return stream_go<W, 8, false, 1>(a, tab, st);
+  if (a.rows.M <= 32) return stream_go<W, RT, 2, false, 2>(a, tab, st);
+  if (a.rows.M <= 48) return stream_go<W, RT, 3, false, 1>(a, tab, st);
+  if (a.rows.M <= 64) return stream_go<W, RT, 4, false, 1>(a, tab, st);
+  return stream_go<W, RT, 6, false, 1>(a, tab, st);
 }
 
 template <int JT>
@@ -1000,6 +1028,11 @@ hipError_t launch_shrink_both(const AdapterRows& rows, const uint16_t* X, int64_
   return rows.whole ? shrink2_by_rank<false, true>(t, g, st) : shrink2_by_rank<false, false>(t, g, st);
 }
 
+// Up to 64 rows, and up to 128 of a smaller weight: the stream's workgroups read all of X in each, which
+// a product over tiles of 128 x 128 does not (128 rows: 4096 x 4096 23 us here and 28 by tiles, 14336 x
+// 4096 64 and 41, 4096 x 14336 60 and 42; 64 rows: 14336 x 4096 33 and 36, 4096 x 14336 41 and 37).
+bool adapter_stream_fits(int64_t M, int64_t N, int64_t K) { return M <= 64 || (M <= kStreamMaxRows && N * K < (int64_t(1) << 25)); }
+
 // Where the stream's workgroups form T and post it: one tile of rows, few enough elements that no
 // workgroup forms more than two and that the posted words (elements times workgroups) cost less
 // than the launch that they save (4096 x 4096: one row of 16 ranks 9.4 us and 12.3 in two launches,
@@ -1018,15 +1051,19 @@ hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, co
   const int tiles = (int)((rows.M + kRowTile - 1) / kRowTile), ranks = (rows.width + 15) / 16;
   const StreamArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, rows, drop, T, Y,
                      std::min((int)rows.count, kRowTile), static_cast<uint64_t*>(head)};
-  const bool wide = N / kStreamRows > 512;
+  const bool wide = N / kStreamRows > 512;  // more than fit at once
   if (stream_forms_t(rows.M, N, rows.width))
-    return wide ? stream_go<4, 1, true, 4>(a, tab, st) : stream_go<8, 1, true, 4>(a, tab, st);
+    return wide ? stream_go<4, 1, 1, true, 4>(a, tab, st) : stream_go<8, 1, 1, true, 4>(a, tab, st);
   const dim3 grid_t((unsigned)(tiles * ranks * a.lists));
   if (drop.threshold) hipLaunchKernelGGL(k_adapter_t<true>, grid_t, dim3(kStreamThreads), 0, st, a);
   else hipLaunchKernelGGL(k_adapter_t<false>, grid_t, dim3(kStreamThreads), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return wide ? stream_as<4>(a, tab, st) : stream_as<8>(a, tab, st);
+  if (rows.M <= 16) return wide ? stream_go<4, 1, 1, false, 4>(a, tab, st) : stream_go<8, 1, 1, false, 4>(a, tab, st);
+  if (rows.M > 96) return wide ? stream_go<4, 1, 8, false, 1>(a, tab, st) : stream_go<8, 1, 8, false, 1>(a, tab, st);
+  // two weight tiles to a workgroup where that leaves one for each compute unit (and registers last)
+  if (N < 8192) return stream_as<8, 1>(a, tab, st);
+  return wide ? stream_as<4, 2>(a, tab, st) : stream_as<8, 2>(a, tab, st);
 }
 
 GradPlan adapter_grad_plan(int64_t M, int64_t N, int64_t K, int32_t count, int32_t max_rank) {

@@ -62,7 +62,7 @@ AdapterRows rows_of(const qlora_adapters_t* set, const int32_t* ids, int64_t M) 
 
 // Few rows read the weight's codes as they are; more (and formats that only the decode kernels
 // read) go through the decoded copy.
-bool stream_path(int64_t M, int dq) { return M <= kStreamMaxRows && dq == QLORA_DQ_E4M3; }
+bool stream_path(int64_t M, int64_t N, int64_t K, int dq) { return dq == QLORA_DQ_E4M3 && adapter_stream_fits(M, N, K); }
 // The product over the codes, for the rows between few and many.
 bool codes_path(int64_t M, int64_t F, int64_t Kr, int dq) { return dq == QLORA_DQ_E4M3 && adapter_gemm_fits(M, F, Kr); }
 
@@ -83,7 +83,7 @@ Layout layout(bool bwd, int64_t M, const qlora_adapters_t* set, int dq) {
   const size_t t_bytes = sizeof(float) * (size_t)M * width;
   w.t = take(t_bytes);
   if (bwd) w.g = take(t_bytes);
-  if (bwd || !stream_path(M, dq)) {
+  if (bwd || !stream_path(M, N, K, dq)) {
     const int32_t t_split = shrink_split(M, K), g_split = shrink_split(M, N);
     w.spart = take(t_split > 1 ? t_bytes * t_split : 0);
     if (bwd) w.gspart = take(g_split > 1 ? t_bytes * g_split : 0);
@@ -179,7 +179,7 @@ int qlora_adapters_fwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   float* part = reinterpret_cast<float*>(base + L.spart);
   unsigned int* counters = static_cast<unsigned int*>(ws);
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(Wq->codes);
-  if (stream_path(M, dq))
+  if (stream_path(M, N, K, dq))
     return hip_status(launch_adapter_stream(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, X, rows, drop,
                                             stream_forms_t(M, N, rows.width) ? T_save : T, Y, ws, tab, stream));
   const AdapterHead head{rows, T, 0, 1.f, DropMask{}};

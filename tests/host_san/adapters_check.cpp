@@ -92,7 +92,7 @@ void linears() {
                                         saved ? at<float>(10) : nullptr, dx ? at<uint16_t>(12) : nullptr, at<void>(11), bytes,
                                         nullptr);
             };
-            const bool stream = M <= 128 && dq == QLORA_DQ_E4M3;
+            const bool stream = (M <= 64 || (M <= 128 && N * K < int64_t(1) << 25)) && dq == QLORA_DQ_E4M3;
             for (int save = 0; save < 2; ++save) {
               // T and the stream, or T (with the decode, or before it), the product, its parts' sum
               run([&] { return fwd(fw, save); }, stream ? 1 : 2, stream ? 2 : 4, "fwd", M, N, K);

@@ -137,6 +137,12 @@ SHAPES = [  # M, d_out, d_in, ranks, ids
     (50, 8208, 192, [7, 16], "tokens"),
     (95, 8208, 128, [16, 8], "runs"),
     (127, 8240, 192, [48, 9, 16], "tokens"),
+    (20, 8192, 128, [16, 8], "tokens"),
+    (61, 8192, 320, [24, 5], "tokens"),
+    (79, 8192, 192, [16, 64], "runs"),
+    # up to 128 rows of a large weight
+    (65, 8192, 4096, [16], "none"),
+    (128, 4112, 8192, [16, 24], "tokens"),
     # several row tiles of a narrow weight
     (96, 112, 1344, [16, 16], "tokens"),
     (113, 64, 4160, [24, 128], "tokens"),
