@@ -48,8 +48,7 @@ struct ShrinkArgs {
 // address unit bounds the loads: 256 rows of 48 adapters over 14336 columns 21 us).
 template <int JT>
 struct ShrinkLds {
-  uint4 tiles[kShrinkWaves][(1 + JT) * 128];
-  bool last;
+  uint4 tiles[kShrinkWaves][(1 + JT) * 128];  // (no byte more: two of 80 KB, JT = 4, fill a compute unit)
 };
 template <int JT, bool QT, bool DROP, bool VEC, int D>
 __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, uint32_t wg, ShrinkLds<JT>& lds) {
@@ -195,11 +194,11 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, uint32_t wg, Sh
   __syncthreads();
   if (threadIdx.x == 0) {
     const unsigned int old = __hip_atomic_fetch_add(&a.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    lds.last = old + 1u == split;
-    if (lds.last) __hip_atomic_store(&a.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    lds.tiles[0][0].x = old + 1u == split;  // (the sums are read)
+    if (old + 1u == split) __hip_atomic_store(&a.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
-  if (!lds.last) return;
+  if (!lds.tiles[0][0].x) return;
   for (int t = wave; t < JT; t += kShrinkWaves) {
     const int j = 16 * t + 4 * g;
     if (m >= M || j >= width) continue;
