@@ -10,7 +10,7 @@ import functools
 import torch
 
 from ._binding import (DQ_FORMATS, OP_BWD, OP_FWD, QuantizedWeight, _check, _Nf4dq, _ptr, _tokens, _validate,
-                       _weight_specs, load_library)
+                       _weight_specs, load_library, quant_sizes)
 from ._training import TYPES, _BF16, _F32, _I64, _raw_stream, _right, _workspace
 
 
@@ -133,6 +133,22 @@ class AdapterSet:
         return self._sizes[key]
 
 
+def _weight_right(q, index) -> bool:
+    """The quantized weight's buffers, contiguous on that GPU, as many elements as its shape and format
+    need (what is not so is left to the full check)."""
+    nc, n8, n2 = quant_sizes(q.d_out, q.d_in, q.dq)
+    c, c8, u8 = q.codes, q.code8, torch.uint8
+    try:
+        if not (c.dtype is u8 and c.numel() == nc and c.get_device() == index and c.is_contiguous()
+                and c8.dtype is u8 and c8.numel() == n8 and c8.get_device() == index and c8.is_contiguous()):
+            return False
+        s, mu = q.c2s, q.mu
+        return q.dq == "none" or (s.dtype is _F32 and 4 * s.numel() == n2 and s.get_device() == index and s.is_contiguous()
+                                  and mu.dtype is _F32 and mu.numel() == 1 and mu.get_device() == index)
+    except AttributeError:
+        return False
+
+
 def _linear_check(q, adapters, specs, ids, dropout, rng, M):
     if not isinstance(q, QuantizedWeight):
         raise ValueError("weight: need a QuantizedWeight")
@@ -148,8 +164,9 @@ def _linear_check(q, adapters, specs, ids, dropout, rng, M):
         specs.append((rng, _I64, "rng", (2,)))
     device = adapters.device
     index = device.index
-    specs += _weight_specs(q)
     # what is right passes a short check (a call takes about as long as a small launch)
+    if not _weight_right(q, index):
+        specs += _weight_specs(q)
     for t, dtype, _, shape in specs:
         if not _right(t, dtype, shape, index):
             _validate(specs, device)
