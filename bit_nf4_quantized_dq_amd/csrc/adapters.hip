@@ -45,7 +45,9 @@ struct ShrinkArgs {
 // JT: 16-rank tiles.  QT: the operand is B_a [Kd, r], else A_a [r, Kd].  Rows of X (dY) and A come in
 // whole cache lines and pass through the wavefront's own LDS into operand order, chunks laid as in
 // the stream below (straight into operand order, where neighbouring lanes are in 16 rows, the
-// address unit bounds the loads: 256 rows of 48 adapters over 14336 columns 21 us).
+// address unit bounds the loads: 8192 rows over 14336 columns 91 us, so 76).  Bound by HBM for many rows
+// (those 76 us: 235 MB of dY, and 147 MB of the decode beside it), by A's rows through the L2 where a
+// tile's rows name many adapters or ranks (256 rows of 48 adapters over 14336 columns 20 us for 103 MB).
 template <int JT>
 struct ShrinkLds {
   uint4 tiles[kShrinkWaves][(1 + JT) * 128];  // (no byte more: two of 80 KB, JT = 4, fill a compute unit)
@@ -236,7 +238,8 @@ __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a,
                                             (int64_t)(grp - gn * groups_k), threadIdx.x);
   }
 }
-// T and G in one launch: they are independent, and a launch alone takes 6 to 8 us for few rows.
+// T and G in one launch: they are independent (555 rows of 6 adapters at 1040 x 4096: 16 us together, G
+// alone 9).
 template <int JT, bool DROP, bool VEC, int D>
 __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink2(ShrinkArgs t, ShrinkArgs g, uint32_t n_t) {
   __shared__ ShrinkLds<JT> lds;
@@ -763,8 +766,11 @@ struct GradsArgs {
 // Workgroup (x, y, z): 64 columns of dA (or of dB), a slice of the rows, an adapter and up to 64 of
 // its ranks.  The workgroup looks through 1024 rows at a time, lists those of its adapter (ballots
 // over ids) and deals them to its wavefronts 32 by 32, so that runs of one adapter's rows are
-// shared like rows that lie apart: U [32 rows][ranks] as hi and lo BF16 parts and V [32 rows][64
-// columns], both transposed through LDS.
+// shared like rows that lie apart (555 rows of 6 adapters in runs 19.4 us when each wavefront kept to
+// 256 rows, so 11.8): U [32 rows][ranks] as hi and lo BF16 parts and V [32 rows][64
+// columns], both transposed through LDS.  Bound by HBM at low ranks (8192 rows of 4 adapters of rank 16
+// at 14336 x 4096 81 us for 303 MB), by U at high ones, which every tile of columns reads anew (4096
+// rows of rank 64 at 4096 x 4096 38 us: 134 MB of U through the L2 beside 67 MB of V).
 template <int JT>
 struct GradsLds {
   static constexpr int kWaveBytes = (4 + 2 * JT) * kVTile;
