@@ -5,7 +5,7 @@
 // shrink : T[m] = drop(X[m]) A_a^T  and  G[m] = dY[m] B_a           (FP32 [M, width])
 // stream : Y = X w_hat^T + s_a T B_a^T for few rows, the weight decoded as it is read
 // grads  : dA_a = s_a sum of G[m]^T drop(X[m]),  dB_a = s_a sum of dY[m]^T T[m]
-// (many rows' Y and dX: gemm_nt.hip)
+// (more rows' Y, and dX: adapters_gemm.hip and gemm_nt.hip)
 //
 // Rows come in any order.  A workgroup finds the distinct adapters of its rows by ballots, loads
 // each one's operand once and takes the result for the rows that name it: a select, not a

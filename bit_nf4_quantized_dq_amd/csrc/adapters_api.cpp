@@ -1,6 +1,6 @@
 // C ABI of the frozen linear with many adapters and of dropout (declared in
 // include/qlora_adapters.h): argument checks, workspace layouts and plans; the kernels and their
-// launches are in adapters.hip, gemm_nt.hip and dropout.hip.
+// launches are in adapters.hip, adapters_gemm.hip, gemm_nt.hip and dropout.hip.
 #include <algorithm>
 #include <cmath>
 

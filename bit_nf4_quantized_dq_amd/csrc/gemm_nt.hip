@@ -558,13 +558,12 @@ hipError_t launch_gemm_nt_adapters(const uint16_t* A, int64_t F, const uint16_t*
   const auto go = [&](auto kernel) {
     hipExtLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, t.start, t.stop, 0, A, F, B, M, Kr, head, C, part, kb_per);
   };
-  const bool fullk = Kr % BK == 0;
   if (head.transposed) {
+    const bool fullk = Kr % BK == 0;
     if (ksplit > 1) fullk ? go(k_gemm_nt_rows<true, true, kRowsA>) : go(k_gemm_nt_rows<true, false, kRowsA>);
     else fullk ? go(k_gemm_nt_rows<false, true, kRowsA>) : go(k_gemm_nt_rows<false, false, kRowsA>);
-  } else {
-    if (ksplit > 1) fullk ? go(k_gemm_nt_rows<true, true, kRowsB>) : go(k_gemm_nt_rows<true, false, kRowsB>);
-    else fullk ? go(k_gemm_nt_rows<false, true, kRowsB>) : go(k_gemm_nt_rows<false, false, kRowsB>);
+  } else {  // the reduction is d_in, a multiple of 64
+    ksplit > 1 ? go(k_gemm_nt_rows<true, true, kRowsB>) : go(k_gemm_nt_rows<false, true, kRowsB>);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || ksplit <= 1) return e;

@@ -192,13 +192,13 @@ def test_formats(gpu_lib, M, dq, codebook):
     check_bwd(c, 0.1)
 
 
-@pytest.mark.parametrize("M", [4, 40, 140])
-def test_values_that_are_not_finite_stay_with_their_rows(gpu_lib, M):
+@pytest.mark.parametrize("M,N", [(4, 272), (4, 1040), (40, 272), (140, 272)])
+def test_values_that_are_not_finite_stay_with_their_rows(gpu_lib, M, N):
     """One adapter holds infinities and NaN: every row that names another, and every other
     adapter's gradient, comes out as if it were finite."""
     import bit_nf4_quantized_dq_amd as Q
 
-    c = make(M, M, 272, 320, [16, 8, 24], "tokens")
+    c = make(M, M, N, 320, [16, 8, 24], "tokens")
     ids = torch.arange(M, dtype=torch.int32, device="cuda") % 4 - 1
     out = []
     for poison in (False, True):
@@ -325,6 +325,63 @@ def test_two_streams_at_once(gpu_lib):
         for o in outs[k]:
             assert torch.equal(o[0], want[k][0]) and torch.equal(o[1], want[k][1])
         assert all(map(torch.equal, want[k][2:], c["set"].dA + c["set"].dB))
+
+
+@pytest.mark.parametrize("shape", [(260, 16, 2**20 + 64, [8, 16], "tokens"), (260, 2**20 + 16, 64, [16, 5], "tokens")])
+def test_long_rows(gpu_lib, shape):
+    """Rows of more than a million columns, on either side: the gradients look through fewer rows at once."""
+    print(shape, flush=True)
+    c = make(5, *shape)
+    check_fwd(c)
+    check_bwd(c)
+
+
+@pytest.mark.parametrize("i,shape", enumerate([(1, 4096, 4096, [16, 64], "tokens"), (2, 1040, 1088, [16, 8], "tokens"),
+                                               (4, 4096, 192, [16, 5, 24], "tokens"), (1, 16384, 128, [30], "none")]))
+def test_few_rows_again_and_again(gpu_lib, i, shape):
+    """T handed over within a launch: eager calls and replays with other ids, two streams at once, and
+    the workspace's head zero after them all."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    M = shape[0]
+    cases = [make(i, *shape, grads=False), make(i + 10, *shape, grads=False)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    work = [Q.new_workspace(c["set"].workspace_size(Q.OP_FWD, M)) for c in cases]
+    for turn in range(6):
+        want = []
+        for c in cases:
+            if c["ids"] is not None:
+                c["ids"].copy_(torch.randint(-1, len(c["A"]), (M,), generator=torch.Generator().manual_seed(turn)))
+            Y, T = check_fwd(c, 0.1)
+            want.append((Y, T))
+        torch.cuda.synchronize()
+        got = [[], []]
+        for _ in range(10):
+            for k, (c, s) in enumerate(zip(cases, streams)):
+                with torch.cuda.stream(s):
+                    T = torch.empty(M, c["set"].t_width, device="cuda")
+                    Y = Q.linear_adapters_fwd(c["q"], c["set"], c["X"], c["ids"], dropout=0.1, rng=c["rng"], T_save=T, ws=work[k])
+                    got[k].append((Y, T))
+        torch.cuda.synchronize()
+        for k in range(2):
+            assert not work[k][: 512 * 1024].any()
+            for Y, T in got[k]:
+                assert torch.equal(Y, want[k][0]) and torch.equal(T, want[k][1])
+    c, Y = cases[0], torch.empty(M, shape[1], dtype=torch.bfloat16, device="cuda")
+    with torch.cuda.stream(streams[0]):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=streams[0]):
+            for _ in range(5):
+                Q.linear_adapters_fwd(c["q"], c["set"], c["X"], c["ids"], dropout=0.1, rng=c["rng"], Y=Y, ws=work[0])
+    for turn in range(5):
+        if c["ids"] is not None:
+            c["ids"].copy_(torch.randint(-1, len(c["A"]), (M,), generator=torch.Generator().manual_seed(50 + turn)))
+        c["rng"].copy_(torch.tensor([RNG[0], turn]))
+        Y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = Q.linear_adapters_fwd(c["q"], c["set"], c["X"], c["ids"], dropout=0.1, rng=c["rng"])
+        assert torch.equal(Y, eager) and not work[0][: 512 * 1024].any()
 
 
 def test_two_graphs_on_one_workspace(gpu_lib):
