@@ -660,29 +660,69 @@ __global__ __launch_bounds__(64 * W, !POST && RT == 1 && MT <= 3 ? 4 : 2) void k
   }
 
   if (!POST) {
-    // ---- this wavefront's adapters
+    // ---- this wavefront's adapters, 32 ranks an item
     const rsrc_t rt = make_rsrc(a.T, (int64_t)M * width * 4);
-    for (int k = 0; k < count; ++k) {
-      const int one = __builtin_amdgcn_readlane(mine, k), r = __builtin_amdgcn_readlane(rank_l, k);
-      const float s = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_l), k));
-      for (int r0 = 0; r0 < r; r0 += 32) {
-        const int at = r0 + 8 * g;
-        uint4 w[RT];
+    const auto load_t = [&](int t, int one, int at, uint4& x, uint4& y) {
+      const uint32_t off = (id[t] == one && at < width) ? (uint32_t)(((16 * t + l16) * width + at) * 4) : kOOB;
+      x = bload16(rt, off), y = bload16(rt, off == kOOB ? kOOB : off + 16);
+    };
+    const auto take = [&](int t, const uint4 (&w)[RT], const uint4& x, const uint4& y, float s, bool has) {
+      const float v[8] = {__uint_as_float(x.x) * s, __uint_as_float(x.y) * s, __uint_as_float(x.z) * s,
+                          __uint_as_float(x.w) * s, __uint_as_float(y.x) * s, __uint_as_float(y.y) * s,
+                          __uint_as_float(y.z) * s, __uint_as_float(y.w) * s};
+      uint4 hi, lo;
+      split_bf16(v, hi, lo);
 #pragma unroll
-        for (int u = 0; u < RT; ++u) w[u] = load_b(k, r0, u);
+      for (int q = 0; q < RT; ++q) add_term(acc[q][t], w[q], hi, lo, has);
+    };
+    const auto scale_of = [&](int k) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_l), k)); };
+    // D items' loads in flight, as registers allow (37 rows of 24 adapters at 14336 x 4096 36.5 us one
+    // by one, 35.0 so)
+    if constexpr (MT <= 4) {
+      constexpr int D = RT == 1 && MT <= 3 ? 5 - MT : (MT <= 3 ? 4 : 3);
+      uint4 w[D][RT], u[D][MT][2];
+      int k = 0, r0 = 0, which[D], lane_of[D];
+      const auto fetch = [&](int d) {
+        which[d] = -2;
+        if (k >= count) return;
+        lane_of[d] = k;
+        which[d] = __builtin_amdgcn_readlane(mine, k);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          const bool has = id[t] == one;
-          if (!__ballot(has)) continue;
-          const uint32_t off = (has && at < width) ? (uint32_t)(((16 * t + l16) * width + at) * 4) : kOOB;
-          const uint4 x = bload16(rt, off), y = bload16(rt, off == kOOB ? kOOB : off + 16);
-          const float v[8] = {__uint_as_float(x.x) * s, __uint_as_float(x.y) * s, __uint_as_float(x.z) * s,
-                              __uint_as_float(x.w) * s, __uint_as_float(y.x) * s, __uint_as_float(y.y) * s,
-                              __uint_as_float(y.z) * s, __uint_as_float(y.w) * s};
-          uint4 hi, lo;
-          split_bf16(v, hi, lo);
+        for (int v = 0; v < RT; ++v) w[d][v] = load_b(k, r0, v);
 #pragma unroll
-          for (int u = 0; u < RT; ++u) add_term(acc[u][t], w[u], hi, lo, has);
+        for (int t = 0; t < MT; ++t) load_t(t, which[d], r0 + 8 * g, u[d][t][0], u[d][t][1]);
+        r0 += 32;
+        if (r0 >= __builtin_amdgcn_readlane(rank_l, k)) r0 = 0, ++k;
+      };
+#pragma unroll
+      for (int d = 0; d < D; ++d) fetch(d);
+      while (which[0] != -2) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          if (which[d] == -2) continue;
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const bool has = id[t] == which[d];
+            if (__ballot(has)) take(t, w[d], u[d][t][0], u[d][t][1], scale_of(lane_of[d]), has);
+          }
+          fetch(d);
+        }
+      }
+    } else {
+      for (int k = 0; k < count; ++k) {
+        const int one = __builtin_amdgcn_readlane(mine, k), r = __builtin_amdgcn_readlane(rank_l, k);
+        for (int r0 = 0; r0 < r; r0 += 32) {
+          uint4 w[RT];
+#pragma unroll
+          for (int u = 0; u < RT; ++u) w[u] = load_b(k, r0, u);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const bool has = id[t] == one;
+            if (!__ballot(has)) continue;
+            uint4 x, y;
+            load_t(t, one, r0 + 8 * g, x, y);
+            take(t, w, x, y, scale_of(k), has);
+          }
         }
       }
     }
