@@ -375,12 +375,13 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_t(StreamArgs a) {
     for (int b0 = wave; b0 < nb; b0 += kStreamWaves * D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        // blocks past the end are zeros; the wavefront's LDS accesses run in order
+        const int blk = b0 + kStreamWaves * d;
+        if (blk >= nb) break;
+        // the wavefront's LDS accesses run in order
         asm volatile("" ::: "memory");
 #pragma unroll
         for (int i = 0; i < 2; ++i) xs[64 * i + lane] = x[d][i], xs[128 + 64 * i + lane] = q[d][i];
         asm volatile("" ::: "memory");
-        const int blk = b0 + kStreamWaves * d;
         load(d, blk + kStreamWaves * D);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
