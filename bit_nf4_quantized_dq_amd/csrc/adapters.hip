@@ -82,7 +82,7 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, uint32_t wg, Sh
   uint4* qs = xs + 128;
 
   uint64_t pending = __ballot(id >= 0);
-  int cur = -1, from = 0, at = wave;  // the adapter's lane (`from`: the last one's), the block within the slice
+  int cur = -1, at = wave;  // the adapter's lane, the block within the slice
   if (len > 0 && pending) {
     cur = lowest(pending);
     const auto step = [&](int by) {  // to the item `by` further on
@@ -99,13 +99,13 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, uint32_t wg, Sh
       int which[D], blk[D];
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        const bool live = cur >= 0;
-        from = live ? cur : from;
-        which[d] = live ? __builtin_amdgcn_readlane(id, from) : -2;
+        which[d] = -2;
+        if (cur < 0) continue;
+        which[d] = __builtin_amdgcn_readlane(id, cur);
         blk[d] = sbeg + at;
-        const int r = __builtin_amdgcn_readlane(rank, from);
+        const int r = __builtin_amdgcn_readlane(rank, cur);
         const uint64_t rows_mine = __ballot(id == which[d]);  // bit m: row m of the tile
-        const rsrc_t rq = make_rsrc(reinterpret_cast<const void*>(readlane64(base, from)), live ? (int64_t)r * Kd * 2 : 0);
+        const rsrc_t rq = make_rsrc(reinterpret_cast<const void*>(readlane64(base, cur)), (int64_t)r * Kd * 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int row = 8 * i + (lane >> 3), chunk = (lane & 7) ^ ((4 * i + (lane >> 4)) & 7);
@@ -125,15 +125,16 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, uint32_t wg, Sh
               const int j = 16 * t + 8 * (lane & 1);
               if (VEC)
                 qv[d][t][i] = bload16(rq, (kr < Kd && j < r) ? (uint32_t)((kr * r + j) * 2) : kOOB);
-              else  // past the rows (or without an item) the last row again, whose product with zeros is not taken
-                qv[d][t][i] = load_row8(reinterpret_cast<const uint16_t*>(readlane64(base, from)), Kd * r, (kr < Kd ? kr : Kd - 1) * r, j, r);
+              else  // past the rows the last row again, whose product with zeros is not taken
+                qv[d][t][i] = load_row8(reinterpret_cast<const uint16_t*>(readlane64(base, cur)), Kd * r, (kr < Kd ? kr : Kd - 1) * r, j, r);
             }
           }
         }
-        if (live) step(kShrinkWaves);
+        step(kShrinkWaves);
       }
 #pragma unroll
       for (int d = 0; d < D; ++d) {
+        if (which[d] == -2) break;  // no more items
         const bool mine = id == which[d];
         // the wavefront's LDS tiles are reused item after item; its LDS accesses run in order
         asm volatile("" ::: "memory");
@@ -884,6 +885,7 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
       uint4 vv[D][4], uw[D][JT][2];
 #pragma unroll
       for (int d = 0; d < D; ++d) {
+        if (i0 + kStep * d >= count) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int m = row(i0 + kStep * d + 8 * i + (lane >> 3));
@@ -901,6 +903,7 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
       }
 #pragma unroll
       for (int d = 0; d < D; ++d) {
+        if (i0 + kStep * d >= count) break;
         // the wavefront's LDS tiles are reused chunk after chunk; its LDS accesses run in order
         asm volatile("" ::: "memory");
 #pragma unroll
