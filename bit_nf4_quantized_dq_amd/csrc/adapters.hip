@@ -239,8 +239,8 @@ __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink(ShrinkArgs a,
                                             (int64_t)(grp - gn * groups_k), threadIdx.x);
   }
 }
-// T and G in one launch: they are independent (555 rows of 6 adapters at 1040 x 4096: 16 us together, G
-// alone 9).
+// T and G in one launch: they are independent, and few rows fill the chip with neither (555 rows of 6
+// adapters at 1040 x 4096: 13 us together).
 template <int JT, bool DROP, bool VEC, int D>
 __global__ __launch_bounds__(kShrinkThreads) void k_adapter_shrink2(ShrinkArgs t, ShrinkArgs g, uint32_t n_t) {
   __shared__ ShrinkLds<JT> lds;
@@ -809,7 +809,7 @@ struct GradsArgs {
 // its ranks.  The workgroup looks through 1024 rows at a time, lists those of its adapter (ballots
 // over ids) and deals them to its wavefronts 32 by 32, so that runs of one adapter's rows are
 // shared like rows that lie apart (555 rows of 6 adapters in runs 19.4 us when each wavefront kept to
-// 256 rows, so 11.8): U [32 rows][ranks] as hi and lo BF16 parts and V [32 rows][64
+// 256 rows, so 11): U [32 rows][ranks] as hi and lo BF16 parts and V [32 rows][64
 // columns], both transposed through LDS.  Bound by HBM at low ranks (8192 rows of 4 adapters of rank 16
 // at 14336 x 4096 81 us for 303 MB), by U at high ones, which every tile of columns reads anew (4096
 // rows of rank 64 at 4096 x 4096 38 us: 134 MB of U through the L2 beside 67 MB of V).
