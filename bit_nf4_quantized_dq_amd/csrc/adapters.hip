@@ -313,6 +313,7 @@ struct StreamArgs {
   uint16_t* Y;
   int32_t lists;
   uint64_t* words;  // [workgroup][row][width], zero before and after
+  int32_t polls;    // how often a word that is not there yet is looked for
 };
 
 // T for the stream: 16 rows, 16 ranks and every `lists`-th of the rows' distinct adapters, over the
@@ -420,58 +421,97 @@ __global__ __launch_bounds__(kStreamThreads) void k_adapter_t(StreamArgs a) {
 // ---- T of a row or a few, formed by the stream's own workgroups.  Workgroup j takes element j of T
 // [M][width] (and every gridDim.x-th from there), a dot product of two rows of K, and posts it, with a
 // bit that marks it as there, to a word of its own in each workgroup's block, in the workspace's
-// head.  A workgroup reads its words after its share of the weight, waits for those that are still
-// on their way, and clears them, so the head is zero after every call.  A workgroup posts before
-// it waits, and those that post start first, so each wait ends.  (A launch for T before the stream
-// costs 2 to 4 us; T formed anew by every workgroup, which reads all of A from the L2 in each, took
-// 12.2 us for one row of 64 ranks at 4096 x 4096, here 9.8.)
+// head.  A workgroup reads its words after its share of the weight and clears them.  (A launch for T
+// before the stream costs 1 to 8 us: stream_forms_t().)
+//
+// Nothing says that the posting workgroups run while others wait: each XCD starts its workgroups on
+// its own, and launches on several streams share the chip.  So no wait depends on it.  A reader looks
+// a.polls times, then forms the elements that are missing itself, by the same sums in the same
+// order, so to the same bits.  Posts are additions to a word that is zero, and such a reader subtracts
+// from the word what it formed: whichever of the two comes first, both leave zero, and a late post
+// finds no word to spoil.  The head is zero after every call.
 constexpr uint64_t kPosted = uint64_t(1) << 32;  // beside the value's 32 bits
-constexpr int kMostPolls = 1 << 20;
 constexpr int64_t kPostedWords = 32768;
+
+// The word of a value: all NaN are one, so that two ways to form it agree.
+__device__ __forceinline__ uint64_t posted_word(float t) { return kPosted | (t == t ? __float_as_uint(t) : 0x7FC00000u); }
+
+// Thread tid's share of row m of X (its dropout applied) times a row of A, summed over its wavefront.
+template <int W>
+__device__ __forceinline__ float dot_share(const StreamArgs& a, const RngKey& key, uint32_t t2, uint32_t m,
+                                           const uint16_t* A_row, int tid) {
+  const uint32_t chunks = (uint32_t)(a.K / 8);
+  const uint4* p = reinterpret_cast<const uint4*>(A_row);
+  const uint4* x = reinterpret_cast<const uint4*>(a.X + (int64_t)m * a.K);
+  float sum = 0.f;
+  for (uint32_t c = (uint32_t)tid; c < chunks; c += 64 * W) {
+    const uint4 u = p[c];
+    uint4 v = x[c];
+    if (a.drop.threshold) v = drop8(v, key, (uint64_t)m * chunks + c, t2);
+    const uint32_t pu[4] = {u.x, u.y, u.z, u.w}, pv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum = fmaf(bf16lo_to_f32(pu[i]), bf16lo_to_f32(pv[i]), sum);
+      sum = fmaf(bf16hi_to_f32(pu[i]), bf16hi_to_f32(pv[i]), sum);
+    }
+  }
+#pragma unroll
+  for (int by = 32; by; by >>= 1) sum += __shfl_xor(sum, by);
+  return sum;
+}
 
 template <int W>
 __device__ __forceinline__ void post_t(const StreamArgs& a, int tid) {
   __shared__ float dots[W];
   const uint32_t width = (uint32_t)a.rows.width, slots = (uint32_t)a.rows.M * width, groups = gridDim.x;
   if (blockIdx.x >= slots) return;
-  const uint32_t chunks = (uint32_t)(a.K / 8), t2 = threshold_halves(a.drop.threshold);
-  const bool drop = a.drop.threshold != 0;
+  const uint32_t t2 = threshold_halves(a.drop.threshold);
   RngKey key{};
-  if (drop) key = load_rng(a.drop.rng);
+  if (a.drop.threshold) key = load_rng(a.drop.rng);
   for (uint32_t slot = blockIdx.x; slot < slots; slot += groups) {
     const uint32_t m = slot / width, j = slot - m * width;
     const int one = adapter_of(a.rows, m);
     const bool has = one >= 0 && (int)j < a.rows.table[one].r;
     float t = 0.f;
     if (has) {
-      const uint4* p = reinterpret_cast<const uint4*>(a.rows.table[one].A + (int64_t)j * a.K);
-      const uint4* x = reinterpret_cast<const uint4*>(a.X + (int64_t)m * a.K);
-      float sum = 0.f;
-      for (uint32_t c = (uint32_t)tid; c < chunks; c += 64 * W) {
-        const uint4 u = p[c];
-        uint4 v = x[c];
-        if (drop) v = drop8(v, key, (uint64_t)m * chunks + c, t2);
-        const uint32_t pu[4] = {u.x, u.y, u.z, u.w}, pv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum = fmaf(bf16lo_to_f32(pu[i]), bf16lo_to_f32(pv[i]), sum);
-          sum = fmaf(bf16hi_to_f32(pu[i]), bf16hi_to_f32(pv[i]), sum);
-        }
-      }
-#pragma unroll
-      for (int by = 32; by; by >>= 1) sum += __shfl_xor(sum, by);
+      const float sum = dot_share<W>(a, key, t2, m, a.rows.table[one].A + (int64_t)j * a.K, tid);
       if ((tid & 63) == 0) dots[tid >> 6] = sum;
       __syncthreads();
       t = dots[0];
 #pragma unroll
       for (int w = 1; w < W; ++w) t += dots[w];
       t *= a.drop.scale;
-      const uint64_t word = kPosted | __float_as_uint(t);
+      const uint64_t word = posted_word(t);
       for (uint32_t to = (uint32_t)tid; to < groups; to += 64 * W)
-        __hip_atomic_store(a.words + (uint64_t)to * slots + slot, word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+        __hip_atomic_fetch_add(a.words + (uint64_t)to * slots + slot, word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
       __syncthreads();  // dots is free again
     }
     if (a.T && tid == 0) a.T[slot] = t;
+  }
+}
+
+// The words of row k that did not arrive (bit i of a lane's `missing`: word i of its eight ranks), formed
+// by this wavefront and taken out of the memory that they would have come to.
+template <int W>
+__device__ __forceinline__ void form_missing(const StreamArgs& a, uint64_t* words, int k, int r0, uint32_t missing, int lane,
+                                             uint64_t (&t)[8]) {
+  const uint32_t t2 = threshold_halves(a.drop.threshold);
+  RngKey key{};
+  if (a.drop.threshold) key = load_rng(a.drop.rng);
+  const uint16_t* A = a.rows.table[adapter_of(a.rows, k)].A;
+  for (int q = 0; q < 32; ++q) {
+    const int from = 16 * (q >> 3) + k;  // the lane that reads rank r0 + q
+    if (!(((uint32_t)__builtin_amdgcn_readlane((int)missing, from) >> (q & 7)) & 1u)) continue;
+    float sum = 0.f;
+    for (int w = 0; w < W; ++w) {
+      const float d = dot_share<W>(a, key, t2, (uint32_t)k, A + (int64_t)(r0 + q) * a.K, 64 * w + lane);
+      sum = w ? sum + d : d;
+    }
+    const uint64_t word = posted_word(sum * a.drop.scale);
+    if (lane != from) continue;
+    __hip_atomic_fetch_add(words + r0 + q, 0 - word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = i == (q & 7) ? word : t[i];
   }
 }
 
@@ -738,22 +778,28 @@ __global__ __launch_bounds__(64 * W, !POST && RT == 1 && MT <= 3 ? 4 : 2) void k
         const int at = r0 + 8 * g, have = l16 == k && at < r ? r - at : 0;
         const uint4 w = k == wave && r0 == 0 ? ahead_b : load_b(k, r0, 0);
         uint64_t t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = i < have ? 0 : kPosted;
         bool ready = false;
-        for (int it = 0; !ready && it < kMostPolls; ++it) {
+        for (int it = 0; !ready && it < a.polls; ++it) {
           if (it) __builtin_amdgcn_s_sleep(1);
           ready = true;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            t[i] = i < have ? __hip_atomic_load(mine_t + k * width + at + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM) : kPosted;
+            if (i < have) t[i] = __hip_atomic_load(mine_t + k * width + at + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
             ready = ready && (t[i] & kPosted);
           }
         }
+        uint32_t missing = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) missing |= (t[i] & kPosted) ? 0u : 1u << i;
+        if (__ballot(missing != 0)) form_missing<W>(a, mine_t + k * width, k, r0, missing, lane, t);
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          // (never in practice: a word that did not arrive makes its row NaN instead of waiting for good)
-          v[i] = __uint_as_float((t[i] & kPosted) ? (uint32_t)t[i] : 0x7FC00000u) * s;
-          if (i < have) __hip_atomic_store(mine_t + k * width + at + i, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+          v[i] = __uint_as_float((uint32_t)t[i]) * s;
+          if (i < have && !((missing >> i) & 1u))
+            __hip_atomic_store(mine_t + k * width + at + i, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
         }
         uint4 hi, lo;
         split_bf16(v, hi, lo);
@@ -1084,9 +1130,11 @@ bool adapter_stream_fits(int64_t M, int64_t N, int64_t K) { return M <= 64 || (M
 
 // Where the stream's workgroups form T and post it: one tile of rows, few enough elements that no
 // workgroup forms more than two and that the posted words (elements times workgroups) cost less
-// than the launch that they save (4096 x 4096: one row of 16 ranks 9.4 us and 12.3 in two launches,
-// of 64 ranks 9.8 and 12.2, 8 rows 10.7 and 12.3, 16 rows 12.6 and 12.5; 14336 x 4096: one row 20 and
-// 24, 8 rows of 8 ranks, 57000 words, 33 and 24; 64 x 64, four elements each: 8.6 and 7.0).
+// than the launch that they save (replayed, here and in two launches: 4096 x 4096: one row of 64 ranks
+// 10.9 us and 12.6, 8 rows of 16 11.7 and 12.8; 14336 x 4096: one row of 16 20.2 and 23.0; 4096 x
+// 14336: 19 and 27.  At the rule's edge nothing is left of it: 4096 x 4096, one row of 128 ranks 13.8
+// and 13.1, 16 rows of 8 14.0 and 13.1.  Past it: 14336 x 4096, 8 rows of 8 ranks, 57000 words, 33 and
+// 24; 64 x 64, four elements each, 8.6 and 7.0).
 bool stream_forms_t(int64_t M, int64_t N, int32_t width) {
   const int64_t slots = M * width, groups = N / kStreamRows;
   static_assert(kPostedWords * sizeof(uint64_t) <= QLORA_WS_COUNTER_BYTES, "in the workspace's head");
@@ -1095,11 +1143,11 @@ bool stream_forms_t(int64_t M, int64_t N, int32_t width) {
 
 hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, const float* c2s, const float* mu,
                                  int64_t N, int64_t K, const uint16_t* X, const AdapterRows& rows, const DropMask& drop,
-                                 float* T, uint16_t* Y, void* head, const Nf4Tables& tab, hipStream_t st) {
+                                 float* T, uint16_t* Y, void* head, int32_t polls, const Nf4Tables& tab, hipStream_t st) {
   if (rows.M > kStreamMaxRows) return hipErrorInvalidValue;
   const int tiles = (int)((rows.M + kRowTile - 1) / kRowTile), ranks = (rows.width + 15) / 16;
   const StreamArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, rows, drop, T, Y,
-                     std::min((int)rows.count, kRowTile), static_cast<uint64_t*>(head)};
+                     std::min((int)rows.count, kRowTile), static_cast<uint64_t*>(head), polls};
   const bool wide = N / kStreamRows > 512;  // more than fit at once
   if (stream_forms_t(rows.M, N, rows.width))
     return wide ? stream_go<4, 1, 1, true, 4>(a, tab, st) : stream_go<8, 1, 1, true, 4>(a, tab, st);

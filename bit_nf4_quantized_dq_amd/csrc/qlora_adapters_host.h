@@ -66,12 +66,13 @@ hipError_t launch_shrink_both(const AdapterRows& rows, const uint16_t* X, int64_
 
 // ---- few rows: Y by a launch that streams the weight once (E4M3 constants).  T (FP32 [M, width]) is
 // written by a launch before it, or, where stream_forms_t(), by the same one (T may then be NULL),
-// by way of the workspace's head.
+// by way of the workspace's head, where a workgroup looks `polls` times for an element before it forms
+// it itself.
 bool adapter_stream_fits(int64_t M, int64_t N, int64_t K);
 bool stream_forms_t(int64_t M, int64_t N, int32_t width);
 hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, const float* c2s, const float* mu,
                                  int64_t N, int64_t K, const uint16_t* X, const AdapterRows& rows, const DropMask& drop,
-                                 float* T, uint16_t* Y, void* head, const Nf4Tables& tab, hipStream_t st);
+                                 float* T, uint16_t* Y, void* head, int32_t polls, const Nf4Tables& tab, hipStream_t st);
 
 // ---- many rows: the GEMM over the decoded copy (gemm_nt.hip), its accumulators started from the
 // adapters' term, scale s_a U W_a^T (fwd: U = T, W_a = B_a [F, r]; else U = G, W_a = A_a^T of
