@@ -146,14 +146,16 @@ __device__ __forceinline__ bool adapter_rows(const AdapterHead& h, int64_t F, in
     if (r0 >= r) next_adapter();
     if (cur >= 0) load();
 #pragma unroll
-    for (int j = 0; j < TJ; ++j)
+    for (int i = 0; i < TI; ++i) {
+      const bf16x8_t wl = finite_only(wo[i]);
 #pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        const f32x16_t t = mfma32(wo[i], lo[j], mfma32(wo[i], hi[j], f32x16_t{}));
+      for (int j = 0; j < TJ; ++j) {
+        const f32x16_t t = mfma32(wl, lo[j], mfma32(wo[i], hi[j], f32x16_t{}));
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] += mine[j] ? t[q] : 0.f;
         __builtin_amdgcn_sched_barrier(0);  // one tile's temporaries at a time
       }
+    }
   }
   return any;
 }

@@ -518,7 +518,8 @@ __device__ __forceinline__ void form_missing(const StreamArgs& a, uint64_t* word
 // acc += B's 16 rows times hi + lo (eight ranks for each lane's row of X) where `has`: the products of
 // other rows are not taken.
 __device__ __forceinline__ void add_term(f32x4_t& acc, const uint4& w, const uint4& hi, const uint4& lo, bool has) {
-  const f32x4_t p = mfma16x16x32(as_bf16x8(w), as_bf16x8(lo), mfma16x16x32(as_bf16x8(w), as_bf16x8(hi), f32x4_t{0.f, 0.f, 0.f, 0.f}));
+  const f32x4_t p = mfma16x16x32(finite_only(as_bf16x8(w)), as_bf16x8(lo),
+                                 mfma16x16x32(as_bf16x8(w), as_bf16x8(hi), f32x4_t{0.f, 0.f, 0.f, 0.f}));
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i] += has ? p[i] : 0.f;
 }
@@ -952,6 +953,7 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
         if (i0 + kStep * d >= count) break;
         // the wavefront's LDS tiles are reused chunk after chunk; its LDS accesses run in order
         asm volatile("" ::: "memory");
+        uint32_t most = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int in = 8 * i + (lane >> 3), ct = (lane & 7) >> 1, half = lane & 1;
@@ -960,6 +962,7 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
             const int m = row(i0 + kStep * d + in);
             v = drop8(v, key, (uint64_t)((first + (m < 0 ? 0 : m)) * (C / 8) + c0 / 8 + (lane & 7)), t2);
           }
+          most = most_halves(most, v);
           *reinterpret_cast<uint4*>(vt + ct * kVTile + in * 32 + 16 * half) = v;
         }
 #pragma unroll
@@ -976,12 +979,20 @@ __device__ __forceinline__ void grads_body(const GradsArgs& a, GradsLds<JT>& lds
         bf16x8_t b[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) b[q] = tr_operand(vt + q * kVTile, lane & 15, 8 * (lane >> 4));
+        const auto add = [&](const char* u) {
 #pragma unroll
-        for (int t = 0; t < JT; ++t) {
-          const bf16x8_t hi = tr_operand(ut + t * kVTile, lane & 15, 8 * (lane >> 4)), lo = tr_operand(ut + (JT + t) * kVTile, lane & 15, 8 * (lane >> 4));
+          for (int t = 0; t < JT; ++t) {
+            const bf16x8_t v = tr_operand(u + t * kVTile, lane & 15, 8 * (lane >> 4));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[t][q] = mfma16x16x32(lo, b[q], mfma16x16x32(hi, b[q], acc[t][q]));
+            for (int q = 0; q < 4; ++q) acc[t][q] = mfma16x16x32(v, b[q], acc[t][q]);
+          }
+        };
+        add(ut);
+        if (some_not_finite(most)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) b[q] = finite_only(b[q]);
         }
+        add(ut + JT * kVTile);
         asm volatile("" ::: "memory");
       }
     }

@@ -53,8 +53,13 @@ __device__ __forceinline__ uint4 drop8(uint4 v, const RngKey& key, uint64_t bloc
                     v.w & keep_halves(w.w, t2));
 }
 
-// ---- FP32 values as hi + lo of BF16: sixteen bits of significand, so that a product on the
-// matrix cores loses 2^-17 of the value instead of 2^-9.  An infinite value has lo = 0.
+// ---- FP32 values as hi + lo of BF16, so that a product on the matrix cores loses little of them: hi is
+// off by at most half a step, 2^-8 of the value, and lo, which is that difference, by half a step
+// of its own, 2^-17 of the value.  An infinite value has lo = 0, and one that rounds past BF16's
+// largest (3.39e38) counts as infinite.
+//
+// Times an infinite operand, hi gives the infinity (or NaN) of the whole product, and lo, whose sign
+// is its own, must not: lo meets an operand without its infinities and NaN (finite_only()).
 __device__ __forceinline__ void split_bf16(const float f[8], uint4& hi, uint4& lo) {
   uint32_t h[4], l[4];
 #pragma unroll
@@ -67,6 +72,32 @@ __device__ __forceinline__ void split_bf16(const float f[8], uint4& hi, uint4& l
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// The larger of each half of `most` and of the magnitudes of the BF16 values of w.
+__device__ __forceinline__ uint32_t most_halves(uint32_t most, uint32_t w) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, most), __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu)));
+}
+__device__ __forceinline__ uint32_t most_halves(uint32_t most, const uint4& v) {
+  return most_halves(most_halves(most_halves(most_halves(most, v.x), v.y), v.z), v.w);
+}
+// Whether some lane's magnitudes reach infinity (or NaN); the same for the whole wavefront.
+__device__ __forceinline__ bool some_not_finite(uint32_t most) {
+  return __ballot(most >= 0x7F800000u || (most & 0xFFFFu) >= 0x7F80u) != 0;
+}
+// Eight BF16 values, zeros for those that are not finite.
+__device__ __forceinline__ bf16x8_t finite_only(const bf16x8_t& v) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  const u16x2 one = {1, 1}, most = {0x7F7F, 0x7F7F};
+  const uint4 u = __builtin_bit_cast(uint4, v);
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const u16x2 over = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu), most);
+    w[i] = __builtin_bit_cast(uint32_t, (u16x2)(__builtin_bit_cast(u16x2, w[i]) * __builtin_elementwise_sub_sat(one, over)));
+  }
+  return as_bf16x8(make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 // ---- operands

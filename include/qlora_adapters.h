@@ -82,7 +82,8 @@ int qlora_adapters_workspace_size(int op, int64_t M, const qlora_adapters_t *set
  *   T_save: device FP32 [M, t_width], 16-byte aligned, receives T for the backward (zeros past a
  *        row's rank and for rows without an adapter); may be NULL.
  * A row's result depends on its own adapter only: values of others that are not finite stay
- * with the rows that name them.
+ * with the rows that name them.  Infinite operands give the infinities and NaN that the formulas
+ * give, here and in the backward (a T or G past BF16's largest, 3.39e38, counts as infinite).
  * ws: qlora_adapters_workspace_size(QLORA_OP_FWD) bytes.
  * Errors: INVALID_ARG (null or misaligned pointer, Y overlapping X, M outside [1, 2^23], dropout
  * outside [0, 1) or so near 1 that t would be 65536), BAD_SHAPE (also where the weight's shape is not the

@@ -91,7 +91,7 @@ def bwd(what, A, B, alpha, X, dY, ids=None, p=0.0, rng=(0, 0), T=None):
         G, Gm = dY[at] @ Ba, dY[at].abs() @ Ba.abs()
         back, backm = s * (G @ Aa), abs(s) * (Gm @ Aa.abs())
         dX[at] += back if gate is None else torch.where(gate[at] > 0, back * gate[at], 0.0)
-        branch[at] = backm if gate is None else backm * gate[at]
+        branch[at] = backm if gate is None else torch.where(gate[at] > 0, backm * gate[at], 0.0)
         t = Xd[at] @ Aa.T if T is None else T[at, :r].to(F64)
         tm = Xd[at].abs() @ Aa.abs().T if T is None else t.abs()
         out["dA"].append(s * (G.T @ Xd[at]))
