@@ -125,8 +125,9 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, uint32_t wg, Sh
               const int j = 16 * t + 8 * (lane & 1);
               if (VEC)
                 qv[d][t][i] = bload16(rq, (kr < Kd && j < r) ? (uint32_t)((kr * r + j) * 2) : kOOB);
-              else  // past the rows the last row again, whose product with zeros is not taken
-                qv[d][t][i] = load_row8(reinterpret_cast<const uint16_t*>(readlane64(base, cur)), Kd * r, (kr < Kd ? kr : Kd - 1) * r, j, r);
+              else  // zeros past the rows (in the reduction, dY's zeros there would not do beside an infinity)
+                qv[d][t][i] = load_row8(reinterpret_cast<const uint16_t*>(readlane64(base, cur)), Kd * r, (kr < Kd ? kr : Kd - 1) * r, j,
+                                        kr < Kd ? r : 0);
             }
           }
         }

@@ -71,3 +71,49 @@ def test_infinities_are_the_definitions(gpu_lib, shape, what, p):
         agree(c["set"].dB[i], b["dB"][i], HALF * b["dB"][i].abs() + (ADD * (K + M + 16) + SPLIT) * b["dB_sum"][i], f"dB[{i}]")
     # the infinities came through
     assert any(t.isinf().any() for t in (f["Y"], b["dX"], *b["dA"], *b["dB"]))
+
+
+@pytest.mark.parametrize("ranks", [[16, 8, 24], [16, 5, 24], [5, 16, 24]])
+@pytest.mark.parametrize("M,N,K", [(4, 1040, 320), (40, 272, 320), (140, 272, 320), (700, 592, 128)])
+def test_an_infinity_in_the_last_row_of_b(gpu_lib, M, N, K, ranks):
+    """d_out past a multiple of 64: G = dY B takes nothing from beyond B's last row, whatever it holds
+    and whatever ranks the set's other adapters have."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    print(M, N, K, ranks, flush=True)
+    c = make(9, M, N, K, ranks, "tokens")
+    c["ids"] = torch.arange(M, dtype=torch.int32, device="cuda") % 3
+    c["B"][0][-1, 2] = INF
+    dX = Q.linear_adapters_bwd(c["q"], c["set"], c["X"], c["dY"], c["ids"])
+    b = AO.bwd(c["what"].cpu(), [t.cpu() for t in c["A"]], [t.cpu() for t in c["B"]], c["alpha"], c["X"].cpu(), c["dY"].cpu(), c["ids"].cpu())
+    r = c["set"].t_width
+    assert b["dX"].isinf().any()
+    agree(dX, b["dX"], HALF * b["dX"].abs() + ADD * (N + 8) * b["dX_base"] + (ADD * (N + r + 16) + SPLIT) * b["dX_branch"], "dX")
+    for i in range(len(ranks)):
+        agree(c["set"].dA[i], b["dA"][i], HALF * b["dA"][i].abs() + (ADD * (N + M + 16) + SPLIT) * b["dA_sum"][i], f"dA[{i}]")
+
+
+@pytest.mark.parametrize("p", [0.0, 0.1])
+@pytest.mark.parametrize("shape", CASES)
+def test_poisoned_adapter_reaches_its_own_rows_only(gpu_lib, shape, p):
+    """Every path, ranks of any kind, dropout: rows that name other adapters, and the other adapters'
+    gradients, have the bits that they have beside a finite one."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    print(shape, p, flush=True)
+    M, N, K, ranks = shape
+    c = make(11, M, N, K, ranks, "tokens")
+    ids = torch.arange(M, dtype=torch.int32, device="cuda") % 4 - 1
+    kw = dict(dropout=p, rng=c["rng"] if p else None)
+    out = []
+    for poison in (False, True):
+        if poison:
+            A, B = c["A"][1], c["B"][1]
+            A[0], A[-1, 7], A[:, -1] = float("nan"), INF, -INF
+            B[-1], B[5], B[:, 1] = float("nan"), INF, -INF
+        T = torch.empty(M, c["set"].t_width, device="cuda")
+        Y = Q.linear_adapters_fwd(c["q"], c["set"], c["X"], ids, T_save=T, **kw)
+        dX = Q.linear_adapters_bwd(c["q"], c["set"], c["X"], c["dY"], ids, **kw)
+        clean = ids != 1
+        out.append([Y[clean], T[clean], dX[clean]] + [c["set"].dA[a].clone() for a in (0, 2)] + [c["set"].dB[a].clone() for a in (0, 2)])
+    assert all(t.isfinite().all() for t in out[0]) and all(map(torch.equal, *out))
