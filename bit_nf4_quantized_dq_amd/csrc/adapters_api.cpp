@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 
 #include "qlora_adapters_host.h"
 
@@ -21,6 +22,16 @@ inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t
 inline bool apart(const void* p, size_t bytes, const void* q, size_t other) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return a + bytes <= b || b + other <= a;
+}
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+// `out` shares no byte with any of `with` (null ranges are none).
+inline bool apart_from(const Range& out, std::initializer_list<Range> with) {
+  for (const Range& r : with)
+    if (out.p && r.p && !apart(out.p, out.bytes, r.p, r.bytes)) return false;
+  return true;
 }
 int hip_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP; }
 inline bool type_ok(int type) { return type == QLORA_BF16 || type == QLORA_F32; }
@@ -175,7 +186,9 @@ int qlora_adapters_fwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   int st = check_call(Wq, set, M, ids, dropout, rng, &drop);
   if (st) return st;
   if (!X || !Y || !aligned(X, 16) || !aligned(Y, 16) || !aligned(T_save, 16)) return QLORA_ERR_INVALID_ARG;
-  if (!apart(X, 2 * (size_t)M * Wq->d_in, Y, 2 * (size_t)M * Wq->d_out)) return QLORA_ERR_INVALID_ARG;
+  const Range x{X, 2 * (size_t)M * Wq->d_in}, y{Y, 2 * (size_t)M * Wq->d_out}, t{T_save, sizeof(float) * (size_t)M * width_of(set)};
+  const Range id{ids, sizeof(int32_t) * (size_t)M}, words{drop.threshold ? rng : nullptr, 2 * sizeof(uint64_t)};
+  if (!apart_from(y, {x, id, words}) || !apart_from(t, {x, y, id, words})) return QLORA_ERR_INVALID_ARG;
   const int dq = Wq->dq_format;
   const Layout L = layout(false, M, set, dq);
   if ((st = check_ws(ws, ws_bytes, L.total))) return st;
@@ -218,7 +231,8 @@ int qlora_adapters_bwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   if (!X || !dY || !aligned(X, 16) || !aligned(dY, 16) || !aligned(dX, 16) || !aligned(T_saved, 16))
     return QLORA_ERR_INVALID_ARG;
   const size_t x_bytes = 2 * (size_t)M * Wq->d_in;
-  if (dX && (!apart(dX, x_bytes, X, x_bytes) || !apart(dX, x_bytes, dY, 2 * (size_t)M * Wq->d_out)))
+  if (!apart_from({dX, x_bytes}, {{X, x_bytes}, {dY, 2 * (size_t)M * Wq->d_out}, {T_saved, sizeof(float) * (size_t)M * width_of(set)},
+                                  {ids, sizeof(int32_t) * (size_t)M}, {drop.threshold ? rng : nullptr, 2 * sizeof(uint64_t)}}))
     return QLORA_ERR_INVALID_ARG;
   const int dq = Wq->dq_format;
   const Layout L = layout(true, M, set, dq);
@@ -281,6 +295,7 @@ int qlora_dropout(const void* x, int x_type, int64_t n, float dropout, const uin
     return (p == out && bytes == ob) || apart(p, (size_t)n * bytes, out, (size_t)n * ob);
   };
   if (!separate(x, xb) || (residual && !separate(residual, ob))) return QLORA_ERR_INVALID_ARG;
+  if (drop.threshold && !apart(rng, 2 * sizeof(uint64_t), out, (size_t)n * ob)) return QLORA_ERR_INVALID_ARG;
   return hip_status(launch_dropout(x, x_type == QLORA_F32, n, drop, residual, out, out_type == QLORA_F32, stream));
 }
 

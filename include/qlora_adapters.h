@@ -85,9 +85,9 @@ int qlora_adapters_workspace_size(int op, int64_t M, const qlora_adapters_t *set
  * with the rows that name them.  Infinite operands give the infinities and NaN that the formulas
  * give, here and in the backward (a T or G past BF16's largest, 3.39e38, counts as infinite).
  * ws: qlora_adapters_workspace_size(QLORA_OP_FWD) bytes.
- * Errors: INVALID_ARG (null or misaligned pointer, Y overlapping X, M outside [1, 2^23], dropout
- * outside [0, 1) or so near 1 that t would be 65536), BAD_SHAPE (also where the weight's shape is not the
- * set's), UNSUPPORTED, WORKSPACE, HIP. */
+ * Errors: INVALID_ARG (null or misaligned pointer, Y or T_save overlapping X, ids, rng or each other,
+ * M outside [1, 2^23], dropout outside [0, 1) or so near 1 that t would be 65536), BAD_SHAPE (also where
+ * the weight's shape is not the set's), UNSUPPORTED, WORKSPACE, HIP. */
 int qlora_adapters_fwd(const qlora_nf4dq_t *Wq, const qlora_adapters_t *set, const uint16_t *X, int64_t M,
                        const int32_t *ids, float dropout, const uint64_t *rng, uint16_t *Y, float *T_save, void *ws,
                        size_t ws_bytes, hipStream_t stream);
@@ -101,8 +101,8 @@ int qlora_adapters_fwd(const qlora_nf4dq_t *Wq, const qlora_adapters_t *set, con
  * adapter).  dY [M, d_out], X [M, d_in], dX: device BF16, 16-byte aligned.  T_saved: the
  * forward's, or NULL to recompute it.  dropout and rng as in the forward.
  * ws: qlora_adapters_workspace_size(QLORA_OP_BWD) bytes.
- * Errors: as the forward, INVALID_ARG also for a set without gradients and for dX overlapping X
- * or dY. */
+ * Errors: as the forward, INVALID_ARG also for a set without gradients and for dX overlapping X, dY,
+ * T_saved, ids or rng. */
 int qlora_adapters_bwd(const qlora_nf4dq_t *Wq, const qlora_adapters_t *set, const uint16_t *X, const uint16_t *dY,
                        int64_t M, const int32_t *ids, float dropout, const uint64_t *rng, const float *T_saved,
                        uint16_t *dX, void *ws, size_t ws_bytes, hipStream_t stream);
@@ -113,7 +113,7 @@ int qlora_adapters_bwd(const qlora_nf4dq_t *Wq, const qlora_adapters_t *set, con
  *   elements.  out may be residual, and x where the types agree; otherwise they do not overlap.
  *   One FP32 fused multiply-add an element, rounded once to out_type.  n == 0 is a no-op.
  * No workspace.  Errors: INVALID_ARG (n negative or over 2^40, null or misaligned pointer,
- * dropout as above, partial overlap), UNSUPPORTED (unknown type), HIP. */
+ * dropout as above, partial overlap, out over rng), UNSUPPORTED (unknown type), HIP. */
 int qlora_dropout(const void *x, int x_type, int64_t n, float dropout, const uint64_t *rng, const void *residual,
                   void *out, int out_type, hipStream_t stream);
 
