@@ -67,6 +67,24 @@ def _on_device(fn):
     return call
 
 
+def _grads_apart(A, B, dA, dB) -> None:
+    """Refuses gradients that share memory with one another or with an adapter (the kernels write
+    them in no order)."""
+    spans = []
+    for name, ts in (("A", A), ("B", B), ("dA", dA or ()), ("dB", dB or ())):
+        spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{name}[{i}]") for i, t in enumerate(ts)]
+    read, written = (0, ""), (0, "")  # where the spans so far end
+    for start, end, name in sorted(spans):
+        grad = name[0] == "d"
+        for over, other in ((written,) if not grad else (written, read)):
+            if start < over:
+                raise ValueError(f"{name}: overlaps {other}")
+        if grad:
+            written = max(written, (end, name))
+        else:
+            read = max(read, (end, name))
+
+
 class AdapterSet:
     """The adapters of one linear [d_out, d_in], laid out once: a device table that
     linear_adapters_fwd and _bwd go by.  It holds the tensors (their values may change, their memory
@@ -74,8 +92,8 @@ class AdapterSet:
 
     A[i] [r_i, d_in], B[i] [d_out, r_i]: contiguous BF16 CUDA tensors, ranks 1..128 that may differ.
     alpha: one number, or one per adapter (the branch is scaled by alpha / r).  dA, dB: tensors of
-    the same shapes for the backward's gradients (views of a flat gradient buffer, say); None: a
-    set that is not trained."""
+    the same shapes for the backward's gradients (views of a flat gradient buffer, say), which
+    overlap neither each other nor an adapter; None: a set that is not trained."""
 
     def __init__(self, A, B, alpha, dA=None, dB=None):
         self.A, self.B = list(A), list(B)
@@ -101,6 +119,7 @@ class AdapterSet:
             if self.dA is not None:
                 specs += [(self.dA[i], _BF16, f"dA[{i}]", (r, self.d_in)), (self.dB[i], _BF16, f"dB[{i}]", (self.d_out, r))]
         _validate(specs, self.device)
+        _grads_apart(self.A, self.B, self.dA, self.dB)
         L = _lib()
         VP = ctypes.c_void_p * n
         ptrs = lambda ts: None if ts is None else VP(*[t.data_ptr() for t in ts])  # noqa: E731

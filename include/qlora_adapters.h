@@ -56,7 +56,8 @@ int qlora_adapters_size(int count, size_t *table_bytes);
  *   A[i] [r[i], d_in], B[i] [d_out, r[i]]: device BF16 adapters, 16-byte aligned (B[i] by its
  *   elements only where r[i] is no multiple of 8); alpha[i]: the branch is scaled by alpha / r.
  *   dA, dB: device BF16 of the same shapes that qlora_adapters_bwd writes, aligned by their
- *   elements; both NULL for a set that is never trained.
+ *   elements; both NULL for a set that is never trained.  They overlap neither each other nor any
+ *   operand of the calls (not checked here).
  * Errors: INVALID_ARG (null or misaligned pointer, count, r outside [1, 128], alpha not finite),
  * BAD_SHAPE (as qlora.h), WORKSPACE (table NULL or too small), HIP. */
 int qlora_adapters_init(int count, const uint16_t *const *A, const uint16_t *const *B, const int32_t *r,

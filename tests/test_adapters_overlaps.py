@@ -4,6 +4,7 @@ written (no GPU is touched: the pointers here are never dereferenced)."""
 import ctypes
 
 import pytest
+import torch
 
 from bit_nf4_quantized_dq_amd import _adapters as AD
 from bit_nf4_quantized_dq_amd._binding import _Nf4dq
@@ -61,3 +62,16 @@ def test_dropout_over_its_generator(L):
     x, rng = BASE, BASE + (1 << 16)
     for off in (-198, -16, 0, 8, 14):
         assert L.qlora_dropout(x, 0, 100, 0.1, rng, None, rng + off, 0, None) == INVALID, off
+
+
+def test_gradients_of_a_set():
+    flat = torch.zeros(4096, dtype=torch.bfloat16)
+    cut = lambda a, n: flat[a:a + n]  # noqa: E731
+    A, B, dA, dB = [cut(0, 64), cut(64, 64)], [cut(128, 64), cut(192, 64)], [cut(256, 64), cut(320, 64)], [cut(384, 64), cut(448, 64)]
+    AD._grads_apart(A, B, dA, dB)
+    AD._grads_apart([A[0], A[0]], [B[0], B[0]], dA, dB)  # one adapter twice, each with gradients of its own
+    AD._grads_apart(A, B, None, None)
+    for bad in ((A, B, [dA[0], dA[0]], dB), (A, B, dA, [dB[0], cut(447, 64)]), (A, B, dA, [cut(127, 64), dB[1]]), (A, B, A, dB),
+                (A, B, [cut(319, 64), cut(319 - 32, 64)], dB), ([cut(256, 512), A[1]], B, dA, dB)):
+        with pytest.raises(ValueError, match="overlap"):
+            AD._grads_apart(*bad)
