@@ -1,0 +1,78 @@
+"""Long reductions of the linear with many adapters, with tolerances that bind.  Rows of X (or of dY)
+are zero but for a few columns, the first and the last ones among them: zeros add exactly, so
+an element's sum has as many roundings as it has terms that are not zero, whatever the length.
+Beside that the tolerances are test_gpu_adapters' own.  Each is also asserted to lie well below the
+values that it is for."""
+
+import pytest
+import torch
+
+from oracle import adapters_oracle as AO
+from test_gpu_adapters import ADD, HALF, RNG, SPLIT
+
+pytestmark = pytest.mark.gpu
+FEW = 12
+
+
+def sparse(gen, M, n):
+    """[M, n] BF16: FEW values a row, in the first and last columns and spread over the rest."""
+    at = torch.randint(0, n, (M, FEW), generator=gen, device="cuda")
+    at[:, 0], at[:, 1] = 0, n - 1
+    at[:, 2] = n - 1 - torch.arange(M, device="cuda") % 64
+    at[:, 3] = torch.arange(M, device="cuda") * (n // M)
+    x = torch.zeros(M, n, dtype=torch.bfloat16, device="cuda")
+    return x.scatter_(1, at, torch.randn(M, FEW, generator=gen, device="cuda").bfloat16())
+
+
+def near(got, ref, tol, name):
+    got = got.double()
+    bad = ~((got - ref).abs() <= tol)
+    assert not bad.any(), (name, int(bad.sum()), bad.nonzero()[0].tolist(), float(got[bad][0]), float(ref[bad][0]), float(tol[bad][0]))
+    # a twentieth of the values: a lost term or a wrong column cannot pass
+    some = ref[ref != 0].abs()
+    assert len(some) and float(tol[ref != 0].median()) < 0.05 * float(some.median()), name
+
+
+# rows, d_out, d_in, ranks, dropout: long reductions of T and Y, then of dX and G
+@pytest.mark.parametrize("M,N,K,ranks,p", [
+    (1, 16, 2**20 + 64, [16, 5], 0.0), (3, 48, 2**20 + 64, [16, 5], 0.2), (40, 16, 2**20 + 64, [40, 8], 0.0), (100, 32, 2**20 + 64, [16, 8], 0.0),
+    (260, 16, 2**20 + 64, [8, 16], 0.0), (70, 16, 2**22, [16, 8], 0.0), (270, 16, 2**22, [24, 3], 0.0), (140, 1024, 2**22, [8, 16], 0.0),
+    (1, 2**20 + 16, 64, [16, 5], 0.2), (40, 2**20 + 16, 64, [16, 5], 0.2), (100, 2**20 + 16, 64, [8, 40], 0.0), (260, 2**20 + 16, 64, [16, 5], 0.2),
+    (70, 2**22, 64, [16, 8], 0.0), (270, 2**22, 64, [24, 3], 0.0), (140, 2**22, 1024, [8, 16], 0.0),
+])
+def test_long_reductions(gpu_lib, M, N, K, ranks, p):
+    import bit_nf4_quantized_dq_amd as Q
+
+    print(M, N, K, ranks, p, flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    randn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    long_in = K > N
+    q = Q.quantize(randn(N, K))
+    A, B = [randn(r, K).bfloat16() for r in ranks], [randn(N, r).bfloat16() for r in ranks]
+    alpha = [float(r) for r in ranks]
+    X = sparse(gen, M, K) if long_in else randn(M, K).bfloat16()
+    dY = randn(M, N).bfloat16() if long_in else sparse(gen, M, N)
+    ids = torch.randint(-1, len(ranks), (M,), generator=gen, device="cuda", dtype=torch.int32)
+    ids[0] = 0
+    s = Q.AdapterSet(A, B, alpha, dA=[torch.empty_like(t) for t in A], dB=[torch.empty_like(t) for t in B])
+    kw = dict(dropout=p, rng=torch.tensor(RNG, device="cuda") if p else None)
+    T = torch.empty(M, s.t_width, device="cuda")
+    Y = Q.linear_adapters_fwd(q, s, X, ids, T_save=T, **kw)
+    what = Q.dequantize(q)
+    k, n, r = (FEW, N, s.t_width) if long_in else (K, FEW, s.t_width)
+    ref = AO.fwd(what, A, B, alpha, X, ids, p, RNG)
+    near(T, ref["T"], 2.0**-23 * ref["T"].abs() + ADD * (k + 8) * ref["T_sum"], "T")
+    near(Y, ref["Y"], HALF * ref["Y"].abs() + ADD * (k + 8) * ref["Y_base"] + (ADD * (k + r + 16) + SPLIT) * ref["Y_branch"], "Y")
+    del ref, Y
+    dX = Q.linear_adapters_bwd(q, s, X, dY, ids, **kw)
+    ref = AO.bwd(what, A, B, alpha, X, dY, ids, p, RNG)
+    near(dX, ref["dX"], HALF * ref["dX"].abs() + ADD * (n + 8) * ref["dX_base"] + (ADD * (n + r + 16) + SPLIT) * ref["dX_branch"], "dX")
+    for i in range(len(ranks)):
+        if not (ids == i).any():
+            assert not s.dA[i].any() and not s.dB[i].any()
+            continue
+        near(s.dA[i], ref["dA"][i], HALF * ref["dA"][i].abs() + (ADD * (n + M + 16) + SPLIT) * ref["dA_sum"][i], f"dA[{i}]")
+        near(s.dB[i], ref["dB"][i], HALF * ref["dB"][i].abs() + (ADD * (k + M + 16) + SPLIT) * ref["dB_sum"][i], f"dB[{i}]")
+    dA, dB = [t.clone() for t in s.dA], [t.clone() for t in s.dB]
+    assert torch.equal(dX, Q.linear_adapters_bwd(q, s, X, dY, ids, **kw))
+    assert all(map(torch.equal, dA + dB, s.dA + s.dB))
