@@ -2,7 +2,6 @@
 // include/qlora_adapters.h): argument checks, workspace layouts and plans; the kernels and their
 // launches are in adapters.hip, adapters_gemm.hip, gemm_nt.hip and dropout.hip.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
@@ -78,10 +77,6 @@ bool stream_path(int64_t M, int64_t N, int64_t K, int dq) { return dq == QLORA_D
 // The product over the codes, for the rows between few and many.
 bool codes_path(int64_t M, int64_t F, int64_t Kr, int dq) { return dq == QLORA_DQ_E4M3 && adapter_gemm_fits(M, F, Kr); }
 
-// How often a workgroup of the few rows' launch looks for an element of T that another one forms
-// (about a microsecond each) before it forms it itself.
-std::atomic<int32_t> g_posted_polls{512};
-
 // ---- workspaces: the counter head, then T and G, then what the steps need in turn
 struct Layout {
   size_t t, g, spart, gspart, wcopy, gpart, grads, total;
@@ -121,9 +116,6 @@ ShrinkDecode decode_args(const qlora_nf4dq_t* Wq, uint16_t* out) {
 }  // namespace
 
 extern "C" {
-
-// Not part of the ABI: a test sets 0, so that every workgroup forms T for itself.
-void qlora_posted_polls(int32_t polls) { g_posted_polls.store(polls < 0 ? 0 : polls, std::memory_order_relaxed); }
 
 int qlora_adapters_size(int count, size_t* table_bytes) {
   if (!table_bytes || count < 1 || count > QLORA_MAX_ADAPTERS) return QLORA_ERR_INVALID_ARG;
@@ -202,8 +194,7 @@ int qlora_adapters_fwd(const qlora_nf4dq_t* Wq, const qlora_adapters_t* set, con
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(Wq->codes);
   if (stream_path(M, N, K, dq))
     return hip_status(launch_adapter_stream(codes, Wq->code8, Wq->c2s, Wq->mu, N, K, X, rows, drop,
-                                            stream_forms_t(M, N, rows.width) ? T_save : T, Y, ws, g_posted_polls.load(std::memory_order_relaxed),
-                                            tab, stream));
+                                            stream_forms_t(M, N, rows.width) ? T_save : T, Y, ws, posted_polls(), tab, stream));
   const AdapterHead head{rows, T, 0, 1.f, DropMask{}};
   float* gpart = reinterpret_cast<float*>(base + L.gpart);
   if (codes_path(M, N, K, dq)) {

@@ -4,6 +4,7 @@
 // constants for double quantization, folded from the per-exponent integer sums that the
 // first quantize pass gathers.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -261,6 +262,9 @@ TimingState& timing() {
 }  // namespace
 
 namespace qlora {
+
+std::atomic<int32_t> g_posted_polls{512};
+int32_t posted_polls() { return g_posted_polls.load(std::memory_order_relaxed); }
 
 int check_weight(const qlora_nf4dq_t* Wq) { return check_wq(Wq); }
 bool linear_shape_ok(int64_t d_out, int64_t d_in) { return shape_ok(d_out, d_in); }
@@ -771,6 +775,9 @@ int qlora_e4m3_encode(const float* in, uint8_t* out, int64_t n, hipStream_t stre
   if (n == 0) return QLORA_OK;
   return hip_status(launch_e4m3_encode(in, out, n, stream));
 }
+
+// Not part of the ABI: a test sets 0, so that every workgroup forms what others post to it.
+void qlora_posted_polls(int32_t polls) { g_posted_polls.store(polls < 0 ? 0 : polls, std::memory_order_relaxed); }
 
 int qlora_timing_enable(int kernel_mask) {
   TimingState& T = timing();

@@ -27,13 +27,18 @@
 // each wavefront takes the dot product of its X slices with its slice of row j of A in
 // registers (8 products per lane, then a fixed-order sum across the lanes) and parks it in LDS
 // before the barrier that publishes the X slices, so T[m][j] is complete right after that
-// barrier, while the codes are still in flight.  The workgroup then writes bf16(s T[m][j])
-// with a tag into a private block of words of every workgroup, in the workspace head.  Each
+// barrier, while the codes are still in flight.  The workgroup then posts bf16(s T[m][j])
+// with a tag to a private block of words of every workgroup, in the workspace head.  Each
 // workgroup, after its rows, reads its M x r words until all carry the tag, applies (s T) B^T
-// for its rows on MFMA, writes Y and then clears the words.  Each word block is read and cleared by its one owner, so the head is zero again
-// after every call and a stale T is never taken for a new one, with no counter shared between
-// workgroups.  Workgroups 0 .. r-1 are dispatched first and write T before they wait on
-// anything, so no reader waits on a workgroup that has not started.
+// for its rows on MFMA, writes Y and then clears the words.  Each word block is read and cleared by
+// its one owner, with no counter shared between workgroups.
+//
+// Nothing says that the posting workgroups run while others wait: each XCD starts its workgroups on
+// its own, and launches on several streams share the chip.  So no wait depends on it.  A reader looks
+// `polls` times, then forms the words that are missing itself, by the same sums in the same order,
+// so to the same bits.  Posts are additions to a word that is zero, and such a reader subtracts
+// from the word what it formed: whichever of the two comes first, both leave zero.  The head is
+// zero again after every call, and a stale T is never taken for a new one.
 #include "qlora_device.h"
 #include "qlora_host.h"
 
@@ -61,6 +66,7 @@ struct RowsArgs {
   uint32_t* words;  // [workgroups][M][r] (tag | bf16(s T)), zero between calls
   int32_t M, r;
   float s;
+  int32_t polls;
 };
 
 // LDS.  The byte-pair table comes first, at address 0, so a lookup address is the v_perm
@@ -136,6 +142,50 @@ __device__ __forceinline__ bf16x8_t lookup8(const uint32_t* pair, uint32_t u, ui
   return as_bf16x8(w);
 }
 
+// The word of a value of s T: all NaN are one, so that two ways to form it agree.
+__device__ __forceinline__ uint32_t posted_word(float t) {
+  return kTag | (t == t ? pack_bf16x2(t, 0.f) & 0xFFFFu : 0x7FC0u);
+}
+
+// Sum of the products of 8 BF16 values with 8 others.
+__device__ __forceinline__ float dot8(uint4 x, uint4 y) {
+  const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+  float d = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    d = fmaf(bf16lo_to_f32(xw[e]), bf16lo_to_f32(yw[e]), d);
+    d = fmaf(bf16hi_to_f32(xw[e]), bf16hi_to_f32(yw[e]), d);
+  }
+  return d;
+}
+
+// The words of ranks q0 .. q0 + 31 that did not arrive (bit i of a lane's `missing`: word i of its
+// eight ranks, of token lane % 16), formed by this wavefront and taken out of the memory that
+// they would have come to.
+template <int NBW>
+__device__ __forceinline__ void form_missing(const RowsArgs& a, uint32_t* mine, int q0, uint32_t missing, int lane,
+                                             uint32_t (&tw)[8]) {
+  const rsrc_t rx = make_rsrc(a.X, a.M * a.K * 2);
+  for (int m = 0; m < a.M; ++m)
+    for (int q = 0; q < 32; ++q) {
+      const int from = 16 * (q >> 3) + m;  // the lane that reads rank q0 + q of token m
+      if (!(((uint32_t)__builtin_amdgcn_readlane((int)missing, from) >> (q & 7)) & 1u)) continue;
+      const rsrc_t ra = make_rsrc(a.A + (int64_t)(q0 + q) * a.K, a.K * 2);
+      float t = 0.f;
+      for (int w = 0; w < kWaves; ++w) {
+        const uint32_t k = (uint32_t)(w * NBW * 64 + 8 * lane);
+        const uint32_t ox = lane < 8 * NBW ? (uint32_t)((m * a.K + k) * 2) : kOOB, oa = lane < 8 * NBW ? 2 * k : kOOB;
+        const float d = wave_sum(dot8(bload16(rx, ox), bload16(ra, oa)));
+        t = w ? t + d : d;
+      }
+      const uint32_t word = posted_word(a.s * t);
+      if (lane != from) continue;
+      __hip_atomic_fetch_add(mine + m * a.r + q0 + q, 0u - word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) tw[i] = i == (q & 7) ? word : tw[i];
+    }
+}
+
 // The operands the loads need come first, as scalars: the leading argument dwords (14 here)
 // are preloaded into SGPRs (a by-value struct would not be), so the loads issue without
 // waiting for the argument block.  mu (loaded after the codes) and the rest follow.
@@ -145,6 +195,7 @@ struct RowsRest {
   uint16_t* T_save;
   uint32_t* words;
   float s;
+  int32_t polls;
 };
 
 template <int NBW>  // blocks of 64 weights per wavefront: K = 64 * 8 * NBW
@@ -168,6 +219,7 @@ __global__ __launch_bounds__(kThreads) void k_gemv_rows(const uint16_t* X, const
   a.M = M32;
   a.r = r32;
   a.s = rest.s;
+  a.polls = rest.polls;
   __shared__ RowsLds<NBW> S;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -215,16 +267,9 @@ __global__ __launch_bounds__(kThreads) void k_gemv_rows(const uint16_t* X, const
   for (int m = 0; m < kMaxM; ++m)
     if (m < M && lane < 8 * NBW) S.x[wave][m][lane] = nibble_order(xv[m]);
   {
-    const uint32_t av[4] = {xv[kMaxM].x, xv[kMaxM].y, xv[kMaxM].z, xv[kMaxM].w};
 #pragma unroll
     for (int m = 0; m < kMaxM; ++m) {
-      const uint32_t xw[4] = {xv[m].x, xv[m].y, xv[m].z, xv[m].w};
-      float d = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        d = fmaf(bf16lo_to_f32(xw[e]), bf16lo_to_f32(av[e]), d);
-        d = fmaf(bf16hi_to_f32(xw[e]), bf16hi_to_f32(av[e]), d);
-      }
+      const float d = dot8(xv[m], xv[kMaxM]);
       if (m < M) {  // uniform: every lane takes part in the sum
         const float t = wave_sum(d);
         if (lane == 0) S.tp[wave][m] = t;
@@ -252,8 +297,7 @@ __global__ __launch_bounds__(kThreads) void k_gemv_rows(const uint16_t* X, const
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) t += S.tp[w][m];
       if (i < M && a.T_save) a.T_save[m * r + c] = (uint16_t)(pack_bf16x2(t, 0.f) & 0xFFFFu);
-      const uint32_t w = kTag | (pack_bf16x2(a.s * t, 0.f) & 0xFFFFu);
-      __hip_atomic_store(a.words + (int64_t)i * r + c, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+      __hip_atomic_fetch_add(a.words + (int64_t)i * r + c, posted_word(a.s * t), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
     }
   }
 
@@ -288,8 +332,10 @@ __global__ __launch_bounds__(kThreads) void k_gemv_rows(const uint16_t* X, const
   if (wave == 0) {
     const bool live0 = l16 < M && 8 * g < r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      tw[i] = live0 ? __hip_atomic_load(mine + l16 * r + 8 * g + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM) : kTag;
+    for (int i = 0; i < 8; ++i) {
+      tw[i] = live0 ? 0u : kTag;
+      if (live0 && a.polls) tw[i] = __hip_atomic_load(mine + l16 * r + 8 * g + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       e[i] = __builtin_amdgcn_raw_buffer_load_b16(rb, 8 * g < r ? (int)((n * r + 8 * g + i) * 2) : (int)kOOB, 0, 0);
@@ -303,6 +349,7 @@ __global__ __launch_bounds__(kThreads) void k_gemv_rows(const uint16_t* X, const
     const f32x4_t v = S.red[w][lane];
     y[0] += v[0]; y[1] += v[1]; y[2] += v[2]; y[3] += v[3];
   }
+  uint32_t formed = 0;  // of step q0 in bits q0 / 4 ..: words that this workgroup formed itself
   for (int q0 = 0; q0 < r; q0 += 32) {
     // A operand: bf16(s T[m][q0 + 8 g .. +7]) from this workgroup's words; B operand: B[n][same]
     const int j0 = q0 + 8 * g;
@@ -313,9 +360,12 @@ __global__ __launch_bounds__(kThreads) void k_gemv_rows(const uint16_t* X, const
         e[i] = __builtin_amdgcn_raw_buffer_load_b16(rb, j0 < r ? (int)((n * r + j0 + i) * 2) : (int)kOOB, 0, 0);
     }
     bool ready = false;
-    // bounded wait (about 2^20 polls): should the words never arrive, the outputs become NaN
-    // instead of the wavefront spinning forever.  The first step's first read was issued above.
-    for (int it = 0; !ready && it < (1 << 20); ++it) {
+    if (q0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) tw[i] = live ? 0u : kTag;
+    }
+    // (the first step's first read was issued above)
+    for (int it = 0; !ready && it < a.polls; ++it) {
       if (it || q0) {
         if (it) __builtin_amdgcn_s_sleep(2);
 #pragma unroll
@@ -326,9 +376,12 @@ __global__ __launch_bounds__(kThreads) void k_gemv_rows(const uint16_t* X, const
 #pragma unroll
       for (int i = 0; i < 8; ++i) ready = ready && (tw[i] & 0xFFFF0000u) == kTag;
     }
-    if (!ready) {
+    uint32_t missing = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) tw[i] = kTag | 0x7FC0u;
+    for (int i = 0; i < 8; ++i) missing |= (tw[i] & 0xFFFF0000u) == kTag ? 0u : 1u << i;
+    if (__ballot(missing != 0)) {
+      formed |= missing << (q0 / 4);
+      form_missing<NBW>(a, mine, q0, missing, lane, tw);
     }
     uint32_t tv[4];
 #pragma unroll
@@ -348,7 +401,9 @@ __global__ __launch_bounds__(kThreads) void k_gemv_rows(const uint16_t* X, const
     const int j0 = q0 + 8 * g;
     if (l16 < M && j0 < r) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) __hip_atomic_store(mine + l16 * r + j0 + i, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+      for (int i = 0; i < 8; ++i)
+        if (!((formed >> (q0 / 4 + i)) & 1u))
+          __hip_atomic_store(mine + l16 * r + j0 + i, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
     }
   }
 }
@@ -388,7 +443,7 @@ hipError_t launch_gemv_rows(const uint32_t* codes, const uint8_t* code8, const f
     L.hi[w] = T.lut_hi[w];
   }
   const dim3 grid((unsigned)(N / kRows));
-  const RowsRest rest{a.B, a.Y, a.T_save, a.words, a.s};
+  const RowsRest rest{a.B, a.Y, a.T_save, a.words, a.s, posted_polls()};
   LaunchTimer t(3, st);
   if (K == 4096)
     hipExtLaunchKernelGGL(k_gemv_rows<8>, grid, dim3(kThreads), 0, st, t.start, t.stop, 0, a.X, a.A, a.code8, a.c2s,

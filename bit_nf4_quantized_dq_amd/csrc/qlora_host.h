@@ -47,6 +47,10 @@ size_t fwd_workspace_bytes(int64_t M, int64_t d_out, int64_t d_in, int32_t r, in
 int fwd_enqueue(const qlora_nf4dq_t* Wq, const uint16_t* X, int64_t M, const uint16_t* A, const uint16_t* B,
                 int32_t r, float alpha, uint16_t* Y, uint16_t* T_save, void* ws, hipStream_t stream);
 
+// How often a workgroup looks for a value that another workgroup of its launch posts (about a
+// microsecond each) before it forms the value itself (api.cpp).
+int32_t posted_polls();
+
 // The checks of a weight descriptor and of a shape, and the level tables of its codebook (api.cpp).
 int check_weight(const qlora_nf4dq_t* Wq);
 bool linear_shape_ok(int64_t d_out, int64_t d_in);
