@@ -49,7 +49,6 @@ constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kRows = 16;            // weight rows per workgroup
 constexpr int kMaxM = 4;             // tokens per call on this path
-constexpr uint32_t kTag = 0x10000u;  // marks a written word (tag | bf16 bits)
 constexpr size_t kHeadUse = QLORA_WS_COUNTER_BYTES;
 
 struct RowsArgs {
@@ -142,23 +141,6 @@ __device__ __forceinline__ bf16x8_t lookup8(const uint32_t* pair, uint32_t u, ui
   return as_bf16x8(w);
 }
 
-// The word of a value of s T: all NaN are one, so that two ways to form it agree.
-__device__ __forceinline__ uint32_t posted_word(float t) {
-  return kTag | (t == t ? pack_bf16x2(t, 0.f) & 0xFFFFu : 0x7FC0u);
-}
-
-// Sum of the products of 8 BF16 values with 8 others.
-__device__ __forceinline__ float dot8(uint4 x, uint4 y) {
-  const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-  float d = 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    d = fmaf(bf16lo_to_f32(xw[e]), bf16lo_to_f32(yw[e]), d);
-    d = fmaf(bf16hi_to_f32(xw[e]), bf16hi_to_f32(yw[e]), d);
-  }
-  return d;
-}
-
 // The words of ranks q0 .. q0 + 31 that did not arrive (bit i of a lane's `missing`: word i of its
 // eight ranks, of token lane % 16), formed by this wavefront and taken out of the memory that
 // they would have come to.
@@ -175,10 +157,10 @@ __device__ __forceinline__ void form_missing(const RowsArgs& a, uint32_t* mine, 
       for (int w = 0; w < kWaves; ++w) {
         const uint32_t k = (uint32_t)(w * NBW * 64 + 8 * lane);
         const uint32_t ox = lane < 8 * NBW ? (uint32_t)((m * a.K + k) * 2) : kOOB, oa = lane < 8 * NBW ? 2 * k : kOOB;
-        const float d = wave_sum(dot8(bload16(rx, ox), bload16(ra, oa)));
+        const float d = wave_sum(dot8(bload16(rx, ox), bload16(ra, oa), 0.f));
         t = w ? t + d : d;
       }
-      const uint32_t word = posted_word(a.s * t);
+      const uint32_t word = posted_bf16(a.s * t);
       if (lane != from) continue;
       __hip_atomic_fetch_add(mine + m * a.r + q0 + q, 0u - word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
 #pragma unroll
@@ -269,7 +251,7 @@ __global__ __launch_bounds__(kThreads) void k_gemv_rows(const uint16_t* X, const
   {
 #pragma unroll
     for (int m = 0; m < kMaxM; ++m) {
-      const float d = dot8(xv[m], xv[kMaxM]);
+      const float d = dot8(xv[m], xv[kMaxM], 0.f);
       if (m < M) {  // uniform: every lane takes part in the sum
         const float t = wave_sum(d);
         if (lane == 0) S.tp[wave][m] = t;
@@ -297,7 +279,7 @@ __global__ __launch_bounds__(kThreads) void k_gemv_rows(const uint16_t* X, const
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) t += S.tp[w][m];
       if (i < M && a.T_save) a.T_save[m * r + c] = (uint16_t)(pack_bf16x2(t, 0.f) & 0xFFFFu);
-      __hip_atomic_fetch_add(a.words + (int64_t)i * r + c, posted_word(a.s * t), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+      __hip_atomic_fetch_add(a.words + (int64_t)i * r + c, posted_bf16(a.s * t), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
     }
   }
 

@@ -62,7 +62,6 @@ constexpr int kMaxR = 128;
 constexpr int kRegion = 87 * 1024;       // activations, block constants, scales (then the T sums)
 constexpr int kC8Loads = 24;             // staged block-constant dwords per thread, at most
 constexpr int kSumU = 16;                // partials loaded together in the split-K sum
-constexpr uint32_t kTag = 0x10000u;      // marks a handed-over word (tag | bf16)
 constexpr int kMaxHandP = 8;             // reduction pieces of 4096 per producer lane (K <= 32768)
 
 // Workgroup barrier that waits for this wavefront's LDS accesses only (lgkmcnt), so global
@@ -116,7 +115,8 @@ struct StreamArgs {
   float* tpart;  // [ksplit][M][r]
   unsigned int* counters;  // [row groups of the launch], zero between calls
   uint32_t* words;         // handed-over T: [row groups of the launch][r] (tag | bf16(s T)), zero between calls
-  int32_t nprod;           // workgroups that also form a column of T (the first ones dispatched)
+  int32_t nprod;           // workgroups that also form a column of T (the first ones in dispatch order)
+  int32_t polls;           // how often a word that is not there yet is looked for
   int64_t N, K;
   int32_t M, r;
   float s;
@@ -165,18 +165,38 @@ struct Chunk {
   uint4 av[RT16];    // adapter rows 16 k + (lane & 15), this wavefront's 32-index step
 };
 
+// The dot product of token 0 with a row of A over the whole reduction, as a producer's workgroup sums it.
+__device__ __forceinline__ float whole_dot(const rsrc_t rx, const uint16_t* A_row, int64_t K, int lane) {
+  const rsrc_t ra = make_rsrc(A_row, K * 2);
+  float t = 0.f;
+  for (int w = 0; w < kWaves; ++w) {
+    float d = 0.f;
+    for (int p = 0; p < kMaxHandP; ++p) {
+      const int64_t k = 4096 * p + 8 * (64 * w + lane);
+      const uint32_t off = k < K ? (uint32_t)(k * 2) : kOOB;
+      d = dot8(bload16(rx, off), bload16(ra, off), d);
+    }
+    d = wave_sum(d);
+    t = w ? t + d : d;
+  }
+  return t;
+}
+
 // RT16: 16-wide rank tiles (r <= 16 RT16).  NQ: accumulator registers kept (1 for M = 1,
 // where only row 0 of the 32x32 product is live; 8 for M <= 16).  K is a multiple of 256, so
 // a chunk's four E4M3 bytes form one aligned word and share one second-level scale.
 // HAND (M = 1 only): T is not formed in the loop.  The first count r workgroups in dispatch
 // order each also form one column j of T = x A^T of one linear over the whole reduction
 // (8 products per lane and piece of 4096, a fixed-order DPP sum per wavefront, then the
-// wavefronts in order) while their first chunks land, and write bf16(s T) with a tag into
+// wavefronts in order) while their first chunks land, and post bf16(s T) with a tag to
 // the word block of every row group of that linear in the workspace head.  Row groups take
 // the adapter term in split 0 only: after the loop, each wavefront reads its row group's
-// words (bounded wait), applies them to B on MFMA and adds the result; the words are cleared
-// after the outputs.  Producers wait on nothing before they publish and are dispatched
-// first, so no reader waits on a workgroup that has not started.
+// words, applies them to B on MFMA and adds the result; the words are cleared after the
+// outputs.  No wait depends on a workgroup having started (each XCD starts its own, and
+// launches on several streams share the chip): after `polls` looks a wavefront forms the
+// missing words itself, by the same sums in the same order.  Posts are additions to words
+// that are zero, and words are cleared by subtracting what they hold or will hold, so that they
+// are zero after the call whichever comes first.
 template <int RT16, int NQ, int kDepth, bool MULTI, bool HAND>
 __global__ __launch_bounds__(kThreads) void k_gemv_stream(StreamArgs a, Lut L, typename GroupArg<MULTI>::type G) {
   __shared__ Smem sm;
@@ -379,19 +399,12 @@ __global__ __launch_bounds__(kThreads) void k_gemv_stream(StreamArgs a, Lut L, t
   if (HAND && producer) {  // this wavefront's part of T[0][pj]
     float d = 0.f;
 #pragma unroll
-    for (int p = 0; p < (HAND ? kMaxHandP : 1); ++p) {
-      const uint32_t xw[4] = {hx[p].x, hx[p].y, hx[p].z, hx[p].w}, aw[4] = {ha[p].x, ha[p].y, ha[p].z, ha[p].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        d = fmaf(bf16lo_to_f32(xw[e]), bf16lo_to_f32(aw[e]), d);
-        d = fmaf(bf16hi_to_f32(xw[e]), bf16hi_to_f32(aw[e]), d);
-      }
-    }
+    for (int p = 0; p < (HAND ? kMaxHandP : 1); ++p) d = dot8(hx[p], ha[p], d);
     const float t = wave_sum(d);
     if (lane == 0) sm.tp[wave] = t;
   }
   lds_barrier();
-  if (HAND && producer) {  // publish column pj to every row group of linear pli
+  if (HAND && producer) {  // post column pj to every row group of linear pli
     float t = sm.tp[0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) t += sm.tp[w];
@@ -403,9 +416,9 @@ __global__ __launch_bounds__(kThreads) void k_gemv_stream(StreamArgs a, Lut L, t
       ge = G.gstart[pli + 1];
     }
     if (tid == 0 && pT) pT[pj] = (uint16_t)(pack_bf16x2(t, 0.f) & 0xFFFFu);
-    const uint32_t word = kTag | (pack_bf16x2(a.s * t, 0.f) & 0xFFFFu);
+    const uint32_t word = posted_bf16(a.s * t);
     for (int q = gb + tid; q < ge; q += kThreads)
-      __hip_atomic_store(a.words + (int64_t)q * a.r + pj, word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+      __hip_atomic_fetch_add(a.words + (int64_t)q * a.r + pj, word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
   }
 
   const uint32_t lane4 = (uint32_t)lane * 4u;
@@ -492,6 +505,7 @@ __global__ __launch_bounds__(kThreads) void k_gemv_stream(StreamArgs a, Lut L, t
   // ---- adapter up-projection: rows n of this wavefront, with this range's T, or (HAND) with
   // the handed-over T in split 0 only
   uint32_t* const mine = HAND ? a.words + pgrp * a.r : nullptr;  // this row group's words
+  uint32_t* const taken = reinterpret_cast<uint32_t*>(sT);       // what they hold (HAND: sT is free)
   if (!HAND || ks == 0) {
     f32x16_t up = {};
 #pragma unroll
@@ -500,12 +514,12 @@ __global__ __launch_bounds__(kThreads) void k_gemv_stream(StreamArgs a, Lut L, t
       const int j0 = 16 * u + 8 * h;
       uint32_t tv[4];
       if constexpr (HAND) {
-        // bounded wait (about 2^20 polls): should the words never arrive, the outputs become
-        // NaN instead of the wavefront spinning forever
         const bool live = l32 == 0;  // token row 0 of the A operand
         uint32_t tw[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) tw[i] = (live && j0 + i < a.r) ? 0u : kTag;
         bool ready = false;
-        for (int it = 0; !ready && it < (1 << 20); ++it) {
+        for (int it = 0; !ready && it < a.polls; ++it) {
           if (it) __builtin_amdgcn_s_sleep(2);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -515,9 +529,22 @@ __global__ __launch_bounds__(kThreads) void k_gemv_stream(StreamArgs a, Lut L, t
 #pragma unroll
           for (int i = 0; i < 8; ++i) ready = ready && (tw[i] & 0xFFFF0000u) == kTag;
         }
-        if (!ready) {
+        uint32_t missing = 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) tw[i] = kTag | 0x7FC0u;
+        for (int i = 0; i < 8; ++i) missing |= (tw[i] & 0xFFFF0000u) == kTag ? 0u : 1u << i;
+        if (__ballot(missing != 0)) {
+          for (int q = 0; q < 16; ++q) {  // rank 16 u + q, which lane 0 or 32 reads
+            const int from = 32 * (q >> 3);
+            if (!(((uint32_t)__builtin_amdgcn_readlane((int)missing, from) >> (q & 7)) & 1u)) continue;
+            const uint32_t word = posted_bf16(a.s * whole_dot(rx, l_A + (int64_t)(16 * u + q) * K, K, lane));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tw[i] = (lane == from && i == (q & 7)) ? word : tw[i];
+          }
+        }
+        if (wave == 0 && live) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (j0 + i < a.r) taken[j0 + i] = tw[i];
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) tv[e] = live ? ((tw[2 * e] & 0xFFFFu) | (tw[2 * e + 1] << 16)) : 0u;
@@ -560,7 +587,7 @@ __global__ __launch_bounds__(kThreads) void k_gemv_stream(StreamArgs a, Lut L, t
     if (HAND) {  // every wavefront has read the words: clear them for the next call
       lds_barrier();
       for (int i = tid; i < a.r; i += kThreads)
-        __hip_atomic_store(mine + i, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+        __hip_atomic_fetch_add(mine + i, 0u - taken[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
     }
     return;
   }
@@ -581,7 +608,7 @@ __global__ __launch_bounds__(kThreads) void k_gemv_stream(StreamArgs a, Lut L, t
   __syncthreads();
   if (HAND && ks == 0) {  // every wavefront has read the words: clear them for the next call
     for (int i = tid; i < a.r; i += kThreads)
-      __hip_atomic_store(mine + i, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+      __hip_atomic_fetch_add(mine + i, 0u - taken[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
   }
   if (tid == 0) {
     const unsigned int old = __hip_atomic_fetch_add(&a.counters[pgrp], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -730,6 +757,7 @@ hipError_t stream_launch(int count, const StreamLinear* lins, int64_t K, const u
                     (size_t)(woff + p.groups * r) * 4 <= QLORA_WS_COUNTER_BYTES;
   a.words = hand ? reinterpret_cast<uint32_t*>(counters + woff) : nullptr;
   a.nprod = hand ? count * r : 0;
+  a.polls = posted_polls();
   a.N = Nt;
   a.K = K;
   a.M = (int32_t)M;

@@ -273,4 +273,22 @@ __device__ __forceinline__ float wave_sum(float v) {
   return ((r0 + r1) + r2) + r3;
 }
 
+// d + the products of 8 BF16 values with 8 others.
+__device__ __forceinline__ float dot8(uint4 x, uint4 y, float d) {
+  const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    d = fmaf(bf16lo_to_f32(xw[e]), bf16lo_to_f32(yw[e]), d);
+    d = fmaf(bf16hi_to_f32(xw[e]), bf16hi_to_f32(yw[e]), d);
+  }
+  return d;
+}
+
+// A value of s T in BF16 as it is posted to another workgroup's word, with a bit that marks it as there.
+// All NaN are one, so that two ways to form the value agree.
+constexpr uint32_t kTag = 0x10000u;
+__device__ __forceinline__ uint32_t posted_bf16(float t) {
+  return kTag | (t == t ? pack_bf16x2(t, 0.f) & 0xFFFFu : 0x7FC0u);
+}
+
 }  // namespace qlora

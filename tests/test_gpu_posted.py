@@ -10,6 +10,8 @@ HEAD = 512 * 1024
 # d_out, d_in, rows, rank: whole rows to a workgroup
 ROWS = [(4096, 2048, 3, 8), (6144, 4096, 2, 64), (4096, 4096, 1, 40), (5120, 4096, 4, 24), (4096, 4096, 4, 16), (4096, 2048, 4, 128),
         (4096, 4096, 1, 16)]
+# one token of a large weight: its reduction split or not, a partial row group, ranks of any kind, the longest reduction
+STREAM = [(8192, 4096, 1, 16), (8192 + 160, 4096, 1, 40), (14336, 4096, 1, 5), (4096, 14336, 1, 64), (1024, 32768, 1, 24), (57344, 1024, 1, 128)]
 
 
 @pytest.fixture
@@ -59,7 +61,7 @@ def check_close(c, got):
         assert float((g.double() - ref).norm() / ref.norm()) <= 1e-2
 
 
-@pytest.mark.parametrize("shape", ROWS)
+@pytest.mark.parametrize("shape", ROWS + STREAM)
 def test_same_bits_whoever_forms_an_element(looks, shape):
     print(shape, flush=True)
     c = make(*shape)
@@ -74,7 +76,7 @@ def test_same_bits_whoever_forms_an_element(looks, shape):
         assert same(got, want) and not ws[:HEAD].any(), n
 
 
-@pytest.mark.parametrize("shape", [(4096, 4096, 2, 16)])
+@pytest.mark.parametrize("shape", [(4096, 4096, 2, 16), (8192, 4096, 1, 16)])
 def test_values_that_are_not_finite(looks, shape):
     c = make(*shape)
     ws = workspace(c)
@@ -89,7 +91,7 @@ def test_values_that_are_not_finite(looks, shape):
             assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
 
 
-@pytest.mark.parametrize("shape", [(4096, 4096, 1, 16)])
+@pytest.mark.parametrize("shape", [(4096, 4096, 1, 16), (14336, 4096, 1, 40)])
 def test_on_streams_at_once_and_replayed(looks, shape):
     cases = [make(*shape, seed=i) for i in range(4)]
     work = [workspace(c) for c in cases]
@@ -120,3 +122,27 @@ def test_on_streams_at_once_and_replayed(looks, shape):
         eager = call(c, ws)
         torch.cuda.synchronize()
         assert all(same(o, eager) for o in out) and not ws[:HEAD].any()
+
+
+@pytest.mark.parametrize("rank", [16, 40])
+def test_linears_of_one_launch(looks, rank):
+    """Several weights over the same activations: each linear's row groups take its own columns of T."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    shapes = [(8192, 4096), (1024, 4096), (1024, 4096)]
+    cases = [make(n, k, 1, rank, seed=i) for i, (n, k) in enumerate(shapes)]
+    qs, As, Bs, X = [c[0] for c in cases], [c[2] for c in cases], [c[3] for c in cases], cases[0][1]
+    ws = Q.new_workspace(Q.workspace_size_multi(qs, 1, rank), "cuda")
+
+    def run():
+        Ts = [torch.empty(1, rank, dtype=torch.bfloat16, device="cuda") for _ in qs]
+        return [*Q.linear_fwd_multi(qs, X, As, Bs, 24.0, T_saves=Ts, ws=ws), *Ts]
+
+    want = run()
+    for c, y, t in zip(cases, want[:3], want[3:]):
+        check_close((c[0], X, c[2], c[3]), (y, t))
+    for n in (0, 1, 0, 512):
+        looks(n)
+        got = run()
+        torch.cuda.synchronize()
+        assert same(got, want) and not ws[:HEAD].any(), n
