@@ -500,10 +500,12 @@ __device__ __forceinline__ void form_missing(const StreamArgs& a, uint64_t* word
   RngKey key{};
   if (a.drop.threshold) key = load_rng(a.drop.rng);
   const uint16_t* A = a.rows.table[adapter_of(a.rows, k)].A;
+#pragma unroll 1
   for (int q = 0; q < 32; ++q) {
     const int from = 16 * (q >> 3) + k;  // the lane that reads rank r0 + q
     if (!(((uint32_t)__builtin_amdgcn_readlane((int)missing, from) >> (q & 7)) & 1u)) continue;
     float sum = 0.f;
+#pragma unroll 1
     for (int w = 0; w < W; ++w) {
       const float d = dot_share<W>(a, key, t2, (uint32_t)k, A + (int64_t)(r0 + q) * a.K, 64 * w + lane);
       sum = w ? sum + d : d;
@@ -793,9 +795,11 @@ __global__ __launch_bounds__(64 * W, !POST && RT == 1 && MT <= 3 ? 4 : 2) void k
           }
         }
         uint32_t missing = 0;
+        if (__builtin_expect(__ballot(!ready) != 0, 0)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) missing |= (t[i] & kPosted) ? 0u : 1u << i;
-        if (__ballot(missing != 0)) form_missing<W>(a, mine_t + k * width, k, r0, missing, lane, t);
+          for (int i = 0; i < 8; ++i) missing |= (t[i] & kPosted) ? 0u : 1u << i;
+          form_missing<W>(a, mine_t + k * width, k, r0, missing, lane, t);
+        }
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -1142,11 +1146,11 @@ bool adapter_stream_fits(int64_t M, int64_t N, int64_t K) { return M <= 64 || (M
 
 // Where the stream's workgroups form T and post it: one tile of rows, few enough elements that no
 // workgroup forms more than two and that the posted words (elements times workgroups) cost less
-// than the launch that they save (replayed, here and in two launches: 4096 x 4096: one row of 64 ranks
-// 10.9 us and 12.6, 8 rows of 16 11.7 and 12.8; 14336 x 4096: one row of 16 20.2 and 23.0; 4096 x
-// 14336: 19 and 27.  At the rule's edge nothing is left of it: 4096 x 4096, one row of 128 ranks 13.8
-// and 13.1, 16 rows of 8 14.0 and 13.1.  Past it: 14336 x 4096, 8 rows of 8 ranks, 57000 words, 33 and
-// 24; 64 x 64, four elements each, 8.6 and 7.0).
+// than the launch that they save (replayed, here and in two launches: 4096 x 4096: one row of 16 ranks
+// 9.3 us and 12.4, of 64 10.7 and 12.6, 8 rows of 16 11.3 and 12.9; 14336 x 4096: one row of 16 19.9 and
+// 22.7; 4096 x 14336: 18.4 and 26.9.  At the rule's edges little is left of it: 4096 x 4096, one row of
+// 128 ranks 13.6 and 13.3, 16 rows of 8 13.6 and 13.3; 64 x 64 7.4 and 7.1.  Past them: 14336 x 4096,
+// 8 rows of 8 ranks, 57000 words, 33 and 24; 64 x 64, four elements each, 8.6 and 7.0).
 bool stream_forms_t(int64_t M, int64_t N, int32_t width) {
   const int64_t slots = M * width, groups = N / kStreamRows;
   static_assert(kPostedWords * sizeof(uint64_t) <= QLORA_WS_COUNTER_BYTES, "in the workspace's head");
