@@ -88,7 +88,12 @@ def _grads_apart(A, B, dA, dB) -> None:
 class AdapterSet:
     """The adapters of one linear [d_out, d_in], laid out once: a device table that
     linear_adapters_fwd and _bwd go by.  It holds the tensors (their values may change, their memory
-    stays theirs); the table is written on the stream that is current when the set is made.
+    stays theirs).
+
+    Streams.  The table is written on the stream that is current when the set is made, and its memory
+    belongs to that stream, as any tensor's.  Calls on another stream first wait for that one (an
+    event, or wait_stream); and the set is kept until such calls have run, and for as long as a
+    captured graph that goes by it is replayed.
 
     A[i] [r_i, d_in], B[i] [d_out, r_i]: contiguous BF16 CUDA tensors, ranks 1..128 that may differ.
     alpha: one number, or one per adapter (the branch is scaled by alpha / r).  dA, dB: tensors of

@@ -1141,7 +1141,8 @@ hipError_t launch_shrink_both(const AdapterRows& rows, const uint16_t* X, int64_
 
 // Up to 64 rows, and up to 128 of a smaller weight: the stream's workgroups read all of X in each, which
 // a product over tiles of 128 x 128 does not (128 rows: 4096 x 4096 23 us here and 28 by tiles, 14336 x
-// 4096 64 and 41, 4096 x 14336 60 and 42; 64 rows: 14336 x 4096 33 and 36, 4096 x 14336 41 and 37).
+// 4096 64 and 41, 4096 x 14336 60 and 42; 64 rows: 14336 x 4096 33 and 36, 4096 x 14336 41 and 37, where
+// the rule, which does not go by the reduction's length, loses).
 bool adapter_stream_fits(int64_t M, int64_t N, int64_t K) { return M <= 64 || (M <= kStreamMaxRows && N * K < (int64_t(1) << 25)); }
 
 // Where the stream's workgroups form T and post it: one tile of rows, few enough elements that no
@@ -1164,7 +1165,7 @@ hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, co
   const int tiles = (int)((rows.M + kRowTile - 1) / kRowTile), ranks = (rows.width + 15) / 16;
   const StreamArgs a{reinterpret_cast<const uint8_t*>(codes), code8, c2s, mu, N, K, X, rows, drop, T, Y,
                      std::min((int)rows.count, kRowTile), static_cast<uint64_t*>(head), polls};
-  const bool wide = N / kStreamRows > 512;  // more than fit at once
+  const bool wide = N / kStreamRows > 512;  // more single tiles than workgroups of eight wavefronts fit at once
   if (stream_forms_t(rows.M, N, rows.width))
     return wide ? stream_go<4, 1, 1, true, 4>(a, tab, st) : stream_go<8, 1, 1, true, 4>(a, tab, st);
   const dim3 grid_t((unsigned)(tiles * ranks * a.lists));
@@ -1174,7 +1175,8 @@ hipError_t launch_adapter_stream(const uint32_t* codes, const uint8_t* code8, co
   if (e != hipSuccess) return e;
   if (rows.M <= 16) return wide ? stream_go<4, 1, 1, false, 4>(a, tab, st) : stream_go<8, 1, 1, false, 4>(a, tab, st);
   if (rows.M > 96) return wide ? stream_go<4, 1, 8, false, 1>(a, tab, st) : stream_go<8, 1, 8, false, 1>(a, tab, st);
-  // two weight tiles to a workgroup where that leaves one for each compute unit (and registers last)
+  // two weight tiles to a workgroup where that leaves one for each compute unit (and registers last), by
+  // four wavefronts, and by eight at the narrowest of these weights, whose 256 workgroups are one each
   if (N < 8192) return stream_as<8, 1>(a, tab, st);
   return wide ? stream_as<4, 2>(a, tab, st) : stream_as<8, 2>(a, tab, st);
 }

@@ -52,6 +52,7 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_barrier" ::: "memory");
 }
 
+// (sized for TJ = 2; a workgroup has a compute unit to itself with TJ = 1 too)
 __shared__ uint4 s_w0[1024], s_w1[1024];              // decoded weights, 16 KB each
 __shared__ uint4 s_x0[2048], s_x1[2048], s_x2[2048];  // activations, 32 KB each
 template <int I> __device__ __forceinline__ uint4* wbuf() { return I == 0 ? s_w0 : s_w1; }

@@ -36,8 +36,10 @@ extern "C" {
 #define QLORA_MAX_ADAPTERS 4096
 
 /* The adapters of one linear [d_out, d_in], laid out once for the calls that follow: a table in
- * the caller's device memory.  The tensors' values may change between calls; their addresses
- * and ranks may not.  The struct is plain data of the caller's. */
+ * the caller's device memory, written on the stream that qlora_adapters_init is given: calls on
+ * another stream wait for that first, and the table stays until the last call, or replay of a
+ * captured one, has run.  The tensors' values may change between calls; their addresses and
+ * ranks may not.  The struct is plain data of the caller's. */
 typedef struct qlora_adapters {
   void *table;
   int64_t d_out, d_in;

@@ -76,3 +76,35 @@ def test_long_reductions(gpu_lib, M, N, K, ranks, p):
     dA, dB = [t.clone() for t in s.dA], [t.clone() for t in s.dB]
     assert torch.equal(dX, Q.linear_adapters_bwd(q, s, X, dY, ids, **kw))
     assert all(map(torch.equal, dA + dB, s.dA + s.dB))
+
+
+def test_as_many_adapters_as_a_set_holds(gpu_lib):
+    """4096 adapters of two ranks, rows that name some of them in no order, and gradients of them all."""
+    import bit_nf4_quantized_dq_amd as Q
+
+    M, N, K, n = 700, 64, 128, 4096
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    randn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    q = Q.quantize(randn(N, K))
+    ranks = [8 if i % 3 else 70 for i in range(n)]
+    A, B = [randn(r, K).bfloat16() for r in ranks], [randn(N, r).bfloat16() for r in ranks]
+    s = Q.AdapterSet(A, B, 8.0, dA=[torch.full_like(t, 3.0) for t in A], dB=[torch.full_like(t, 3.0) for t in B])
+    X, dY = randn(M, K).bfloat16(), randn(M, N).bfloat16()
+    for rows in (1, 40, M):
+        ids = torch.randint(-1, n, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+        ids[0] = n - 1
+        Y = Q.linear_adapters_fwd(q, s, X[:rows], ids)
+        dX = Q.linear_adapters_bwd(q, s, X[:rows], dY[:rows], ids)
+        named = sorted(set(ids.tolist()) - {-1})
+        at = {a: i for i, a in enumerate(named)}
+        few = torch.tensor([at.get(a, -1) for a in ids.tolist()], device="cuda")
+        args = (Q.dequantize(q), [A[a] for a in named], [B[a] for a in named], [8.0] * len(named), X[:rows])
+        f, b = AO.fwd(*args, few), AO.bwd(*args, dY[:rows], few)
+        r = s.t_width
+        near(Y, f["Y"], HALF * f["Y"].abs() + ADD * (K + 8) * f["Y_base"] + (ADD * (K + r + 16) + SPLIT) * f["Y_branch"], "Y")
+        near(dX, b["dX"], HALF * b["dX"].abs() + ADD * (N + 8) * b["dX_base"] + (ADD * (N + r + 16) + SPLIT) * b["dX_branch"], "dX")
+        for i, a in enumerate(named):
+            near(s.dA[a], b["dA"][i], HALF * b["dA"][i].abs() + (ADD * (N + rows + 16) + SPLIT) * b["dA_sum"][i], f"dA[{a}]")
+            near(s.dB[a], b["dB"][i], HALF * b["dB"][i].abs() + (ADD * (K + rows + 16) + SPLIT) * b["dB_sum"][i], f"dB[{a}]")
+        none = sorted(set(range(n)) - set(named))
+        assert not torch.cat([t.view(-1) for a in none for t in (s.dA[a], s.dB[a])]).any()
