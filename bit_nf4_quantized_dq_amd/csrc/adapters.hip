@@ -863,8 +863,8 @@ struct GradsArgs {
 // shared like rows that lie apart (555 rows of 6 adapters in runs 19.4 us when each wavefront kept to
 // 256 rows, so 11): U [32 rows][ranks] as hi and lo BF16 parts and V [32 rows][64
 // columns], both transposed through LDS.  Bound by HBM at low ranks (8192 rows of 4 adapters of rank 16
-// at 14336 x 4096 81 us for 303 MB), by U at high ones, which every tile of columns reads anew (4096
-// rows of rank 64 at 4096 x 4096 38 us: 134 MB of U through the L2 beside 67 MB of V).
+// at 14336 x 4096 84 us for 303 MB), by U at high ones, which every tile of columns reads anew (4096
+// rows of rank 64 at 4096 x 4096 40 us: 134 MB of U through the L2 beside 67 MB of V).
 template <int JT>
 struct GradsLds {
   static constexpr int kWaveBytes = (4 + 2 * JT) * kVTile;
