@@ -24,13 +24,13 @@ def sparse(gen, M, n):
     return x.scatter_(1, at, torch.randn(M, FEW, generator=gen, device="cuda").bfloat16())
 
 
-def near(got, ref, tol, name):
+def near(got, ref, tol, name, share=0.05):
     got = got.double()
     bad = ~((got - ref).abs() <= tol)
     assert not bad.any(), (name, int(bad.sum()), bad.nonzero()[0].tolist(), float(got[bad][0]), float(ref[bad][0]), float(tol[bad][0]))
     # a twentieth of the values: a lost term or a wrong column cannot pass
     some = ref[ref != 0].abs()
-    assert len(some) and float(tol[ref != 0].median()) < 0.05 * float(some.median()), name
+    assert len(some) and float(tol[ref != 0].median()) < share * float(some.median()), name
 
 
 # rows, d_out, d_in, ranks, dropout: long reductions of T and Y, then of dX and G
@@ -108,3 +108,69 @@ def test_as_many_adapters_as_a_set_holds(gpu_lib):
             near(s.dB[a], b["dB"][i], HALF * b["dB"][i].abs() + (ADD * (K + rows + 16) + SPLIT) * b["dB_sum"][i], f"dB[{a}]")
         none = sorted(set(range(n)) - set(named))
         assert not torch.cat([t.view(-1) for a in none for t in (s.dA[a], s.dB[a])]).any()
+
+
+def kept_rows(rows, K, p):
+    """[len(rows), K] bool: which elements of those rows of X stay (element m K + k has half e % 8 of block e // 8)."""
+    import numpy as np
+
+    block = (np.asarray(rows, dtype=np.uint64)[:, None] * np.uint64(K // 8) + np.arange(K // 8, dtype=np.uint64)).reshape(-1)
+    low = np.uint64(0xFFFFFFFF)
+    seed, offset = RNG
+    ctr = np.stack([block & low, block >> np.uint64(32), np.full_like(block, offset & 0xFFFFFFFF), np.full_like(block, offset >> 32)], 1)
+    w = AO.philox(ctr, (seed & 0xFFFFFFFF, seed >> 32))
+    return torch.from_numpy((np.stack([w & 0xFFFF, w >> 16], 2).reshape(len(rows), K) >= AO.threshold(p))).cuda()
+
+
+@pytest.mark.parametrize("N,K", [(64, 8192), (8192, 64)])
+def test_more_than_4_gib_of_rows(gpu_lib, N, K):
+    """X, or dY, past 2^32 bytes, with dropout: rows at the start, at the 4 GiB mark and at the end.  (Dense
+    rows: the bounds reach a twelfth of the values, and what is asked is whether the right rows are read.)"""
+    import bit_nf4_quantized_dq_amd as Q
+
+    print(N, K, flush=True)
+    M, p, ranks = 2**18 + 4099, 0.1, [16, 5, 24]
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    randn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    q = Q.quantize(randn(N, K))
+    A, B = [(randn(r, K) / 8).bfloat16() for r in ranks], [(randn(N, r) / 8).bfloat16() for r in ranks]
+    s = Q.AdapterSet(A, B, [float(r) for r in ranks], dA=[torch.empty_like(t) for t in A], dB=[torch.empty_like(t) for t in B])
+    X, dY = [torch.empty(M, n, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for n in (K, N)]
+    ids = torch.randint(-1, 3, (M,), generator=gen, device="cuda", dtype=torch.int32)
+    rows = torch.tensor([*range(20), *range(2**18 - 10, 2**18 + 10), *range(M - 20, M)], device="cuda")
+    kw = dict(dropout=p, rng=torch.tensor(RNG, device="cuda"))
+    T = torch.empty(M, s.t_width, device="cuda")
+    Y = Q.linear_adapters_fwd(q, s, X, ids, T_save=T, **kw)
+    what, keep = Q.dequantize(q).double(), kept_rows(rows.tolist(), K, p)
+    gate = keep.double() * AO.scale(p)
+    x, dy, own = X[rows].double(), dY[rows].double(), ids[rows]
+    # each row's own adapter, zeros for none
+    wide = lambda ts, dim: torch.stack([torch.nn.functional.pad(t.double(), (0, 0, 0, 24 - t.shape[0]) if dim == 0 else (0, 24 - t.shape[1])) for t in ts])  # noqa: E731
+    has = (own >= 0).double()
+    Ar, Br = wide(A, 0)[own.clamp(min=0).long()] * has[:, None, None], wide(B, 1)[own.clamp(min=0).long()] * has[:, None, None]
+    dot = lambda a, b: (a * b).sum(-1)  # noqa: E731
+    xd = x * gate
+    t, tm = dot(Ar, xd[:, None]), dot(Ar.abs(), xd.abs()[:, None])
+    near(T[rows], t, 2.0**-23 * t.abs() + ADD * (K + 8) * tm, "T", 0.25)
+    y, base = x @ what.T + dot(Br, t[:, None]), x.abs() @ what.abs().T
+    near(Y[rows], y, HALF * y.abs() + ADD * (K + 8) * base + (ADD * (K + 40) + SPLIT) * dot(Br.abs(), tm[:, None]), "Y", 0.25)
+    del Y
+    dX = Q.linear_adapters_bwd(q, s, X, dY, ids, T_saved=T, **kw)
+    g, gm = (dy[:, :, None] * Br).sum(1), (dy.abs()[:, :, None] * Br.abs()).sum(1)
+    back, backm = (g[:, :, None] * Ar).sum(1) * gate, (gm[:, :, None] * Ar.abs()).sum(1) * gate
+    ref = dy @ what + back
+    near(dX[rows], ref, HALF * ref.abs() + ADD * (N + 8) * (dy.abs() @ what.abs()) + (ADD * (N + 40) + SPLIT) * backm, "dX", 0.25)
+    del dX
+    # the gradients of those rows alone, few values each, by the T that was checked
+    dy = sparse(gen, len(rows), N)
+    dY.zero_()[rows] = dy
+    assert Q.linear_adapters_bwd(q, s, X, dY, ids, T_saved=T, need_dx=False, **kw) is None
+    dy, t = dy.double(), T[rows].double()
+    g, gm = (dy[:, :, None] * Br).sum(1), (dy.abs()[:, :, None] * Br.abs()).sum(1)
+    for i, r in enumerate(ranks):
+        at = own == i
+        assert at.any()
+        dA, dAm = g[at, :r].T @ xd[at], gm[at, :r].T @ xd[at].abs()
+        near(s.dA[i], dA, HALF * dA.abs() + (ADD * (FEW + 80) + SPLIT) * dAm, f"dA[{i}]")
+        dB, dBm = dy[at].T @ t[at, :r], dy[at].abs().T @ t[at, :r].abs()
+        near(s.dB[i], dB, HALF * dB.abs() + (ADD * 80 + SPLIT) * dBm, f"dB[{i}]")
